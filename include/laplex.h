@@ -247,6 +247,130 @@ laplex_status laplex_plan_set_option(laplex_plan plan, int option, int64_t value
  */
 laplex_status laplex_plan_set_temperature(laplex_plan plan, double t);
 
+/*
+ * ---- Tokens: routing by expert and the gated recurrence ----
+ *
+ * The operator's two halves as a sequence layer uses them: the stable sort
+ * with integer keys (the zero-temperature limit of summary §2.3, routing by
+ * equality) and the causal scan of summary §2.2 with a decay given for each
+ * token.  A layer whose tokens go to several memories routes them (the
+ * offsets of the sort are the sequence offsets of the recurrence), moves the
+ * rows, runs the recurrence and brings the rows back with the router's
+ * weights.
+ *
+ * These calls allocate nothing and wait for nothing: scratch comes from the
+ * caller, and all work is ordered on `stream`, so they can be recorded into
+ * a HIP graph.  Arrays of rows have unit stride along the row and `ld`
+ * values between rows; values are of a laplex_dtype.  Arithmetic, weights
+ * and states are float32; a result is rounded once when it is stored.
+ * Contents of index arrays are not checked on the host: an index outside
+ * its range names no row (it is skipped, never followed).
+ */
+typedef enum { LAPLEX_F32 = 0, LAPLEX_BF16 = 1, LAPLEX_F16 = 2 } laplex_dtype;
+
+/*
+ * laplex_route -- places of token slots in a stable sort by expert.
+ *
+ *   experts  device, int32 (wide = 0) or int64 (wide = 1) [tokens][slots],
+ *            the expert of each slot; a value outside [0, n_experts) drops
+ *            the slot.  1 <= slots, tokens * slots <= 2^30,
+ *            1 <= n_experts <= 4096.
+ *   order    device, int32[tokens * slots]: the slot t * slots + k of each
+ *            row by expert, ascending within an expert; -1 past the last.
+ *   place    device, int32[tokens][slots]: the row of each slot, -1 if dropped.
+ *   offsets  device, int32[n_experts + 1]: first row of each expert, and the
+ *            number of rows.
+ *   ws       device scratch of laplex_route_workspace(...) bytes (16-byte
+ *            aligned; may be NULL when that is 0).
+ * laplex_route_workspace returns -1 for sizes out of range.
+ */
+int64_t laplex_route_workspace(int64_t tokens, int64_t slots, int64_t n_experts);
+laplex_status laplex_route(const void* experts, int wide, int64_t tokens, int64_t slots, int64_t n_experts,
+                           int32_t* order, int32_t* place, int32_t* offsets, void* ws, int64_t ws_bytes,
+                           void* stream);
+
+/*
+ * laplex_dispatch -- xs[place[t][k]] = x[t]: token rows to their places by
+ * expert.  x [tokens][width], xs [tokens * slots][width]; rows of xs past
+ * the last kept slot are set to 0.  Its gradient is laplex_combine of the
+ * rows' gradients without weights.
+ *
+ * laplex_combine -- y[t] = sum over k of weights[t][k] * ys[place[t][k]]:
+ * expert rows back to their tokens.  weights float32 [tokens][slots], or
+ * NULL for all ones; a dropped slot adds nothing (its weight and any row are
+ * not used), a token without kept slots gets 0.
+ *
+ * laplex_combine_backward -- gradients of laplex_combine: dys[place[t][k]] =
+ * weights[t][k] * dy[t] (0 past the last kept slot) and dweights[t][k] =
+ * <dy[t], ys[place[t][k]]> (float32, 0 for a dropped slot).  dys or dweights
+ * may be NULL; ys may be NULL without dweights.
+ *
+ * Outputs may not overlap each other or an input.
+ */
+laplex_status laplex_dispatch(int64_t tokens, int64_t slots, int64_t n_experts, const int32_t* place,
+                              const int32_t* offsets, laplex_dtype type, int64_t width, const void* x, int64_t ldx,
+                              void* xs, int64_t ldxs, void* stream);
+laplex_status laplex_combine(int64_t tokens, int64_t slots, const int32_t* place, laplex_dtype type, int64_t width,
+                             const void* ys, int64_t ldys, const float* weights, void* y, int64_t ldy,
+                             void* stream);
+laplex_status laplex_combine_backward(int64_t tokens, int64_t slots, int64_t n_experts, const int32_t* place,
+                                      const int32_t* offsets, laplex_dtype type, int64_t width, const void* dy,
+                                      int64_t lddy, const void* ys, int64_t ldys, const float* weights, void* dys,
+                                      int64_t lddys, float* dweights, void* stream);
+
+/*
+ * laplex_recur -- y_t = h_t = exp(g_t) h_{t-1} + x_t along each sequence.
+ *
+ *   n, seqs   rows of all sequences together, and sequences.  offsets device
+ *             int32[seqs + 1], ascending: sequence q is rows offsets[q] ..
+ *             offsets[q + 1] - 1 (none if equal); rows outside all sequences
+ *             get y = 0.  NULL: seqs sequences of n / seqs rows each.
+ *   x, y      [n][width] of `type`.
+ *   g         [n][heads] of `gate_type` (`type` or LAPLEX_F32): logarithms of
+ *             the decays, each for width / heads neighbouring channels.
+ *             Where exp(g) is 0 (g = -inf) the state is forgotten, whatever
+ *             it held.
+ *   h0        float32 [seqs][width], the states before the first rows, or
+ *             NULL for 0.
+ *   final     float32 [seqs][width] or NULL: the states after the last rows
+ *             (h0 for a sequence without rows).
+ *   states    float32[laplex_recur_states(n, width)] or NULL: what
+ *             laplex_recur_backward needs of this pass.
+ *   ws        device scratch of laplex_recur_workspace(n, width, heads, 0)
+ *             bytes, 16-byte aligned.
+ *
+ * laplex_recur_backward -- gradients: dy [n][width] of `type` and dfinal
+ *   float32 [seqs][width] (or NULL) in; dx [n][width] of `type`, dg
+ *   [n][heads] of `gate_type`, dh0 float32 [seqs][width] out, each or NULL.
+ *   x, g, h0, offsets as in the forward pass, states from it (NULL if it has
+ *   no values).  Scratch: laplex_recur_workspace(n, width, heads, 1).
+ *
+ * laplex_recur_step -- one token for each of n requests:
+ *   state[slots[i]] = exp(g_i) state[slots[i]] + x_i, y_i = the new state.
+ *   state float32 [pool][width]; slots device int32[n], or NULL for slots[i]
+ *   = i; a slot outside [0, pool) has no state (y = 0).  No two requests
+ *   may share a slot.
+ *
+ * laplex_recur_workspace and laplex_recur_states return -1 for sizes out of
+ * range: 0 <= n < 2^31, 1 <= width <= 2^24, heads dividing width.
+ * Outputs may not overlap each other or an input (state apart).  Results
+ * repeat bit for bit.
+ */
+int64_t laplex_recur_workspace(int64_t n, int64_t width, int64_t heads, int backward);
+int64_t laplex_recur_states(int64_t n, int64_t width);
+laplex_status laplex_recur(int64_t n, int64_t seqs, const int32_t* offsets, int64_t width, int64_t heads,
+                           laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx, const void* g,
+                           int64_t ldg, const float* h0, void* y, int64_t ldy, float* final, float* states,
+                           void* ws, int64_t ws_bytes, void* stream);
+laplex_status laplex_recur_backward(int64_t n, int64_t seqs, const int32_t* offsets, int64_t width, int64_t heads,
+                                    laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx,
+                                    const void* g, int64_t ldg, const float* h0, const float* states,
+                                    const void* dy, int64_t lddy, const float* dfinal, void* dx, int64_t lddx,
+                                    void* dg, int64_t lddg, float* dh0, void* ws, int64_t ws_bytes, void* stream);
+laplex_status laplex_recur_step(int64_t n, int64_t pool, const int32_t* slots, int64_t width, int64_t heads,
+                                laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx,
+                                const void* g, int64_t ldg, float* state, void* y, int64_t ldy, void* stream);
+
 /* Kernel timing: while enabled, every kernel the library launches is
  * bracketed by HIP events on its stream (timing-only events, recorded
  * without a system-scope fence, so they order no memory for the host).

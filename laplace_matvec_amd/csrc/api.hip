@@ -37,6 +37,17 @@ laplex_status fail(laplex_status st, const std::string& msg)
     return st;
 }
 
+// Messages without formatting: nothing to throw at the C entry.
+laplex_status fail(laplex_status st, const char* msg) noexcept
+{
+    try {
+        g_last_error = msg;
+    } catch (...) {
+        g_last_error.clear();
+    }
+    return st;
+}
+
 laplex_status from_hip(hipError_t e, const char* where)
 {
     if (e == hipSuccess) return LAPLEX_OK;
@@ -1620,6 +1631,395 @@ laplex_status laplex_profile_entry(int i, const char** name, int64_t* launches, 
     if (name) *name = g_prof[i].name;
     if (launches) *launches = g_prof[i].launches;
     if (total_ms) *total_ms = g_prof[i].total_ms;
+    return LAPLEX_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------- token routing and recurrence
+//
+// Stateless calls: every array and all scratch are the caller's, so nothing
+// here allocates, waits or records an event.
+
+namespace {
+
+struct Rows {  // an array of rows; width 0: absent
+    const void* p;
+    int64_t rows, ld, width;
+    size_t size;
+};
+
+// Whether two arrays of rows share a byte.  Rows of one pitch may interleave
+// (parts of one wider row).
+bool rows_overlap(const Rows& a, const Rows& b)
+{
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+    const size_t sa = (size_t)a.ld * a.size, sb = (size_t)b.ld * b.size;
+    const size_t wa = (size_t)a.width * a.size, wb = (size_t)b.width * b.size;
+    if (!ranges_overlap(a.p, (size_t)(a.rows - 1) * sa + wa, b.p, (size_t)(b.rows - 1) * sb + wb)) return false;
+    if (sa != sb || a.rows < 2 || b.rows < 2) return true;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    const size_t d = y >= x ? (size_t)(y - x) % sa : (sa - (size_t)(x - y) % sa) % sa;  // b's column in a's rows
+    return d < wa || d + wb > sa;
+}
+
+const char* check_outputs(const Rows* outs, int n_out, const Rows* ins, int n_in)
+{
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (rows_overlap(outs[i], ins[j])) return "an output overlaps an input";
+        for (int j = i + 1; j < n_out; ++j)
+            if (rows_overlap(outs[i], outs[j])) return "two outputs overlap";
+    }
+    return nullptr;
+}
+
+// Values of one array stay below 2^46: byte offsets stay far inside 63 bits.
+bool rows_ok(const Rows& r)
+{
+    return !r.p || (r.ld >= r.width && r.ld <= (int64_t)1 << 40 && (double)r.rows * (double)r.ld < 7.0e13 &&
+                    (uintptr_t)r.p % r.size == 0);
+}
+
+size_t dtype_size(laplex_dtype t) { return t == LAPLEX_F32 ? 4 : 2; }
+bool dtype_ok(laplex_dtype t) { return t == LAPLEX_F32 || t == LAPLEX_BF16 || t == LAPLEX_F16; }
+
+bool route_sizes_ok(int64_t tokens, int64_t slots)
+{
+    return tokens >= 0 && slots >= 1 && slots <= kMaxLen && tokens <= kMaxLen / slots;
+}
+
+bool recur_sizes_ok(int64_t n, int64_t width, int64_t heads)
+{
+    return n >= 0 && n <= 0x7FFFFFFF && width >= 1 && width <= (int64_t)1 << 24 && heads >= 1 && heads <= width &&
+           width % heads == 0;
+}
+
+int64_t recur_tiles(int64_t n) { return (n + lx::kRecurTile - 1) / lx::kRecurTile; }
+int64_t recur_cols(int64_t width) { return (width + lx::kRecurCols - 1) / lx::kRecurCols; }
+
+// Fills the parts both directions share; a message if an argument is bad.
+const char* recur_common(lx::RecurArgs& A, int64_t n, int64_t seqs, const int32_t* offsets, int64_t width,
+                         int64_t heads, laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx,
+                         const void* g, int64_t ldg, const float* h0)
+{
+    if (!recur_sizes_ok(n, width, heads)) return "bad sizes: 0 <= n < 2^31, 1 <= width <= 2^24, heads divides width";
+    if (seqs < 1 || seqs > 0x7FFFFFFE) return "seqs must be in [1, 2^31 - 2]";
+    if (!offsets && n % seqs) return "without offsets n must be a multiple of seqs";
+    if (!dtype_ok(type) || (gate_type != type && gate_type != LAPLEX_F32)) return "bad type or gate_type";
+    if (n > 0 && (!x || !g)) return "x or g is NULL";
+    const int64_t tiles = recur_tiles(n), cols = recur_cols(width);
+    if (n > ((int64_t)1 << 38) / width) return "n * width must be at most 2^38";
+    A.n = n;
+    A.seqs = seqs;
+    A.seq_len = offsets ? 0 : n / seqs;
+    A.offsets = offsets;
+    A.width = (int)width;
+    A.heads = (int)heads;
+    A.per = (int)(width / heads);
+    A.tiles = tiles;
+    A.cols = (int)cols;
+    A.x = x;
+    A.ldx = ldx;
+    A.g = g;
+    A.ldg = ldg;
+    A.h0 = h0;
+    return nullptr;
+}
+
+size_t recur_map_bytes(int64_t n, int64_t width)
+{
+    const int64_t t = recur_tiles(n);
+    return t > 1 ? align256((size_t)((t - 1) * recur_cols(width) * lx::kRecurCols) * 8) : 0;
+}
+size_t recur_state_bytes(int64_t n, int64_t width)
+{
+    const int64_t t = recur_tiles(n);
+    return t > 1 ? align256((size_t)((t - 1) * recur_cols(width) * lx::kRecurCols) * 4) : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t laplex_route_workspace(int64_t tokens, int64_t slots, int64_t n_experts)
+{
+    if (!route_sizes_ok(tokens, slots) || n_experts < 1 || n_experts > lx::kRouteMaxExperts) return -1;
+    const int64_t tiles = (tokens * slots + lx::kRouteTile - 1) / lx::kRouteTile;
+    return tiles > 1 ? (tiles + 1) * n_experts * 4 : 0;
+}
+
+laplex_status laplex_route(const void* experts, int wide, int64_t tokens, int64_t slots, int64_t n_experts,
+                           int32_t* order, int32_t* place, int32_t* offsets, void* ws, int64_t ws_bytes,
+                           void* stream)
+{
+    const int64_t need = laplex_route_workspace(tokens, slots, n_experts);
+    if (need < 0)
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "tokens * slots must be at most 2^30 and n_experts in [1, 4096]");
+    if (wide != 0 && wide != 1) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "wide must be 0 or 1");
+    const int64_t n = tokens * slots;
+    if (!offsets || (n > 0 && (!experts || !order || !place)))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "experts, order, place or offsets is NULL");
+    if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < need))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_route_workspace");
+    const Rows outs[4] = {{order, 1, n, n, 4}, {place, 1, n, n, 4}, {offsets, 1, n_experts + 1, n_experts + 1, 4},
+                          {need > 0 ? ws : nullptr, 1, need, need, 1}};
+    const Rows in = {experts, 1, n, n, wide ? 8u : 4u};
+    if (!rows_ok(outs[0]) || !rows_ok(outs[1]) || !rows_ok(outs[2]) || !rows_ok(in))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a misaligned array");
+    if (const char* m = check_outputs(outs, 4, &in, 1)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::RouteArgs A;
+    A.ids = experts;
+    A.wide = wide;
+    A.n = n;
+    A.tiles = (n + lx::kRouteTile - 1) / lx::kRouteTile;
+    A.experts = (int)n_experts;
+    A.order = order;
+    A.place = place;
+    A.offsets = offsets;
+    A.hist = (uint32_t*)ws;
+    A.total = need > 0 ? (uint32_t*)ws + A.tiles * n_experts : nullptr;
+    LX_TRY(lx::route_launch(A, (hipStream_t)stream), "route");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_dispatch(int64_t tokens, int64_t slots, int64_t n_experts, const int32_t* place,
+                              const int32_t* offsets, laplex_dtype type, int64_t width, const void* x, int64_t ldx,
+                              void* xs, int64_t ldxs, void* stream)
+{
+    if (!route_sizes_ok(tokens, slots) || n_experts < 1 || n_experts > lx::kRouteMaxExperts || width < 1 ||
+        width > (int64_t)1 << 24 || !dtype_ok(type))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "bad sizes or type");
+    if (tokens == 0) return LAPLEX_OK;
+    if (!place || !offsets || !x || !xs) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "place, offsets, x or xs is NULL");
+    const size_t e = dtype_size(type);
+    const Rows out = {xs, tokens * slots, ldxs, width, e};
+    const Rows ins[3] = {{x, tokens, ldx, width, e}, {place, tokens, slots, slots, 4},
+                         {offsets, 1, n_experts + 1, n_experts + 1, 4}};
+    if (!rows_ok(out) || !rows_ok(ins[0])) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(&out, 1, ins, 3)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::MoveArgs A;
+    A.tokens = tokens;
+    A.slots = slots;
+    A.width = width;
+    A.experts = (int)n_experts;
+    A.place = place;
+    A.offsets = offsets;
+    A.in = x;
+    A.ld_in = ldx;
+    A.out = xs;
+    A.ld_out = ldxs;
+    LX_TRY(lx::move_rows_launch(lx::kMoveDispatch, (int)type, A, (hipStream_t)stream), "dispatch");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_combine(int64_t tokens, int64_t slots, const int32_t* place, laplex_dtype type, int64_t width,
+                             const void* ys, int64_t ldys, const float* weights, void* y, int64_t ldy,
+                             void* stream)
+{
+    if (!route_sizes_ok(tokens, slots) || width < 1 || width > (int64_t)1 << 24 || !dtype_ok(type))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "bad sizes or type");
+    if (tokens == 0) return LAPLEX_OK;
+    if (!place || !ys || !y) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "place, ys or y is NULL");
+    const size_t e = dtype_size(type);
+    const Rows out = {y, tokens, ldy, width, e};
+    const Rows ins[3] = {{ys, tokens * slots, ldys, width, e}, {place, tokens, slots, slots, 4},
+                         {weights, tokens, slots, slots, 4}};
+    if (!rows_ok(out) || !rows_ok(ins[0])) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(&out, 1, ins, 3)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::MoveArgs A;
+    A.tokens = tokens;
+    A.slots = slots;
+    A.width = width;
+    A.place = place;
+    A.weights = weights;
+    A.in = ys;
+    A.ld_in = ldys;
+    A.out = y;
+    A.ld_out = ldy;
+    LX_TRY(lx::move_rows_launch(lx::kMoveCombine, (int)type, A, (hipStream_t)stream), "combine");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_combine_backward(int64_t tokens, int64_t slots, int64_t n_experts, const int32_t* place,
+                                      const int32_t* offsets, laplex_dtype type, int64_t width, const void* dy,
+                                      int64_t lddy, const void* ys, int64_t ldys, const float* weights, void* dys,
+                                      int64_t lddys, float* dweights, void* stream)
+{
+    if (!route_sizes_ok(tokens, slots) || n_experts < 1 || n_experts > lx::kRouteMaxExperts || width < 1 ||
+        width > (int64_t)1 << 24 || !dtype_ok(type))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "bad sizes or type");
+    if (tokens == 0 || (!dys && !dweights)) return LAPLEX_OK;
+    if (!place || !dy || (dys && (!weights || !offsets)) || (dweights && !ys))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "place, dy, or what dys or dweights needs is NULL");
+    const size_t e = dtype_size(type);
+    const Rows outs[2] = {{dys, tokens * slots, lddys, width, e}, {dweights, tokens, slots, slots, 4}};
+    const Rows ins[5] = {{dy, tokens, lddy, width, e}, {dweights ? ys : nullptr, tokens * slots, ldys, width, e},
+                         {place, tokens, slots, slots, 4}, {weights, tokens, slots, slots, 4},
+                         {offsets, 1, n_experts + 1, n_experts + 1, 4}};
+    if (!rows_ok(outs[0]) || !rows_ok(ins[0]) || !rows_ok(ins[1]))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 2, ins, 5)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::MoveArgs A;
+    A.tokens = tokens;
+    A.slots = slots;
+    A.width = width;
+    A.experts = (int)n_experts;
+    A.place = place;
+    A.offsets = offsets;
+    A.weights = weights;
+    A.in = dweights ? ys : nullptr;
+    A.ld_in = ldys;
+    A.dy = dy;
+    A.ld_dy = lddy;
+    A.out = dys;
+    A.ld_out = lddys;
+    A.dw = dweights;
+    LX_TRY(lx::move_rows_launch(lx::kMoveCombineGrad, (int)type, A, (hipStream_t)stream), "combine backward");
+    return LAPLEX_OK;
+}
+
+int64_t laplex_recur_states(int64_t n, int64_t width)
+{
+    if (!recur_sizes_ok(n, width, 1)) return -1;
+    const int64_t t = recur_tiles(n);
+    return t > 1 ? (t - 1) * recur_cols(width) * lx::kRecurCols : 0;
+}
+
+int64_t laplex_recur_workspace(int64_t n, int64_t width, int64_t heads, int backward)
+{
+    if (!recur_sizes_ok(n, width, heads) || (backward != 0 && backward != 1)) return -1;
+    size_t b = recur_map_bytes(n, width) + recur_state_bytes(n, width);
+    if (backward && heads < width && !lx::recur_heads_inside((int)width, (int)(width / heads)))
+        b += align256((size_t)n * (size_t)(recur_cols(width) + heads) * 4);
+    return (int64_t)b;
+}
+
+laplex_status laplex_recur(int64_t n, int64_t seqs, const int32_t* offsets, int64_t width, int64_t heads,
+                           laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx, const void* g,
+                           int64_t ldg, const float* h0, void* y, int64_t ldy, float* final, float* states,
+                           void* ws, int64_t ws_bytes, void* stream)
+{
+    lx::RecurArgs A;
+    if (const char* m = recur_common(A, n, seqs, offsets, width, heads, type, gate_type, x, ldx, g, ldg, h0))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    if (n > 0 && !y) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "y is NULL");
+    const int64_t need = laplex_recur_workspace(n, width, heads, 0);
+    if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < need))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_recur_workspace");
+    const size_t e = dtype_size(type), eg = dtype_size(gate_type);
+    const int64_t ns = laplex_recur_states(n, width);
+    const Rows outs[4] = {{y, n, ldy, width, e}, {final, seqs, width, width, 4},
+                          {ns > 0 ? states : nullptr, 1, ns, ns, 4}, {need > 0 ? ws : nullptr, 1, need, need, 1}};
+    const Rows ins[4] = {{x, n, ldx, width, e}, {g, n, ldg, heads, eg}, {h0, seqs, width, width, 4},
+                         {offsets, 1, seqs + 1, seqs + 1, 4}};
+    for (const Rows& r : {outs[0], outs[1], ins[0], ins[1], ins[2]})
+        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 4, ins, 4)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    A.y = y;
+    A.ldy = ldy;
+    A.final = final;
+    A.maps = (float2*)ws;
+    A.states = states ? states : (float*)((char*)ws + recur_map_bytes(n, width));
+    if (final && (offsets || n == 0)) LX_TRY(lx::recur_empty_launch(A, h0, final, s), "recurrence");
+    if (n == 0) return LAPLEX_OK;
+    LX_TRY(lx::recur_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, s), "recurrence");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_recur_backward(int64_t n, int64_t seqs, const int32_t* offsets, int64_t width, int64_t heads,
+                                    laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx,
+                                    const void* g, int64_t ldg, const float* h0, const float* states,
+                                    const void* dy, int64_t lddy, const float* dfinal, void* dx, int64_t lddx,
+                                    void* dg, int64_t lddg, float* dh0, void* ws, int64_t ws_bytes, void* stream)
+{
+    lx::RecurArgs A;
+    if (const char* m = recur_common(A, n, seqs, offsets, width, heads, type, gate_type, x, ldx, g, ldg, h0))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    if (!dx && !dg && !dh0) return LAPLEX_OK;
+    if (n > 0 && !dy) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "dy is NULL");
+    const int64_t ns = laplex_recur_states(n, width);
+    if (ns > 0 && !states) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "states is NULL");
+    const int64_t need = laplex_recur_workspace(n, width, heads, 1);
+    if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < need))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_recur_workspace");
+    const size_t e = dtype_size(type), eg = dtype_size(gate_type);
+    const Rows outs[4] = {{dx, n, lddx, width, e}, {dg, n, lddg, heads, eg}, {dh0, seqs, width, width, 4},
+                          {need > 0 ? ws : nullptr, 1, need, need, 1}};
+    const Rows ins[7] = {{x, n, ldx, width, e}, {g, n, ldg, heads, eg}, {h0, seqs, width, width, 4},
+                         {offsets, 1, seqs + 1, seqs + 1, 4}, {dy, n, lddy, width, e},
+                         {dfinal, seqs, width, width, 4}, {ns > 0 ? states : nullptr, 1, ns, ns, 4}};
+    for (const Rows& r : {outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[4], ins[5], ins[6]})
+        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 4, ins, 7)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    A.dy = dy;
+    A.lddy = lddy;
+    A.dfinal = dfinal;
+    A.states_in = states;
+    A.dx = dx;
+    A.lddx = lddx;
+    A.dg = dg;
+    A.lddg = lddg;
+    A.dh0 = dh0;
+    const size_t mb = recur_map_bytes(n, width), sb = recur_state_bytes(n, width);
+    A.maps = (float2*)ws;
+    A.states = (float*)((char*)ws + mb);
+    A.part = (float*)((char*)ws + mb + sb);
+    if (dh0 && (offsets || n == 0)) LX_TRY(lx::recur_empty_launch(A, dfinal, dh0, s), "recurrence backward");
+    if (n == 0) return LAPLEX_OK;
+    LX_TRY(lx::recur_grad_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, s), "recurrence backward");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_recur_step(int64_t n, int64_t pool, const int32_t* slots, int64_t width, int64_t heads,
+                                laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx,
+                                const void* g, int64_t ldg, float* state, void* y, int64_t ldy, void* stream)
+{
+    if (!recur_sizes_ok(n, width, heads) || pool < 0 || pool > 0x7FFFFFFF)
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "bad sizes: 0 <= n, pool < 2^31, 1 <= width <= 2^24, heads divides width");
+    if (!dtype_ok(type) || (gate_type != type && gate_type != LAPLEX_F32))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "bad type or gate_type");
+    if (!slots && n > pool) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "without slots n must be at most pool");
+    if (n == 0) return LAPLEX_OK;
+    if (!x || !g || !y || (pool > 0 && !state)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "x, g, state or y is NULL");
+    const size_t e = dtype_size(type), eg = dtype_size(gate_type);
+    const Rows outs[2] = {{y, n, ldy, width, e}, {state, pool, width, width, 4}};
+    const Rows ins[3] = {{x, n, ldx, width, e}, {g, n, ldg, heads, eg}, {slots, 1, n, n, 4}};
+    for (const Rows& r : {outs[0], outs[1], ins[0], ins[1]})
+        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 2, ins, 3)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::RecurStepArgs A;
+    A.n = n;
+    A.pool = pool;
+    A.width = (int)width;
+    A.heads = (int)heads;
+    A.per = (int)(width / heads);
+    A.x = x;
+    A.g = g;
+    A.y = y;
+    A.ldx = ldx;
+    A.ldg = ldg;
+    A.ldy = ldy;
+    A.slots = slots;
+    A.state = state;
+    LX_TRY(lx::recur_step_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, (hipStream_t)stream),
+           "recurrence step");
     return LAPLEX_OK;
 }
 

@@ -358,4 +358,89 @@ hipError_t gram_bounds_launch(const float* sa, int64_t n, const float* sb, int64
 hipError_t gram_ranks_launch(const uint32_t* perm, int64_t n, uint32_t* rank, hipStream_t s);
 hipError_t gram_launch(const GramArgs& a, hipStream_t s);
 
+// ---- token routing (route.hip) ----
+constexpr int kRouteTile = 4096;        // slots per workgroup
+constexpr int kRouteMaxExperts = 4096;  // 80 KB of counters in LDS
+struct RouteArgs {
+    const void* ids = nullptr;  // [n] int32, or int64 if wide
+    int wide = 0;
+    int64_t n = 0, tiles = 0;
+    int experts = 0;
+    int32_t* order = nullptr;    // [n]
+    int32_t* place = nullptr;    // [n]
+    int32_t* offsets = nullptr;  // [experts + 1]
+    uint32_t* hist = nullptr;    // [tiles][experts], more than one tile only
+    uint32_t* total = nullptr;   // [experts], likewise
+};
+hipError_t route_launch(const RouteArgs& a, hipStream_t s);
+
+enum MoveKind { kMoveDispatch, kMoveCombine, kMoveCombineGrad };
+struct MoveArgs {
+    int64_t tokens = 0, slots = 0, width = 0;
+    int experts = 0;
+    int groups = 0;                    // 16-byte (or single-value) groups per row, set at launch
+    const int32_t* place = nullptr;    // [tokens][slots]
+    const int32_t* offsets = nullptr;  // [experts + 1] (dispatch, combine_grad with dys)
+    const float* weights = nullptr;    // [tokens][slots]
+    const void* in = nullptr;          // x, or ys
+    const void* dy = nullptr;          // combine_grad
+    void* out = nullptr;               // xs, y, or dys
+    float* dw = nullptr;               // combine_grad
+    int64_t ld_in = 0, ld_out = 0, ld_dy = 0;
+};
+// dtype: 0 float32, 1 bfloat16, 2 float16
+hipError_t move_rows_launch(MoveKind kind, int dtype, const MoveArgs& a, hipStream_t s);
+
+// ---- gated recurrence (recur.hip, recur_grad.hip) ----
+constexpr int kRecurTile = 128;  // rows of a tile
+constexpr int kRecurCols = 64;   // channels of a tile
+struct RecurArgs {
+    int64_t n = 0;         // rows
+    int64_t seqs = 0;      // sequences
+    int64_t seq_len = 0;   // rows of each, without offsets
+    const int32_t* offsets = nullptr;  // [seqs + 1], or null: equal sequences
+    int width = 0, heads = 0, per = 0;  // channels, decays per row, channels per decay
+    int64_t tiles = 0;     // row tiles
+    int cols = 0;          // channel tiles
+    const void* x = nullptr;
+    const void* g = nullptr;
+    int64_t ldx = 0, ldg = 0;
+    const float* h0 = nullptr;  // [seqs][width]
+    void* y = nullptr;
+    int64_t ldy = 0;
+    float* final = nullptr;     // [seqs][width]
+    // backward
+    const void* dy = nullptr;
+    int64_t lddy = 0;
+    const float* dfinal = nullptr;  // [seqs][width]
+    const float* states_in = nullptr;  // [tiles - 1][cols * kRecurCols]: the state after each row tile
+    void* dx = nullptr;
+    void* dg = nullptr;
+    int64_t lddx = 0, lddg = 0;
+    float* dh0 = nullptr;       // [seqs][width]
+    // scratch, [tiles - 1][cols * kRecurCols] each
+    float2* maps = nullptr;     // composed maps of the tiles, in the order of the pass
+    float* states = nullptr;    // state after each row tile (backward: gradient before), likewise
+    float* part = nullptr;      // backward: [n][cols + heads] sums of dg within a channel tile
+};
+// dtype / gtype: 0 float32, 1 bfloat16, 2 float16 (gtype: dtype or 0)
+hipError_t recur_launch(const RecurArgs& a, int dtype, int gtype, hipStream_t s);
+hipError_t recur_grad_launch(const RecurArgs& a, int dtype, int gtype, hipStream_t s);
+// Sequences without rows: final = h0 (forward), dh0 = dfinal (backward).
+hipError_t recur_empty_launch(const RecurArgs& a, const float* from, float* to, hipStream_t s);
+// Whether a decay's channels lie within one channel tile.
+__host__ __device__ inline bool recur_heads_inside(int width, int per) { return kRecurCols % per == 0 || width <= kRecurCols; }
+
+struct RecurStepArgs {
+    int64_t n = 0, pool = 0;
+    int width = 0, heads = 0, per = 0, groups = 0;
+    const void* x = nullptr;
+    const void* g = nullptr;
+    void* y = nullptr;
+    int64_t ldx = 0, ldg = 0, ldy = 0;
+    const int32_t* slots = nullptr;
+    float* state = nullptr;  // [pool][width]
+};
+hipError_t recur_step_launch(const RecurStepArgs& a, int dtype, int gtype, hipStream_t s);
+
 }  // namespace lx

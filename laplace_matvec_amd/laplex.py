@@ -7,8 +7,10 @@ is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -42,6 +44,19 @@ SIGNATURES = {
     "laplex_plan_set_option": (_I32, [_VP, _I32, _I64]),
     "laplex_plan_set_temperature": (_I32, [_VP, ctypes.c_double]),
     "laplex_backward": (_I32, [_VP, _VP, _VP, _I64, _I32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "laplex_route_workspace": (_I64, [_I64, _I64, _I64]),
+    "laplex_route": (_I32, [_VP, _I32, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _I64, _VP]),
+    "laplex_dispatch": (_I32, [_I64, _I64, _I64, _VP, _VP, _I32, _I64, _VP, _I64, _VP, _I64, _VP]),
+    "laplex_combine": (_I32, [_I64, _I64, _VP, _I32, _I64, _VP, _I64, _VP, _VP, _I64, _VP]),
+    "laplex_combine_backward": (_I32, [_I64, _I64, _I64, _VP, _VP, _I32, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _I64,
+                                       _VP, _VP]),
+    "laplex_recur_workspace": (_I64, [_I64, _I64, _I64, _I32]),
+    "laplex_recur_states": (_I64, [_I64, _I64]),
+    "laplex_recur": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP,
+                            _VP, _I64, _VP]),
+    "laplex_recur_backward": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _VP,
+                                     _I64, _VP, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP]),
+    "laplex_recur_step": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP]),
     "laplex_profile_enable": (_I32, [_I32]),
     "laplex_profile_only": (_I32, [ctypes.c_char_p]),
     "laplex_profile_reset": (_I32, []),
@@ -295,6 +310,294 @@ def laplex_plan_info(plan: Plan):
 
 def laplex_plan_destroy(plan: Plan):
     plan.destroy()
+
+
+# ---- tokens: routing by expert and the gated recurrence -------------------
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class Route(NamedTuple):
+    """Token slots sorted by expert (see laplex_route in include/laplex.h)."""
+
+    order: torch.Tensor    # int32 [tokens * slots]: slot of each row, -1 past the last
+    place: torch.Tensor    # int32 [tokens, slots]: row of each slot, -1 if dropped
+    offsets: torch.Tensor  # int32 [experts + 1]: first row of each expert
+
+
+class Recurrence(NamedTuple):
+    """What laplex_recur returns."""
+
+    y: torch.Tensor
+    final: torch.Tensor | None   # float32 [seqs, width], with final=True
+    states: torch.Tensor | None  # for laplex_recur_backward, with keep=True
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """(rows, width, values between rows) of a tensor [..., width] whose
+    leading dimensions step evenly through memory."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is None:
+        if t.dtype not in _DTYPES:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    elif t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    width = t.shape[-1]
+    if t.is_contiguous():
+        return t.numel() // max(width, 1), width, max(width, 1)
+    st, sz = t.stride(), t.shape
+    ok = width == 1 or st[-1] == 1
+    ld, rows = None, 1  # pitch of the rows so far, from the innermost leading dimension
+    for n, step in zip(reversed(sz[:-1]), reversed(st[:-1])):
+        if n != 1:
+            if ld is None:
+                ld = step
+            elif step != ld * rows:
+                ok = False
+        rows *= n
+    ld = width if ld is None else ld
+    if not ok or ld < width:
+        raise ValueError(f"{name} must have unit stride along its last dimension and evenly spaced rows")
+    return rows, width, ld
+
+
+def _flat(t, name, dtype, shape, device):
+    """A contiguous tensor of one type and shape, or None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _launch(stream, device):
+    """(stream handle, context in which outputs and scratch are allocated):
+    with a stream other than the current one they come from its own pool."""
+    if stream is None:
+        p = torch.cuda.current_stream(device).cuda_stream
+        if device.index == torch.cuda.current_device():
+            return ctypes.c_void_p(p), contextlib.nullcontext()
+        return ctypes.c_void_p(p), torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+
+
+def _scratch(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
+
+
+def _size(value, where):
+    if value < 0:
+        raise ValueError(f"{where}: sizes out of range")
+    return value
+
+
+def _route_parts(route, device):
+    place, offsets = route.place, route.offsets
+    for name, t, dim in (("place", place, 2), ("offsets", offsets, 1)):
+        if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.dim() == dim
+                and t.is_contiguous()):
+            raise TypeError(f"route.{name} must be a contiguous {dim}-D int32 tensor on {device}")
+    return place, offsets, place.shape[0], place.shape[1], offsets.numel() - 1
+
+
+def laplex_route(experts, n_experts: int, stream=None) -> Route:
+    """Stable sort of token slots by expert: experts int32 or int64
+    [tokens, slots] (or [tokens]); ids outside [0, n_experts) drop the slot."""
+    if not (isinstance(experts, torch.Tensor) and experts.is_cuda and experts.is_contiguous()
+            and experts.dtype in (torch.int32, torch.int64) and experts.dim() in (1, 2)):
+        raise TypeError("experts must be a contiguous int32 or int64 CUDA tensor [tokens, slots]")
+    tokens, slots = experts.shape[0], 1 if experts.dim() == 1 else experts.shape[1]
+    lib, dev = load(), experts.device
+    need = _size(lib.laplex_route_workspace(tokens, slots, n_experts), "laplex_route")
+    s, ctx = _launch(stream, dev)
+    with ctx:
+        order = torch.empty(tokens * slots, dtype=torch.int32, device=dev)
+        place = torch.empty((tokens, slots), dtype=torch.int32, device=dev)
+        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
+        ws = _scratch(need, dev)
+        _check(lib.laplex_route(_ptr(experts), int(experts.dtype == torch.int64), tokens, slots, n_experts,
+                                _ptr(order), _ptr(place), _ptr(offsets), _ptr(ws), need, s), "laplex_route")
+    return Route(order, place, offsets)
+
+
+def laplex_dispatch(route: Route, x, stream=None):
+    """Rows of x [tokens, width] at their places by expert
+    [tokens * slots, width], 0 past the last kept slot.  Its gradient is
+    laplex_combine(route, dxs)."""
+    rows, width, ld = _rows(x, "x")
+    place, offsets, tokens, slots, experts = _route_parts(route, x.device)
+    if x.dim() != 2 or rows != tokens:
+        raise ValueError(f"x must have shape [{tokens}][width]")
+    s, ctx = _launch(stream, x.device)
+    with ctx:
+        xs = torch.empty((tokens * slots, width), dtype=x.dtype, device=x.device)
+        _check(load().laplex_dispatch(tokens, slots, experts, _ptr(place), _ptr(offsets), _DTYPES[x.dtype], width,
+                                      _ptr(x), ld, _ptr(xs), width, s), "laplex_dispatch")
+    return xs
+
+
+def laplex_combine(route: Route, ys, weights=None, stream=None):
+    """Expert rows ys [tokens * slots, width] back to their tokens
+    [tokens, width], summed with float32 weights [tokens, slots] (None: ones)."""
+    rows, width, ld = _rows(ys, "ys")
+    place, _, tokens, slots, _ = _route_parts(route, ys.device)
+    if ys.dim() != 2 or rows != tokens * slots:
+        raise ValueError(f"ys must have shape [{tokens * slots}][width]")
+    weights = _flat(weights, "weights", torch.float32, (tokens, slots), ys.device)
+    s, ctx = _launch(stream, ys.device)
+    with ctx:
+        y = torch.empty((tokens, width), dtype=ys.dtype, device=ys.device)
+        _check(load().laplex_combine(tokens, slots, _ptr(place), _DTYPES[ys.dtype], width, _ptr(ys), ld,
+                                     _ptr(weights), _ptr(y), width, s), "laplex_combine")
+    return y
+
+
+def laplex_combine_backward(route: Route, dy, ys, weights, stream=None):
+    """Gradients (dys, dweights) of laplex_combine with weights."""
+    rows, width, ld = _rows(dy, "dy")
+    place, offsets, tokens, slots, experts = _route_parts(route, dy.device)
+    if dy.dim() != 2 or rows != tokens:
+        raise ValueError(f"dy must have shape [{tokens}][width]")
+    _, _, ldys = _rows(ys, "ys", dy.dtype, (tokens * slots, width))
+    _same_device(dy.device, ys=ys)
+    if weights is None:
+        raise TypeError("weights must be given")
+    weights = _flat(weights, "weights", torch.float32, (tokens, slots), dy.device)
+    s, ctx = _launch(stream, dy.device)
+    with ctx:
+        dys = torch.empty((tokens * slots, width), dtype=dy.dtype, device=dy.device)
+        dw = torch.empty((tokens, slots), dtype=torch.float32, device=dy.device)
+        _check(load().laplex_combine_backward(tokens, slots, experts, _ptr(place), _ptr(offsets), _DTYPES[dy.dtype],
+                                              width, _ptr(dy), ld, _ptr(ys), ldys, _ptr(weights), _ptr(dys), width,
+                                              _ptr(dw), s), "laplex_combine_backward")
+    return dys, dw
+
+
+def _recur_parts(x, g, offsets, h0):
+    """Sizes and pitches of a recurrence's inputs, checked."""
+    n, width, ldx = _rows(x, "x")
+    if x.dim() not in (2, 3) or (x.dim() == 3 and offsets is not None):
+        raise ValueError("x must be [rows, width], or [seqs, rows, width] without offsets")
+    if not isinstance(g, torch.Tensor) or g.shape[:-1] != x.shape[:-1]:
+        raise ValueError("g must have x's leading dimensions")
+    if g.dtype not in (x.dtype, torch.float32):
+        raise TypeError("g must have x's type or be float32")
+    _, heads, ldg = _rows(g, "g")
+    if width < 1 or heads < 1 or width % heads:
+        raise ValueError("g's last dimension must divide x's")
+    dev = x.device
+    if offsets is not None:
+        if not (isinstance(offsets, torch.Tensor) and offsets.dim() == 1 and offsets.numel() > 1):
+            raise TypeError("offsets must be an int32 tensor [seqs + 1]")
+        _flat(offsets, "offsets", torch.int32, offsets.shape, dev)
+        seqs = offsets.numel() - 1
+    else:
+        seqs = x.shape[0] if x.dim() == 3 else 1
+    _same_device(dev, g=g)
+    _flat(h0, "h0", torch.float32, (seqs, width), dev)
+    return n, seqs, width, heads, ldx, ldg
+
+
+def laplex_recur(x, g, offsets=None, h0=None, final: bool = False, keep: bool = False, stream=None) -> Recurrence:
+    """h_t = exp(g_t) h_{t-1} + x_t along each sequence; y is h.
+
+    x [rows, width] (one sequence, or those of int32 offsets [seqs + 1]) or
+    [seqs, rows, width]; g [..., heads] of x's type or float32, one decay's
+    logarithm for each width / heads neighbouring channels; h0 float32
+    [seqs, width] or None.  final: also return the last states; keep: also
+    return what laplex_recur_backward needs."""
+    n, seqs, width, heads, ldx, ldg = _recur_parts(x, g, offsets, h0)
+    lib, dev = load(), x.device
+    need = _size(lib.laplex_recur_workspace(n, width, heads, 0), "laplex_recur")
+    s, ctx = _launch(stream, dev)
+    with ctx:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        hf = torch.empty((seqs, width), dtype=torch.float32, device=dev) if final else None
+        states = torch.empty(lib.laplex_recur_states(n, width), dtype=torch.float32, device=dev) if keep else None
+        ws = _scratch(need, dev)
+        _check(lib.laplex_recur(n, seqs, _ptr(offsets), width, heads, _DTYPES[x.dtype], _DTYPES[g.dtype], _ptr(x), ldx,
+                                _ptr(g), ldg, _ptr(h0), _ptr(y), width, _ptr(hf), _some(states), _ptr(ws), need, s),
+               "laplex_recur")
+    return Recurrence(y, hf, states)
+
+
+def _some(t):
+    """A tensor's pointer, None if it has no values."""
+    return None if t is None or t.numel() == 0 else ctypes.c_void_p(t.data_ptr())
+
+
+def laplex_recur_backward(x, g, dy, states, offsets=None, h0=None, dfinal=None, want=("dx", "dg", "dh0"),
+                          stream=None) -> dict:
+    """Gradients of laplex_recur from dy (y's shape and type) and dfinal
+    (float32 [seqs, width] or None); x, g, offsets and h0 as in the forward
+    pass, states from it (keep=True).  Returns the requested tensors among
+    dx, dg and dh0 (float32 [seqs, width])."""
+    n, seqs, width, heads, ldx, ldg = _recur_parts(x, g, offsets, h0)
+    dev = x.device
+    _, _, lddy = _rows(dy, "dy", x.dtype, x.shape)
+    _same_device(dev, dy=dy)
+    lib = load()
+    need = _size(lib.laplex_recur_workspace(n, width, heads, 1), "laplex_recur_backward")
+    if not isinstance(states, torch.Tensor):
+        raise TypeError("states must be those of laplex_recur(keep=True)")
+    _flat(states, "states", torch.float32, (lib.laplex_recur_states(n, width),), dev)
+    _flat(dfinal, "dfinal", torch.float32, (seqs, width), dev)
+    s, ctx = _launch(stream, dev)
+    out = {}
+    with ctx:
+        if "dx" in want:
+            out["dx"] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if "dg" in want:
+            out["dg"] = torch.empty(g.shape, dtype=g.dtype, device=dev)
+        if "dh0" in want:
+            out["dh0"] = torch.empty((seqs, width), dtype=torch.float32, device=dev)
+        ws = _scratch(need, dev)
+        _check(lib.laplex_recur_backward(n, seqs, _ptr(offsets), width, heads, _DTYPES[x.dtype], _DTYPES[g.dtype],
+                                         _ptr(x), ldx, _ptr(g), ldg, _ptr(h0), _some(states), _ptr(dy), lddy,
+                                         _ptr(dfinal), _ptr(out.get("dx")), width, _ptr(out.get("dg")), heads,
+                                         _ptr(out.get("dh0")), _ptr(ws), need, s), "laplex_recur_backward")
+    return out
+
+
+def laplex_recur_step(x, g, state, slots=None, stream=None):
+    """One token for each request: state[slots[i]] = exp(g_i) state[slots[i]]
+    + x_i in place (float32 [pool, width]); returns y [n, width], the new
+    states in x's type.  slots int32 [n] (None: request i has state i); a
+    slot outside the pool has no state and gives 0."""
+    n, width, ldx = _rows(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must have shape [n][width]")
+    if not isinstance(g, torch.Tensor) or g.dim() != 2 or g.shape[0] != n or g.shape[1] < 1 or width % g.shape[1]:
+        raise ValueError("g must have shape [n][heads] with heads dividing the width")
+    if g.dtype not in (x.dtype, torch.float32):
+        raise TypeError("g must have x's type or be float32")
+    _, heads, ldg = _rows(g, "g")
+    dev = x.device
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise TypeError("state must be a float32 tensor [pool][width]")
+    _flat(state, "state", torch.float32, (state.shape[0], width), dev)
+    _flat(slots, "slots", torch.int32, (n,), dev)
+    _same_device(dev, g=g)
+    s, ctx = _launch(stream, dev)
+    with ctx:
+        y = torch.empty((n, width), dtype=x.dtype, device=dev)
+        _check(load().laplex_recur_step(n, state.shape[0], _ptr(slots), width, heads, _DTYPES[x.dtype],
+                                        _DTYPES[g.dtype], _ptr(x), ldx, _ptr(g), ldg, _ptr(state), _ptr(y), width, s),
+               "laplex_recur_step")
+    return y
 
 
 # ---- kernel timing -------------------------------------------------------
