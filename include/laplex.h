@@ -335,7 +335,7 @@ laplex_status laplex_combine_backward(int64_t tokens, int64_t slots, int64_t n_e
  *   final     float32 [seqs][width] or NULL: the states after the last rows
  *             (h0 for a sequence without rows).
  *   states    float32[laplex_recur_states(n, width)] or NULL: what
- *             laplex_recur_backward needs of this pass.
+ *             laplex_recur_backward needs of this pass (16-byte aligned).
  *   ws        device scratch of laplex_recur_workspace(n, width, heads, 0)
  *             bytes, 16-byte aligned.
  *

@@ -1727,15 +1727,26 @@ const char* recur_common(lx::RecurArgs& A, int64_t n, int64_t seqs, const int32_
     return nullptr;
 }
 
+// Scratch of a pass: 256 bytes with the ticket, the maps, the states; none
+// for a single row tile.
+constexpr size_t kTicketBytes = 256;
 size_t recur_map_bytes(int64_t n, int64_t width)
 {
     const int64_t t = recur_tiles(n);
     return t > 1 ? align256((size_t)((t - 1) * recur_cols(width) * lx::kRecurCols) * 8) : 0;
 }
-size_t recur_state_bytes(int64_t n, int64_t width)
+size_t recur_pass_bytes(int64_t n, int64_t width)
 {
-    const int64_t t = recur_tiles(n);
-    return t > 1 ? align256((size_t)((t - 1) * recur_cols(width) * lx::kRecurCols) * 4) : 0;
+    const size_t m = recur_map_bytes(n, width);
+    return m ? kTicketBytes + m + align256(m / 2) : 0;
+}
+void recur_scratch(lx::RecurArgs& A, void* ws)
+{
+    const size_t m = recur_map_bytes(A.n, A.width);
+    A.ticket = (uint32_t*)ws;
+    A.maps = (uint64_t*)((char*)ws + kTicketBytes);
+    A.states = (uint32_t*)((char*)ws + kTicketBytes + m);
+    A.part = (float*)((char*)ws + recur_pass_bytes(A.n, A.width));
 }
 
 }  // namespace
@@ -1897,7 +1908,7 @@ int64_t laplex_recur_states(int64_t n, int64_t width)
 int64_t laplex_recur_workspace(int64_t n, int64_t width, int64_t heads, int backward)
 {
     if (!recur_sizes_ok(n, width, heads) || (backward != 0 && backward != 1)) return -1;
-    size_t b = recur_map_bytes(n, width) + recur_state_bytes(n, width);
+    size_t b = recur_pass_bytes(n, width);
     if (backward && heads < width && !lx::recur_heads_inside((int)width, (int)(width / heads)))
         b += align256((size_t)n * (size_t)(recur_cols(width) + heads) * 4);
     return (int64_t)b;
@@ -1917,6 +1928,7 @@ laplex_status laplex_recur(int64_t n, int64_t seqs, const int32_t* offsets, int6
         return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_recur_workspace");
     const size_t e = dtype_size(type), eg = dtype_size(gate_type);
     const int64_t ns = laplex_recur_states(n, width);
+    if (ns > 0 && (uintptr_t)states % 16) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "states must be 16-byte aligned");
     const Rows outs[4] = {{y, n, ldy, width, e}, {final, seqs, width, width, 4},
                           {ns > 0 ? states : nullptr, 1, ns, ns, 4}, {need > 0 ? ws : nullptr, 1, need, need, 1}};
     const Rows ins[4] = {{x, n, ldx, width, e}, {g, n, ldg, heads, eg}, {h0, seqs, width, width, 4},
@@ -1930,10 +1942,8 @@ laplex_status laplex_recur(int64_t n, int64_t seqs, const int32_t* offsets, int6
     A.y = y;
     A.ldy = ldy;
     A.final = final;
-    A.maps = (float2*)ws;
-    A.states = states ? states : (float*)((char*)ws + recur_map_bytes(n, width));
-    if (final && (offsets || n == 0)) LX_TRY(lx::recur_empty_launch(A, h0, final, s), "recurrence");
-    if (n == 0) return LAPLEX_OK;
+    recur_scratch(A, ws);
+    if (states) A.states = (uint32_t*)states;
     LX_TRY(lx::recur_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, s), "recurrence");
     return LAPLEX_OK;
 }
@@ -1975,12 +1985,7 @@ laplex_status laplex_recur_backward(int64_t n, int64_t seqs, const int32_t* offs
     A.dg = dg;
     A.lddg = lddg;
     A.dh0 = dh0;
-    const size_t mb = recur_map_bytes(n, width), sb = recur_state_bytes(n, width);
-    A.maps = (float2*)ws;
-    A.states = (float*)((char*)ws + mb);
-    A.part = (float*)((char*)ws + mb + sb);
-    if (dh0 && (offsets || n == 0)) LX_TRY(lx::recur_empty_launch(A, dfinal, dh0, s), "recurrence backward");
-    if (n == 0) return LAPLEX_OK;
+    recur_scratch(A, ws);
     LX_TRY(lx::recur_grad_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, s), "recurrence backward");
     return LAPLEX_OK;
 }

@@ -392,7 +392,7 @@ struct MoveArgs {
 hipError_t move_rows_launch(MoveKind kind, int dtype, const MoveArgs& a, hipStream_t s);
 
 // ---- gated recurrence (recur.hip, recur_grad.hip) ----
-constexpr int kRecurTile = 128;  // rows of a tile
+constexpr int kRecurTile = 256;  // rows of a tile
 constexpr int kRecurCols = 64;   // channels of a tile
 struct RecurArgs {
     int64_t n = 0;         // rows
@@ -418,16 +418,15 @@ struct RecurArgs {
     void* dg = nullptr;
     int64_t lddx = 0, lddg = 0;
     float* dh0 = nullptr;       // [seqs][width]
-    // scratch, [tiles - 1][cols * kRecurCols] each
-    float2* maps = nullptr;     // composed maps of the tiles, in the order of the pass
-    float* states = nullptr;    // state after each row tile (backward: gradient before), likewise
+    // scratch: [tiles - 1][cols * kRecurCols] each, in the order of the pass
+    uint32_t* ticket = nullptr;
+    uint64_t* maps = nullptr;   // composed map of each row tile
+    uint32_t* states = nullptr; // bits of the state after each row tile (backward: gradient before)
     float* part = nullptr;      // backward: [n][cols + heads] sums of dg within a channel tile
 };
 // dtype / gtype: 0 float32, 1 bfloat16, 2 float16 (gtype: dtype or 0)
 hipError_t recur_launch(const RecurArgs& a, int dtype, int gtype, hipStream_t s);
 hipError_t recur_grad_launch(const RecurArgs& a, int dtype, int gtype, hipStream_t s);
-// Sequences without rows: final = h0 (forward), dh0 = dfinal (backward).
-hipError_t recur_empty_launch(const RecurArgs& a, const float* from, float* to, hipStream_t s);
 // Whether a decay's channels lie within one channel tile.
 __host__ __device__ inline bool recur_heads_inside(int width, int per) { return kRecurCols % per == 0 || width <= kRecurCols; }
 

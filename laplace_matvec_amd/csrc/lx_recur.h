@@ -5,10 +5,9 @@
 // the causal half of the operator's scan with its decays given per token: an
 // affine map per row, composed along rows.  Rows are cut into tiles of
 // kRecurTile rows by kRecurCols channels, one workgroup each.  A thread has V
-// neighbouring channels of L consecutive rows in registers; the LR threads
-// of a row group cover the tile's channels, 4 V groups its rows:
-//     V = 4: 16 lanes x 16 groups of 8 rows, loads of 8 bytes (half types)
-//     V = 1: 64 lanes x  4 groups of 32 rows, for rows without alignment
+// neighbouring channels of L consecutive rows in registers, as stored (half
+// types stay packed, so more rows are in flight per register); the threads of
+// a row group cover the tile's channels, the row groups its rows.
 // A decay of exactly zero forgets the state, whatever it held (inf and NaN
 // too): 0 * h is never formed.  The first row of a sequence is such a row,
 // with a h0 added to x, so one form serves packed and single sequences.
@@ -20,13 +19,11 @@
 
 namespace lx {
 
-constexpr int kRecurThreads = 256;
-
-template <int V>
+template <int V, int L>
 struct RecurLayout {
-    static constexpr int kLanes = kRecurCols / V;               // threads per row
-    static constexpr int kGroups = kRecurThreads / kLanes;      // row groups
-    static constexpr int kRows = kRecurTile / kGroups;          // rows per thread
+    static constexpr int kLanes = kRecurCols / V;         // threads per row
+    static constexpr int kGroups = kRecurTile / L;        // row groups
+    static constexpr int kThreads = kLanes * kGroups;
 };
 
 // e^g by the hardware's base-2 exponential (1 ulp), which flushes results
@@ -47,7 +44,6 @@ __device__ __forceinline__ float step_of(float a, float h, float x) { return a =
 struct RecurRows {
     int start[kRecurTile];  // sequence whose first row this is; -1: none; -2: a row of no sequence
     int last[kRecurTile];   // sequence whose last row this is; -1: none
-    int any;                // whether any row is special
 };
 
 // Index of the first of n values that is not below `key` (values ascend),
@@ -70,12 +66,22 @@ __device__ __forceinline__ int64_t lower_bound64(const int32_t* v, int64_t n, in
     return lo;
 }
 
-// Fills R for the tile of rows [t0, t0 + kRecurTile).  All threads; ends
-// with a barrier.
-__device__ __forceinline__ void recur_rows(const RecurArgs& A, int64_t t0, RecurRows& R)
+// Whether the tile of rows [t0, t0 + kRecurTile) has special rows; then R
+// says which.  All threads; has barriers only if it returns true.
+template <int THREADS>
+__device__ __forceinline__ bool recur_rows(const RecurArgs& A, int64_t t0, RecurRows& R)
 {
+    static_assert(THREADS >= kRecurTile, "a thread per row");
+    const int64_t end = t0 + kRecurTile;
+    int64_t q_first = 0;  // packed: first offset at or past t0
+    if (A.offsets) {
+        q_first = lower_bound64(A.offsets, A.seqs + 1, t0);  // the same in every wave
+        if (end <= A.n && q_first > 0 && q_first <= A.seqs && (int64_t)A.offsets[q_first] > end) return false;
+    } else {
+        const int64_t at = A.seqs == 1 ? t0 : t0 % A.seq_len;
+        if (end <= A.n && at != 0 && at + kRecurTile < A.seq_len) return false;
+    }
     const int tid = threadIdx.x;
-    if (tid == 0) R.any = 0;
     if (tid < kRecurTile) {
         const int64_t t = t0 + tid;
         int start = -1, last = -1;
@@ -93,10 +99,9 @@ __device__ __forceinline__ void recur_rows(const RecurArgs& A, int64_t t0, Recur
         R.last[tid] = last;
     }
     __syncthreads();
-    if (A.offsets && tid < kWave) {
-        // one wave: the offsets in [t0, t0 + kRecurTile], 64 at a time
-        const int64_t end = t0 + kRecurTile;
-        for (int64_t q0 = lower_bound64(A.offsets, A.seqs + 1, t0); q0 <= A.seqs; q0 += kWave) {
+    if (A.offsets) {
+        // one wave: the offsets in [t0, end], 64 at a time
+        for (int64_t q0 = q_first; tid < kWave && q0 <= A.seqs; q0 += kWave) {
             const int64_t q = q0 + tid;
             const int64_t o = q <= A.seqs ? (int64_t)A.offsets[q] : end + 1;
             if (o >= t0 && o <= end) {
@@ -106,95 +111,272 @@ __device__ __forceinline__ void recur_rows(const RecurArgs& A, int64_t t0, Recur
             }
             if (__ballot(o > end)) break;
         }
+        __syncthreads();
     }
-    __syncthreads();
-    if (tid < kRecurTile && (R.start[tid] != -1 || R.last[tid] != -1)) R.any = 1;
-    __syncthreads();
+    return true;
 }
 
-// Raw rows of one array: L rows of V channels, zero outside.
-template <int V, int L, class T>
-__device__ __forceinline__ void load_rows(const void* base, int64_t ld, int64_t row0, int64_t n, int64_t col, bool in,
-                                          float (&out)[L][V])
-{
-    const T* p = (const T*)base + row0 * ld + col;
-    if (in && row0 + L <= n) {
+// L rows of V channels of one array as stored, in 32-bit words (a vector of
+// 16-bit values would be taken apart into a register for each); 0 outside.
+template <class T, int V, int L>
+struct RowPack {
+    static constexpr int kBytes = V * (int)sizeof(T);
+    static constexpr int kWords = (kBytes + 3) / 4;
+    uint32_t w[L][kWords];
+
+    __device__ __forceinline__ void load_row(int j, const T* p)
+    {
+        if constexpr (kBytes == 2) {
+            w[j][0] = *reinterpret_cast<const uint16_t*>(p);
+        } else {
+            const Pack<uint32_t, kWords> q = *reinterpret_cast<const Pack<uint32_t, kWords>*>(p);
 #pragma unroll
-        for (int j = 0; j < L; ++j) load_vec<V>(p + j * ld, out[j]);
-    } else {
+            for (int i = 0; i < kWords; ++i) w[j][i] = q.v[i];
+        }
+    }
+    __device__ __forceinline__ void load(const void* base, int64_t ld, int64_t row0, int64_t n, int64_t col, bool in)
+    {
+        const T* p = (const T*)base + row0 * ld + col;
+        if (in && row0 + L <= n) {
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
-            if (in && row0 + j < n) {
-                load_vec<V>(p + j * ld, out[j]);
-            } else {
+            for (int j = 0; j < L; ++j) load_row(j, p + j * ld);
+        } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v) out[j][v] = 0.f;
+            for (int j = 0; j < L; ++j) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) w[j][i] = 0;
+                if (in && row0 + j < n) load_row(j, p + j * ld);
             }
         }
     }
-}
-
-template <int V, int L, class T>
-__device__ __forceinline__ void store_rows(void* base, int64_t ld, int64_t row0, int64_t n, int64_t col, bool in,
-                                           const float (&val)[L][V])
-{
-    T* p = (T*)base + row0 * ld + col;
-    if (in && row0 + L <= n) {
+    // Makes the compiler forget what it has worked out from a row: a later
+    // use converts it again (and takes the exponentials again) instead of
+    // holding every result in registers in between.
+    __device__ __forceinline__ void forget(int j)
+    {
 #pragma unroll
-        for (int j = 0; j < L; ++j) store_vec<V>(p + j * ld, val[j]);
-    } else if (in) {
-#pragma unroll
-        for (int j = 0; j < L; ++j)
-            if (row0 + j < n) store_vec<V>(p + j * ld, val[j]);
+        for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[j][i]));
     }
+    __device__ __forceinline__ void get(int j, float (&out)[V]) const
+    {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if constexpr (sizeof(T) == 4) {
+                out[v] = __uint_as_float(w[j][v]);
+            } else {
+                const uint32_t q = w[j][v / 2];
+                if constexpr (__is_same(T, bf16_t)) {
+                    out[v] = __uint_as_float(v & 1 ? q & 0xFFFF0000u : q << 16);
+                } else {
+                    out[v] = (float)__builtin_bit_cast(f16_t, (uint16_t)(v & 1 ? q >> 16 : q));
+                }
+            }
+        }
+    }
+};
+
+// Has these values worked out here, not where they are used.
+template <int N>
+__device__ __forceinline__ void settle(float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
 }
 
-// A thread's rows of x and decays.  SH: one decay serves the V channels.
-template <class T, class TG, int V, bool SH>
+// A thread's rows of x and g.  SH: one decay serves the V channels.
+template <class T, class TG, int V, int LL, bool SH>
 struct RecurThread {
-    static constexpr int L = RecurLayout<V>::kRows;
+    static constexpr int L = LL;
     static constexpr int D = SH ? 1 : V;
-    float x[L][V], a[L][D];
+    RowPack<T, V, L> x;
+    RowPack<TG, D, L> g;
     int64_t row0, col;
     int r0, lane, group;  // first row within the tile, thread of the row, row group
     bool in;              // channels inside the width
 
     __device__ __forceinline__ void load(const RecurArgs& A, int64_t tile, int ct)
     {
-        lane = (int)threadIdx.x % RecurLayout<V>::kLanes;
-        group = (int)threadIdx.x / RecurLayout<V>::kLanes;
+        lane = (int)threadIdx.x % RecurLayout<V, L>::kLanes;
+        group = (int)threadIdx.x / RecurLayout<V, L>::kLanes;
         r0 = group * L;
         row0 = tile * kRecurTile + r0;
         col = (int64_t)ct * kRecurCols + lane * V;
         in = col < A.width;
-        load_rows<V, L, T>(A.x, A.ldx, row0, A.n, col, in, x);
-        load_rows<D, L, TG>(A.g, A.ldg, row0, A.n, SH ? col / A.per : col, in, a);
+        x.load(A.x, A.ldx, row0, A.n, col, in);
+        g.load(A.g, A.ldg, row0, A.n, SH ? col / A.per : col, in);
     }
-    __device__ __forceinline__ void decays()
+    // Row j: its decays and terms.  CARE: the tile has special rows or a
+    // decay of 0 (or too small for the plain exponential) may be among them:
+    // first rows take h0 in and forget what came before, rows of no
+    // sequence are 0.
+    template <bool CARE>
+    __device__ __forceinline__ void decays(const RecurRows* R, int j, float (&a)[D])
+    {
+        // one row at a time: all rows' converted values at once would take
+        // more registers than the rows themselves
+        x.forget(j);
+        g.forget(j);
+        g.get(j, a);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            a[d] = CARE ? decay_of(a[d]) : __builtin_amdgcn_exp2f(a[d] * 1.44269504088896341f);
+        if (CARE && R && R->start[r0 + j] != -1) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) a[d] = 0.f;
+        }
+    }
+    template <bool CARE>
+    __device__ __forceinline__ void terms(const RecurArgs& A, const RecurRows* R, int j, float (&t)[V])
+    {
+        x.get(j, t);
+        if (!CARE || !R) return;
+        const int q = R->start[r0 + j];
+        if (q == -2) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) t[v] = 0.f;
+        } else if (q >= 0 && A.h0 && in) {
+            float h[V], a[D];
+            load_vec<V>(A.h0 + (int64_t)q * A.width + col, h);
+            g.get(j, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) t[v] = step_of(decay_of(a[SH ? 0 : v]), h[v], t[v]);
+        }
+    }
+    // h -> a h + t for row j
+    template <bool CARE>
+    __device__ __forceinline__ void step(const RecurArgs& A, const RecurRows* R, int j, const float (&a)[D],
+                                         float (&h)[V])
+    {
+        float t[V];
+        terms<CARE>(A, R, j, t);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            h[v] = CARE ? step_of(a[SH ? 0 : v], h[v], t[v]) : fmaf(a[SH ? 0 : v], h[v], t[v]);
+        settle(h);
+    }
+    // Composed map of the thread's rows: h -> m h + H.
+    template <bool CARE>
+    __device__ __forceinline__ void compose(const RecurArgs& A, const RecurRows* R, float (&m)[D], float (&H)[V])
     {
 #pragma unroll
-        for (int j = 0; j < L; ++j)
+        for (int d = 0; d < D; ++d) m[d] = 1.f;
 #pragma unroll
-            for (int d = 0; d < D; ++d) a[j][d] = decay_of(a[j][d]);
-    }
-    // first rows of sequences take h0 in and forget what came before; rows of
-    // no sequence are 0
-    __device__ __forceinline__ void special(const RecurArgs& A, const RecurRows& R)
-    {
+        for (int v = 0; v < V; ++v) H[v] = 0.f;
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-            const int q = R.start[r0 + j];
-            if (q == -1) continue;
-            float h[V];
+            float a[D];
+            decays<CARE>(R, j, a);
+            step<CARE>(A, R, j, a, H);
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = 0.f;
-            if (q >= 0 && A.h0 && in) load_vec<V>(A.h0 + (int64_t)q * A.width + col, h);
-#pragma unroll
-            for (int v = 0; v < V; ++v) x[j][v] = q < 0 ? 0.f : step_of(a[j][SH ? 0 : v], h[v], x[j][v]);
-#pragma unroll
-            for (int d = 0; d < D; ++d) a[j][d] = 0.f;
+            for (int d = 0; d < D; ++d) m[d] *= a[d];
+            settle(m);
         }
     }
 };
+
+// Whether any of a wave's products of decays is 0: some decay may be.
+template <int D>
+__device__ __forceinline__ bool any_zero(const float (&m)[D])
+{
+    bool z = false;
+#pragma unroll
+    for (int d = 0; d < D; ++d) z |= m[d] == 0.f;
+    return __any(z);
+}
+
+// ---- between tiles -------------------------------------------------------
+//
+// One pass over the data: a workgroup takes the next tile of the pass
+// (ticket order, so the tiles before it have been taken too and their
+// workgroups run), composes its rows' maps, publishes the tile's map
+// h -> A h + H, finds the state that enters it and publishes the state that
+// leaves it.  Words say by themselves whether they have been written: all
+// ones, a NaN that is never stored (NaNs are stored as 0x7fc00000), means
+// not yet.  They are moved by relaxed agent-scope atomics, which bypass the
+// per-die caches, and nothing else is read across workgroups.
+//
+// The entering state is the last published state before the tile, carried
+// on through the published maps of the tiles between, in row order: the
+// very operations by which those tiles make their own states, so the result
+// does not depend on where a look-back finds a state.
+constexpr uint64_t kNoMap = ~(uint64_t)0;
+constexpr uint32_t kNoState = ~(uint32_t)0;
+
+__device__ __forceinline__ uint32_t state_bits(float h) { return h == h ? __float_as_uint(h) : 0x7fc00000u; }
+__device__ __forceinline__ uint64_t map_bits(float a, float h)
+{
+    return (uint64_t)state_bits(h) << 32 | __float_as_uint(a);
+}
+
+// State entering `tile` (> 0) for this lane's channel; maps and states point
+// at the channel's words of tile 0, ld words between tiles.  All 64 lanes.
+__device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t* states, int64_t ld, int64_t tile)
+{
+    constexpr int W = 4;  // tiles read at once
+    int64_t from = tile - W, known = -1;
+    float h = 0.f;
+    for (;;) {
+        const int64_t w0 = known >= 0 ? known + 1 : (from > 0 ? from : 0);
+        uint32_t s[W];
+        uint64_t m[W];
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+            s[q] = kNoState;
+            m[q] = kNoMap;
+            if (w0 + q < tile) {
+                s[q] = ld_agent(states + (w0 + q) * ld);
+                m[q] = ld_agent(maps + (w0 + q) * ld);
+            }
+        }
+        const int64_t before = known;
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+            if (__all(s[q] != kNoState)) {
+                known = w0 + q;
+                h = __uint_as_float(s[q]);
+            } else if (known >= 0 && known == w0 + q - 1 && __all(m[q] != kNoMap)) {
+                known = w0 + q;
+                h = step_of(__uint_as_float((uint32_t)m[q]), h, __uint_as_float((uint32_t)(m[q] >> 32)));
+            }
+        }
+        if (known == tile - 1) return h;
+        if (known == before) {
+            if (known < 0 && w0 > 0) from = w0 - W;  // nothing here yet: further back
+            else __builtin_amdgcn_s_sleep(1);
+        }
+    }
+}
+
+// The tile's map (a, h) of this lane's channel -> the state entering it.
+// `fresh`: nothing enters (its first row starts a sequence or has none);
+// `last`: no tile follows.  One whole wave.
+__device__ __forceinline__ float pass_state(const RecurArgs& A, int64_t tile, int ct, float a, float h, bool fresh,
+                                            bool last)
+{
+    const int64_t ld = (int64_t)A.cols * kRecurCols;
+    const int64_t c = (int64_t)ct * kRecurCols + lane_id();
+    const bool cut = __all(a == 0.f);  // the leaving state does not depend on the entering one
+    if (!last) {
+        if (cut) st_agent(A.states + tile * ld + c, state_bits(h));
+        else st_agent(A.maps + tile * ld + c, map_bits(a, h));
+    }
+    float in = 0.f;
+    if (!fresh && tile > 0) in = look_back(A.maps + c, A.states + c, ld, tile);
+    if (!last && !cut) st_agent(A.states + tile * ld + c, state_bits(step_of(a, in, h)));
+    return in;
+}
+
+// The next tile of the pass.  All threads; has a barrier.
+__device__ __forceinline__ uint32_t next_tile(uint32_t* ticket)
+{
+    __shared__ uint32_t s_ticket;
+    if (threadIdx.x == 0) s_ticket = atomicAdd(ticket, 1u);
+    __syncthreads();
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)s_ticket);
+}
+
+// Clears what a pass publishes (with more than one tile) and gives sequences
+// without rows their result: to[q] = from[q], or 0 without `from`.
+hipError_t recur_begin(const RecurArgs& a, const float* from, float* to, hipStream_t s);
 
 }  // namespace lx

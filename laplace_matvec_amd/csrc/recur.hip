@@ -1,45 +1,53 @@
 // Gated linear recurrence over packed sequences (gfx950): see lx_recur.h for
-// the mathematics and the tile layout.
+// the mathematics, the tile layout and how tiles hand their states on.
 //
-// Reduce-then-scan: every tile's composed map, then the states between tiles
-// (one thread per channel), then every tile's rows from its entering state.
-// No workgroup waits for another and the combine order is fixed, so results
-// repeat bit for bit.
+// One pass: x and g are read once and y is written once.
 #include "lx_recur.h"
 
 namespace lx {
 
 namespace {
 
-// Composes the row groups of a tile.  In: this thread's map, h -> A h + H
-// over its rows.  LDS: sa[groups][kRecurCols / V * D], sh[groups][kRecurCols].
-template <class T, class TG, int V, bool SH>
-__global__ __launch_bounds__(kRecurThreads) void lx_recur_reduce(RecurArgs A)
+// Rows of y (and final states) of one thread from the state entering it.
+template <bool CARE, class Th, class T, int V>
+__device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* R, Th& th, float (&h)[V])
 {
-    using Th = RecurThread<T, TG, V, SH>;
-    using Lay = RecurLayout<V>;
-    __shared__ RecurRows R;
-    __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
-    __shared__ float sh[Lay::kGroups][kRecurCols];
-    const int64_t tile = blockIdx.x / (unsigned)A.cols;
-    const int ct = (int)(blockIdx.x % (unsigned)A.cols);
-    Th th;
-    th.load(A, tile, ct);
-    recur_rows(A, tile * kRecurTile, R);
-    th.decays();
-    if (R.any) th.special(A, R);
-    float m[Th::D], h[V];
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) m[d] = 1.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.f;
+    T* p = (T*)A.y + th.row0 * A.ldy + th.col;
+    const bool whole = th.row0 + Th::L <= A.n;
 #pragma unroll
     for (int j = 0; j < Th::L; ++j) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = step_of(th.a[j][SH ? 0 : v], h[v], th.x[j][v]);
-#pragma unroll
-        for (int d = 0; d < Th::D; ++d) m[d] *= th.a[j][d];
+        float a[Th::D];
+        th.template decays<CARE>(R, j, a);
+        th.template step<CARE>(A, R, j, a, h);
+        if (th.in && (whole || th.row0 + j < A.n)) store_vec<V>(p + j * A.ldy, h);
+        if (CARE && R && A.final && th.in) {
+            const int q = R->last[th.r0 + j];
+            if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col, h);
+        }
     }
+}
+
+template <class T, class TG, int V, int L, bool SH>
+__global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(RecurArgs A)
+{
+    using Th = RecurThread<T, TG, V, L, SH>;
+    using Lay = RecurLayout<V, L>;
+    __shared__ RecurRows rows;
+    __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
+    __shared__ float sh[Lay::kGroups][kRecurCols];
+    const uint32_t turn = A.tiles > 1 ? next_tile(A.ticket) : blockIdx.x;
+    const int64_t tile = turn / (uint32_t)A.cols;
+    const int ct = (int)(turn % (uint32_t)A.cols);
+    Th th;
+    th.load(A, tile, ct);
+    const RecurRows* R = recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows) ? &rows : nullptr;
+    float m[Th::D], h[V];
+    bool care = R != nullptr;
+    if (!care) {
+        th.template compose<false>(A, R, m, h);
+        care = any_zero(m);
+    }
+    if (care) th.template compose<true>(A, R, m, h);
 #pragma unroll
     for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
 #pragma unroll
@@ -54,70 +62,8 @@ __global__ __launch_bounds__(kRecurThreads) void lx_recur_reduce(RecurArgs A)
             ah = step_of(a, ah, sh[i][c]);
             am *= a;
         }
-        A.maps[(tile * A.cols + ct) * kRecurCols + c] = make_float2(am, ah);
-    }
-}
-
-// states[t] = state after tile t (in the order of the pass): one thread per channel.
-__global__ __launch_bounds__(kRecurCols) void lx_recur_carry(RecurArgs A)
-{
-    const int64_t ld = (int64_t)A.cols * kRecurCols;
-    const int64_t c = (int64_t)blockIdx.x * kRecurCols + threadIdx.x;
-    float h = 0.f;
-    int64_t t = 0;
-    constexpr int U = 16;
-    for (; t + U < A.tiles; t += U) {
-        float2 m[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) m[i] = A.maps[(t + i) * ld + c];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            h = step_of(m[i].x, h, m[i].y);
-            A.states[(t + i) * ld + c] = h;
-        }
-    }
-    for (; t < A.tiles - 1; ++t) {
-        const float2 m = A.maps[t * ld + c];
-        h = step_of(m.x, h, m.y);
-        A.states[t * ld + c] = h;
-    }
-}
-
-template <class T, class TG, int V, bool SH>
-__global__ __launch_bounds__(kRecurThreads) void lx_recur_apply(RecurArgs A)
-{
-    using Th = RecurThread<T, TG, V, SH>;
-    using Lay = RecurLayout<V>;
-    __shared__ RecurRows R;
-    __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
-    __shared__ float sh[Lay::kGroups][kRecurCols];
-    const int64_t tile = blockIdx.x / (unsigned)A.cols;
-    const int ct = (int)(blockIdx.x % (unsigned)A.cols);
-    Th th;
-    th.load(A, tile, ct);
-    recur_rows(A, tile * kRecurTile, R);
-    th.decays();
-    if (R.any) th.special(A, R);
-    float m[Th::D], h[V];
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) m[d] = 1.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.f;
-#pragma unroll
-    for (int j = 0; j < Th::L; ++j) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = step_of(th.a[j][SH ? 0 : v], h[v], th.x[j][v]);
-#pragma unroll
-        for (int d = 0; d < Th::D; ++d) m[d] *= th.a[j][d];
-    }
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
-#pragma unroll
-    for (int v = 0; v < V; ++v) sh[th.group][th.lane * V + v] = h[v];
-    __syncthreads();
-    if (threadIdx.x < kRecurCols) {
-        const int c = threadIdx.x;
-        float e = tile > 0 ? A.states[((tile - 1) * A.cols + ct) * kRecurCols + c] : 0.f;
+        float e = 0.f;
+        if (A.tiles > 1) e = pass_state(A, tile, ct, am, ah, R && R->start[0] != -1, tile == A.tiles - 1);
 #pragma unroll
         for (int i = 0; i < Lay::kGroups; ++i) {
             const float next = step_of(sa[i][SH ? c / V : c], e, sh[i][c]);
@@ -128,38 +74,34 @@ __global__ __launch_bounds__(kRecurThreads) void lx_recur_apply(RecurArgs A)
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = sh[th.group][th.lane * V + v];
-#pragma unroll
-    for (int j = 0; j < Th::L; ++j) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) th.x[j][v] = h[v] = step_of(th.a[j][SH ? 0 : v], h[v], th.x[j][v]);
-    }
-    store_rows<V, Th::L, T>(A.y, A.ldy, th.row0, A.n, th.col, th.in, th.x);
-    if (R.any && A.final && th.in) {
-#pragma unroll
-        for (int j = 0; j < Th::L; ++j) {
-            const int q = R.last[th.r0 + j];
-            if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col, th.x[j]);
-        }
-    }
+    if (care) write_rows<true, Th, T>(A, R, th, h);
+    else write_rows<false, Th, T>(A, R, th, h);
 }
 
-__global__ __launch_bounds__(256) void lx_recur_empty(RecurArgs A, const float* __restrict__ from, float* __restrict__ to)
+// Blocks [0, fill): 16 bytes of all ones per thread over the published
+// words; the rest: one sequence each.
+__global__ __launch_bounds__(256) void lx_recur_begin(RecurArgs A, int64_t maps16, int64_t states16, unsigned fill,
+                                                      const float* __restrict__ from, float* __restrict__ to)
 {
-    const int64_t q = blockIdx.x;
+    if (blockIdx.x < fill) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        const uint4 ones = make_uint4(~0u, ~0u, ~0u, ~0u);
+        if (i < maps16) reinterpret_cast<uint4*>(A.maps)[i] = ones;
+        else if (i - maps16 < states16) reinterpret_cast<uint4*>(A.states)[i - maps16] = ones;
+        if (i == 0) *A.ticket = 0;
+        return;
+    }
+    const int64_t q = blockIdx.x - fill;
     if (A.offsets && A.offsets[q + 1] > A.offsets[q]) return;
     for (int c = threadIdx.x; c < A.width; c += 256) to[q * A.width + c] = from ? from[q * A.width + c] : 0.f;
 }
 
-template <class T, class TG, int V, bool SH>
+template <class T, class TG, int V, int L, bool SH>
 hipError_t recur_go(const RecurArgs& a, hipStream_t s)
 {
-    const unsigned blocks = (unsigned)(a.tiles * a.cols);
-    if (a.tiles > 1) {
-        const unsigned part = (unsigned)((a.tiles - 1) * a.cols);
-        LX_LAUNCH("recur_reduce", s, (lx_recur_reduce<T, TG, V, SH><<<part, kRecurThreads, 0, s>>>(a)));
-        LX_LAUNCH("recur_carry", s, (lx_recur_carry<<<(unsigned)a.cols, kRecurCols, 0, s>>>(a)));
-    }
-    LX_LAUNCH("recur", s, (lx_recur_apply<T, TG, V, SH><<<blocks, kRecurThreads, 0, s>>>(a)));
+    LX_LAUNCH("recur", s,
+              (lx_recur_pass<T, TG, V, L, SH>
+               <<<(unsigned)(a.tiles * a.cols), RecurLayout<V, L>::kThreads, 0, s>>>(a)));
     return hipSuccess;
 }
 
@@ -172,8 +114,8 @@ hipError_t recur_type(const RecurArgs& a, hipStream_t s)
     const bool wide = vec_ok(a.x, a.ldx, a.width, sizeof(T), 4) && vec_ok(a.y, a.ldy, a.width, sizeof(T), 4) &&
                       vec_ok(a.h0, a.width, a.width, 4, 4) && vec_ok(a.final, a.width, a.width, 4, 4) &&
                       (sh ? a.per % 4 == 0 : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4));
-    if (wide) return sh ? recur_go<T, TG, 4, true>(a, s) : recur_go<T, TG, 4, false>(a, s);
-    return recur_go<T, TG, 1, true>(a, s);
+    if (wide) return sh ? recur_go<T, TG, 4, 16, true>(a, s) : recur_go<T, TG, 4, 16, false>(a, s);
+    return recur_go<T, TG, 1, 32, true>(a, s);
 }
 
 // One token for each request: state[slot] = e^g state[slot] + x, y = the new state.
@@ -233,15 +175,14 @@ hipError_t step_type(RecurStepArgs a, hipStream_t s)
 
 }  // namespace
 
-hipError_t recur_carry_launch(const RecurArgs& a, hipStream_t s)
+hipError_t recur_begin(const RecurArgs& a, const float* from, float* to, hipStream_t s)
 {
-    LX_LAUNCH("recur_carry", s, (lx_recur_carry<<<(unsigned)a.cols, kRecurCols, 0, s>>>(a)));
-    return hipSuccess;
-}
-
-hipError_t recur_empty_launch(const RecurArgs& a, const float* from, float* to, hipStream_t s)
-{
-    LX_LAUNCH("recur_empty", s, (lx_recur_empty<<<(unsigned)a.seqs, 256, 0, s>>>(a, from, to)));
+    const int64_t words = a.tiles > 1 ? (a.tiles - 1) * a.cols * kRecurCols : 0;
+    const int64_t maps16 = words / 2, states16 = words / 4;
+    const unsigned fill = (unsigned)((maps16 + states16 + 255) / 256);
+    const unsigned each = to && (a.offsets || a.n == 0) ? (unsigned)a.seqs : 0;
+    if (fill + each > 0)
+        LX_LAUNCH("recur_begin", s, (lx_recur_begin<<<fill + each, 256, 0, s>>>(a, maps16, states16, fill, from, to)));
     return hipSuccess;
 }
 
@@ -255,6 +196,8 @@ hipError_t recur_empty_launch(const RecurArgs& a, const float* from, float* to, 
 
 hipError_t recur_launch(const RecurArgs& a, int dtype, int gtype, hipStream_t s)
 {
+    const hipError_t e = recur_begin(a, a.h0, a.final, s);
+    if (e != hipSuccess || a.n == 0) return e;
     LX_BY_TYPE(recur_type, a)
 }
 

@@ -13,131 +13,162 @@
 
 namespace lx {
 
-hipError_t recur_carry_launch(const RecurArgs& a, hipStream_t s);
-
 namespace {
 
-// dy plus dfinal on last rows; 0 on rows of no sequence.
-template <class Th, int V>
-__device__ __forceinline__ void special_dy(const RecurArgs& A, const RecurRows& R, const Th& th, float (&dy)[Th::L][V])
+// dy of row j, plus dfinal on a last row; 0 on a row of no sequence.
+template <bool CARE, class Th, class T, int V>
+__device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, Th& th,
+                                       RowPack<T, V, Th::L>& dy, int j, float (&d)[V])
 {
+    dy.forget(j);
+    dy.get(j, d);
+    if (!CARE || !R) return;
+    if (R->start[th.r0 + j] == -2) {
 #pragma unroll
-    for (int j = 0; j < Th::L; ++j) {
-        if (R.start[th.r0 + j] == -2) {
+        for (int v = 0; v < V; ++v) d[v] = 0.f;
+    }
+    const int q = R->last[th.r0 + j];
+    if (q >= 0 && A.dfinal && th.in) {
+        float f[V];
+        load_vec<V>(A.dfinal + (int64_t)q * A.width + th.col, f);
 #pragma unroll
-            for (int v = 0; v < V; ++v) dy[j][v] = 0.f;
-        }
-        const int q = R.last[th.r0 + j];
-        if (q >= 0 && A.dfinal && th.in) {
-            float d[V];
-            load_vec<V>(A.dfinal + (int64_t)q * A.width + th.col, d);
-#pragma unroll
-            for (int v = 0; v < V; ++v) dy[j][v] += d[v];
-        }
+        for (int v = 0; v < V; ++v) d[v] += f[v];
     }
 }
 
-// The first row of a sequence passes nothing to the row before it; rows
-// of no sequence have no decay.
-template <class T, class TG, int V, bool SH>
-__global__ __launch_bounds__(kRecurThreads) void lx_recur_grad_reduce(RecurArgs A)
+// Gradient of the thread's rows towards the row before them, from none
+// after them (their map is w -> m w + W, m as in the forward direction).
+// The first row of a sequence passes nothing on.
+template <bool CARE, class Th, class T, int V>
+__device__ __forceinline__ void compose_grad(const RecurArgs& A, const RecurRows* R, Th& th,
+                                             RowPack<T, V, Th::L>& dy, float (&w)[V])
 {
-    using Th = RecurThread<T, TG, V, SH>;
-    using Lay = RecurLayout<V>;
-    __shared__ RecurRows R;
-    __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
-    __shared__ float sw[Lay::kGroups][kRecurCols];
-    const int64_t back = blockIdx.x / (unsigned)A.cols;  // tiles before this one in the pass
-    const int64_t tile = A.tiles - 1 - back;
-    const int ct = (int)(blockIdx.x % (unsigned)A.cols);
-    Th th;
-    th.load(A, tile, ct);
-    load_rows<V, Th::L, T>(A.dy, A.lddy, th.row0, A.n, th.col, th.in, th.x);
-    recur_rows(A, tile * kRecurTile, R);
-    th.decays();
-    if (R.any) {
-        special_dy<Th, V>(A, R, th, th.x);
-#pragma unroll
-        for (int j = 0; j < Th::L; ++j)
-            if (R.start[th.r0 + j] != -1)
-#pragma unroll
-                for (int d = 0; d < Th::D; ++d) th.a[j][d] = 0.f;
-    }
-    float m[Th::D], w[V];
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) m[d] = 1.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) w[v] = 0.f;
 #pragma unroll
     for (int j = Th::L - 1; j >= 0; --j) {
+        float a[Th::D], d[V];
+        th.template decays<CARE>(R, j, a);
+        row_dy<CARE, Th, T, V>(A, R, th, dy, j, d);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float a = th.a[j][SH ? 0 : v];
-            w[v] = a == 0.f ? 0.f : a * (th.x[j][v] + w[v]);
+            const float av = a[Th::D == 1 ? 0 : v];
+            w[v] = CARE && av == 0.f ? 0.f : av * (d[v] + w[v]);
         }
-#pragma unroll
-        for (int d = 0; d < Th::D; ++d) m[d] *= th.a[j][d];
-    }
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
-#pragma unroll
-    for (int v = 0; v < V; ++v) sw[th.group][th.lane * V + v] = w[v];
-    __syncthreads();
-    if (threadIdx.x < kRecurCols) {
-        const int c = threadIdx.x;
-        float am = 1.f, aw = 0.f;
-#pragma unroll
-        for (int i = Lay::kGroups - 1; i >= 0; --i) {
-            const float a = sa[i][SH ? c / V : c];
-            aw = step_of(a, aw, sw[i][c]);
-            am *= a;
-        }
-        A.maps[(back * A.cols + ct) * kRecurCols + c] = make_float2(am, aw);
+        settle(w);
     }
 }
 
-template <class T, class TG, int V, bool SH>
-__global__ __launch_bounds__(kRecurThreads) void lx_recur_grad_apply(RecurArgs A)
+// dx, dg and dh0 of the thread's rows from the state h entering them and the
+// gradient w from the rows after them.
+template <bool CARE, class T, class TG, int V, int L, bool SH>
+__device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows* R,
+                                            RecurThread<T, TG, V, L, SH>& th, RowPack<T, V, L>& dy,
+                                            int ct, float (&h)[V], float (&w)[V])
 {
-    using Th = RecurThread<T, TG, V, SH>;
-    using Lay = RecurLayout<V>;
-    constexpr int L = Th::L;
-    __shared__ RecurRows R;
+    using Th = RecurThread<T, TG, V, L, SH>;
+    constexpr int D = Th::D, kLanes = RecurLayout<V, L>::kLanes;
+    float before[L][V];  // state before each row
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        float a[D];
+        th.template decays<CARE>(R, j, a);
+#pragma unroll
+        for (int v = 0; v < V; ++v) before[j][v] = h[v];
+        th.template step<CARE>(A, R, j, a, h);
+    }
+    const bool whole = th.row0 + L <= A.n;
+    const bool own = !SH || A.per == 1;  // a decay for each channel
+    // channels of one decay are neighbouring lanes of a row; the first of
+    // them gets their sum
+    const int head = th.in ? (int)(th.col / A.per) : -1;
+    const bool first = th.in && (th.lane == 0 || (int)((th.col - V) / A.per) != head);
+    const bool inside = recur_heads_inside(A.width, A.per);
+#pragma unroll
+    for (int j = L - 1; j >= 0; --j) {
+        const int64_t row = th.row0 + j;
+        const bool here = th.in && (whole || row < A.n);
+        float a[D], u[V], p[V];
+        th.template decays<CARE>(R, j, a);
+        row_dy<CARE, Th, T, V>(A, R, th, dy, j, u);
+        const int q = CARE && R ? R->start[th.r0 + j] : -1;
+        if (q >= 0) {
+            // the decay of a first row acts on h0 alone
+            float g[D], h0[V], out[V];
+            th.g.get(j, g);
+#pragma unroll
+            for (int v = 0; v < V; ++v) h0[v] = 0.f;
+            if (A.h0 && th.in) load_vec<V>(A.h0 + (int64_t)q * A.width + th.col, h0);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float av = decay_of(g[SH ? 0 : v]);
+                u[v] += w[v];
+                out[v] = av == 0.f ? 0.f : av * u[v];
+                p[v] = av == 0.f ? 0.f : out[v] * h0[v];
+                w[v] = 0.f;
+            }
+            if (A.dh0 && th.in) store_vec<V>(A.dh0 + (int64_t)q * A.width + th.col, out);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float av = a[SH ? 0 : v];
+                u[v] += w[v];
+                w[v] = CARE && av == 0.f ? 0.f : av * u[v];
+                p[v] = CARE && av == 0.f ? 0.f : w[v] * before[j][v];
+            }
+        }
+        settle(w);
+        if (A.dx && here) store_vec<V>((T*)A.dx + row * A.lddx + th.col, u);
+        if (!A.dg) continue;
+        if (own) {
+            if (here) store_vec<V>((TG*)A.dg + row * A.lddg + th.col, p);
+            continue;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum += p[v];
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) {
+            const float o = __shfl_down(sum, d, kLanes);
+            const int oh = __shfl_down(head, d, kLanes);
+            if (th.lane + d < kLanes && oh == head) sum += o;
+        }
+        if (first && here) {
+            if (inside) ((TG*)A.dg)[row * A.lddg + head] = (TG)sum;
+            else A.part[row * (A.cols + A.heads) + ct + head] = sum;
+        }
+    }
+}
+
+template <class T, class TG, int V, int L, bool SH>
+__global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_pass(RecurArgs A)
+{
+    using Th = RecurThread<T, TG, V, L, SH>;
+    using Lay = RecurLayout<V, L>;
+    __shared__ RecurRows rows;
     __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
     __shared__ float sh[Lay::kGroups][kRecurCols];
     __shared__ float sw[Lay::kGroups][kRecurCols];
-    const int64_t back = blockIdx.x / (unsigned)A.cols;
+    const uint32_t turn = A.tiles > 1 ? next_tile(A.ticket) : blockIdx.x;
+    const int64_t back = turn / (uint32_t)A.cols;  // tiles before this one in the pass: from the last rows on
     const int64_t tile = A.tiles - 1 - back;
-    const int ct = (int)(blockIdx.x % (unsigned)A.cols);
+    const int ct = (int)(turn % (uint32_t)A.cols);
     Th th;
-    float dy[L][V];
+    RowPack<T, V, L> dy;
     th.load(A, tile, ct);
-    load_rows<V, L, T>(A.dy, A.lddy, th.row0, A.n, th.col, th.in, dy);
-    recur_rows(A, tile * kRecurTile, R);
-    th.decays();
-    if (R.any) {
-        special_dy<Th, V>(A, R, th, dy);
-        th.special(A, R);
-    }
+    dy.load(A.dy, A.lddy, th.row0, A.n, th.col, th.in);
+    const RecurRows* R = recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows) ? &rows : nullptr;
     float m[Th::D], h[V], w[V];
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) m[d] = 1.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = w[v] = 0.f;
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = step_of(th.a[j][SH ? 0 : v], h[v], th.x[j][v]);
-#pragma unroll
-        for (int d = 0; d < Th::D; ++d) m[d] *= th.a[j][d];
+    bool care = R != nullptr;
+    if (!care) {
+        th.template compose<false>(A, R, m, h);
+        compose_grad<false, Th, T, V>(A, R, th, dy, w);
+        care = any_zero(m);
     }
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float a = th.a[j][SH ? 0 : v];
-            w[v] = a == 0.f ? 0.f : a * (dy[j][v] + w[v]);
-        }
+    if (care) {
+        th.template compose<true>(A, R, m, h);
+        compose_grad<true, Th, T, V>(A, R, th, dy, w);
+    }
 #pragma unroll
     for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
 #pragma unroll
@@ -155,7 +186,17 @@ __global__ __launch_bounds__(kRecurThreads) void lx_recur_grad_apply(RecurArgs A
             sh[i][c] = e;  // state entering group i
             e = next;
         }
-        float b = back > 0 ? A.states[((back - 1) * A.cols + ct) * kRecurCols + c] : 0.f;
+        float am = 1.f, aw = 0.f;
+#pragma unroll
+        for (int i = Lay::kGroups - 1; i >= 0; --i) {
+            const float a = sa[i][SH ? c / V : c];
+            aw = step_of(a, aw, sw[i][c]);
+            am *= a;
+        }
+        // nothing comes back into a tile whose last row ends a sequence or has none
+        const bool fresh = R && (R->last[kRecurTile - 1] != -1 || R->start[kRecurTile - 1] == -2);
+        float b = 0.f;
+        if (A.tiles > 1) b = pass_state(A, back, ct, am, aw, fresh, back == A.tiles - 1);
 #pragma unroll
         for (int i = Lay::kGroups - 1; i >= 0; --i) {
             const float next = step_of(sa[i][SH ? c / V : c], b, sw[i][c]);
@@ -169,81 +210,8 @@ __global__ __launch_bounds__(kRecurThreads) void lx_recur_grad_apply(RecurArgs A
         h[v] = sh[th.group][th.lane * V + v];
         w[v] = sw[th.group][th.lane * V + v];
     }
-    // x[j] becomes the state before row j
-#pragma unroll
-    for (int j = 0; j < L; ++j)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float before = h[v];
-            h[v] = step_of(th.a[j][SH ? 0 : v], h[v], th.x[j][v]);
-            th.x[j][v] = before;
-        }
-    // dy[j] becomes u = dx, x[j] the products w h of dg
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j) {
-        const int q = R.any ? R.start[th.r0 + j] : -1;
-        if (q >= 0) {
-            // the decay of a first row acts on h0 alone
-            float g[Th::D], h0[V];
-#pragma unroll
-            for (int d = 0; d < Th::D; ++d) g[d] = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) h0[v] = 0.f;
-            if (th.in)
-                load_vec<Th::D>((const TG*)A.g + (th.row0 + j) * A.ldg + (SH ? th.col / A.per : th.col), g);
-            if (A.h0 && th.in) load_vec<V>(A.h0 + (int64_t)q * A.width + th.col, h0);
-            float out[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float a = decay_of(g[SH ? 0 : v]);
-                const float u = dy[j][v] + w[v];
-                out[v] = a == 0.f ? 0.f : a * u;
-                dy[j][v] = u;
-                th.x[j][v] = a == 0.f ? 0.f : out[v] * h0[v];
-                w[v] = 0.f;
-            }
-            if (A.dh0 && th.in) store_vec<V>(A.dh0 + (int64_t)q * A.width + th.col, out);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float a = th.a[j][SH ? 0 : v];
-                const float u = dy[j][v] + w[v];
-                w[v] = a == 0.f ? 0.f : a * u;
-                dy[j][v] = u;
-                th.x[j][v] = a == 0.f ? 0.f : w[v] * th.x[j][v];
-            }
-        }
-    }
-    if (A.dx) store_rows<V, L, T>(A.dx, A.lddx, th.row0, A.n, th.col, th.in, dy);
-    if (!A.dg) return;
-    if (!SH || A.per == 1) {
-        store_rows<V, L, TG>(A.dg, A.lddg, th.row0, A.n, th.col, th.in, th.x);
-        return;
-    }
-    // sum over the channels of each decay within this tile: the lanes of a
-    // row that share one are neighbours; the first of them gets the sum
-    const int head = th.in ? (int)(th.col / A.per) : -1;
-    const bool first = th.in && (th.lane == 0 || (int)((th.col - V) / A.per) != head);
-    const bool inside = recur_heads_inside(A.width, A.per);
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        float sum = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) sum += th.x[j][v];
-#pragma unroll
-        for (int d = 1; d < Lay::kLanes; d <<= 1) {
-            const float o = __shfl_down(sum, d, Lay::kLanes);
-            const int oh = __shfl_down(head, d, Lay::kLanes);
-            if (th.lane + d < Lay::kLanes && oh == head) sum += o;
-        }
-        const int64_t row = th.row0 + j;
-        if (first && row < A.n) {
-            if (inside)
-                ((TG*)A.dg)[row * A.lddg + head] = (TG)sum;
-            else
-                A.part[row * (A.cols + A.heads) + ct + head] = sum;
-        }
-    }
+    if (care) write_grads<true>(A, R, th, dy, ct, h, w);
+    else write_grads<false>(A, R, th, dy, ct, h, w);
 }
 
 // Sums of decays whose channels span several channel tiles: a tile and a
@@ -264,17 +232,12 @@ __global__ __launch_bounds__(256) void lx_recur_grad_heads(RecurArgs A)
     ((TG*)A.dg)[row * A.lddg + head] = (TG)sum;
 }
 
-template <class T, class TG, int V, bool SH>
+template <class T, class TG, int V, int L, bool SH>
 hipError_t grad_go(const RecurArgs& a, hipStream_t s)
 {
-    const unsigned blocks = (unsigned)(a.tiles * a.cols);
-    if (a.tiles > 1) {
-        const unsigned part = (unsigned)((a.tiles - 1) * a.cols);
-        LX_LAUNCH("recur_grad_reduce", s, (lx_recur_grad_reduce<T, TG, V, SH><<<part, kRecurThreads, 0, s>>>(a)));
-        const hipError_t e = recur_carry_launch(a, s);
-        if (e != hipSuccess) return e;
-    }
-    LX_LAUNCH("recur_grad", s, (lx_recur_grad_apply<T, TG, V, SH><<<blocks, kRecurThreads, 0, s>>>(a)));
+    LX_LAUNCH("recur_grad", s,
+              (lx_recur_grad_pass<T, TG, V, L, SH>
+               <<<(unsigned)(a.tiles * a.cols), RecurLayout<V, L>::kThreads, 0, s>>>(a)));
     if (a.dg && a.per > 1 && !recur_heads_inside(a.width, a.per))
         LX_LAUNCH("recur_grad_heads", s,
                   (lx_recur_grad_heads<TG><<<(unsigned)((a.n * a.heads + 255) / 256), 256, 0, s>>>(a)));
@@ -290,14 +253,16 @@ hipError_t grad_type(const RecurArgs& a, hipStream_t s)
                       vec_ok(a.dfinal, a.width, a.width, 4, 4) && vec_ok(a.dh0, a.width, a.width, 4, 4) &&
                       (sh ? a.per % 4 == 0
                           : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4) && vec_ok(a.dg, a.lddg, a.width, sizeof(TG), 4));
-    if (wide) return sh ? grad_go<T, TG, 4, true>(a, s) : grad_go<T, TG, 4, false>(a, s);
-    return grad_go<T, TG, 1, true>(a, s);
+    if (wide) return sh ? grad_go<T, TG, 4, 8, true>(a, s) : grad_go<T, TG, 4, 8, false>(a, s);
+    return grad_go<T, TG, 1, 32, true>(a, s);
 }
 
 }  // namespace
 
 hipError_t recur_grad_launch(const RecurArgs& a, int dtype, int gtype, hipStream_t s)
 {
+    const hipError_t e = recur_begin(a, a.dfinal, a.dh0, s);
+    if (e != hipSuccess || a.n == 0) return e;
     switch (dtype) {
         case 0: return grad_type<float, float>(a, s);
         case 1: return gtype ? grad_type<bf16_t, bf16_t>(a, s) : grad_type<bf16_t, float>(a, s);
