@@ -56,7 +56,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     if (threadIdx.x < kRecurCols) {
         const int c = threadIdx.x;
         float am = 1.f, ah = 0.f;
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < Lay::kGroups; ++i) {
             const float a = sa[i][SH ? c / V : c];
             ah = step_of(a, ah, sh[i][c]);
@@ -64,7 +64,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
         }
         float e = 0.f;
         if (A.tiles > 1) e = pass_state(A, tile, ct, am, ah, R && R->start[0] != -1, tile == A.tiles - 1);
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < Lay::kGroups; ++i) {
             const float next = step_of(sa[i][SH ? c / V : c], e, sh[i][c]);
             sh[i][c] = e;  // state entering group i

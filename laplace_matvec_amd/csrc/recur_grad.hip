@@ -15,6 +15,8 @@ namespace lx {
 
 namespace {
 
+constexpr int kSumPitch = kRecurCols / 4 + 1;  // sums of four channels per row, rows on different banks
+
 // dy of row j, plus dfinal on a last row; 0 on a row of no sequence.
 template <bool CARE, class Th, class T, int V>
 __device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, Th& th,
@@ -59,15 +61,33 @@ __device__ __forceinline__ void compose_grad(const RecurArgs& A, const RecurRows
     }
 }
 
+// dg of one row from a product per channel, one channel per lane: the lanes
+// of a decay are neighbours and the first of them gets their sum.
+template <class TG>
+__device__ __forceinline__ void head_sum(const RecurArgs& A, int64_t row, bool here, int ct, int lane, float sum)
+{
+    const int col = ct * kRecurCols + lane;
+    const int head = col < A.width ? col / A.per : -1;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const float o = __shfl_down(sum, d);
+        const int oh = __shfl_down(head, d);
+        if (lane + d < kWave && oh == head) sum += o;
+    }
+    if (!here || (lane > 0 && col % A.per != 0)) return;
+    if (recur_heads_inside(A.width, A.per)) ((TG*)A.dg)[row * A.lddg + head] = (TG)sum;
+    else A.part[row * (A.cols + A.heads) + ct + head] = sum;
+}
+
 // dx, dg and dh0 of the thread's rows from the state h entering them and the
 // gradient w from the rows after them.
 template <bool CARE, class T, class TG, int V, int L, bool SH>
 __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows* R,
                                             RecurThread<T, TG, V, L, SH>& th, RowPack<T, V, L>& dy,
-                                            int ct, float (&h)[V], float (&w)[V])
+                                            int ct, float (&h)[V], float (&w)[V], float (*s_sum)[kSumPitch])
 {
     using Th = RecurThread<T, TG, V, L, SH>;
-    constexpr int D = Th::D, kLanes = RecurLayout<V, L>::kLanes;
+    constexpr int D = Th::D;
     float before[L][V];  // state before each row
 #pragma unroll
     for (int j = 0; j < L; ++j) {
@@ -78,12 +98,9 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
         th.template step<CARE>(A, R, j, a, h);
     }
     const bool whole = th.row0 + L <= A.n;
-    const bool own = !SH || A.per == 1;  // a decay for each channel
-    // channels of one decay are neighbouring lanes of a row; the first of
-    // them gets their sum
-    const int head = th.in ? (int)(th.col / A.per) : -1;
-    const bool first = th.in && (th.lane == 0 || (int)((th.col - V) / A.per) != head);
-    const bool inside = recur_heads_inside(A.width, A.per);
+    const bool own = V == 1 ? A.per == 1 : !SH;  // a decay for each channel
+    T* dx = (T*)A.dx + th.row0 * A.lddx + th.col;
+    TG* dg = (TG*)A.dg + th.row0 * A.lddg + th.col;
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
         const int64_t row = th.row0 + j;
@@ -118,25 +135,40 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             }
         }
         settle(w);
-        if (A.dx && here) store_vec<V>((T*)A.dx + row * A.lddx + th.col, u);
-        if (!A.dg) continue;
+        if (A.dx && here) store_vec<V>(dx + j * A.lddx, u);
         if (own) {
-            if (here) store_vec<V>((TG*)A.dg + row * A.lddg + th.col, p);
-            continue;
+            if (A.dg && here) store_vec<V>(dg + j * A.lddg, p);
+        } else if (V > 1) {
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum += p[v];
+            s_sum[th.r0 + j][th.lane] = sum;
+        } else if (A.dg) {
+            head_sum<TG>(A, row, here, ct, th.lane, p[0]);
         }
+    }
+}
+
+// dg of a tile from s_sum[row][lane], sums over V channels each, V dividing
+// the channels of a decay.  All threads; s_sum is complete.
+template <class TG, int V, int THREADS, int PITCH>
+__device__ __forceinline__ void tile_sums(const RecurArgs& A, int64_t tile, int ct, const float (*s_sum)[PITCH])
+{
+    const int c0 = ct * kRecurCols;
+    const int c1 = c0 + kRecurCols < A.width ? c0 + kRecurCols : A.width;
+    const int first = c0 / A.per, count = (c1 - 1) / A.per - first + 1;
+    const bool inside = recur_heads_inside(A.width, A.per);
+    for (int i = threadIdx.x; i < kRecurTile * count; i += THREADS) {
+        const int r = i / count, head = first + i - r * count;
+        const int64_t row = tile * kRecurTile + r;
+        if (row >= A.n) return;
+        int a = head * A.per - c0, b = a + A.per;
+        a = a < 0 ? 0 : a / V;
+        b = b > c1 - c0 ? (c1 - c0) / V : b / V;
         float sum = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) sum += p[v];
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) {
-            const float o = __shfl_down(sum, d, kLanes);
-            const int oh = __shfl_down(head, d, kLanes);
-            if (th.lane + d < kLanes && oh == head) sum += o;
-        }
-        if (first && here) {
-            if (inside) ((TG*)A.dg)[row * A.lddg + head] = (TG)sum;
-            else A.part[row * (A.cols + A.heads) + ct + head] = sum;
-        }
+        for (; a < b; ++a) sum += s_sum[r][a];
+        if (inside) ((TG*)A.dg)[row * A.lddg + head] = (TG)sum;
+        else A.part[row * (A.cols + A.heads) + ct + head] = sum;
     }
 }
 
@@ -149,6 +181,8 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
     __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
     __shared__ float sh[Lay::kGroups][kRecurCols];
     __shared__ float sw[Lay::kGroups][kRecurCols];
+    constexpr bool kSums = SH && V > 1;
+    __shared__ float s_sum[kSums ? kRecurTile : 1][kSumPitch];
     const uint32_t turn = A.tiles > 1 ? next_tile(A.ticket) : blockIdx.x;
     const int64_t back = turn / (uint32_t)A.cols;  // tiles before this one in the pass: from the last rows on
     const int64_t tile = A.tiles - 1 - back;
@@ -180,14 +214,14 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
     if (threadIdx.x < kRecurCols) {
         const int c = threadIdx.x;
         float e = tile > 0 ? A.states_in[((tile - 1) * A.cols + ct) * kRecurCols + c] : 0.f;
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < Lay::kGroups; ++i) {
             const float next = step_of(sa[i][SH ? c / V : c], e, sh[i][c]);
             sh[i][c] = e;  // state entering group i
             e = next;
         }
         float am = 1.f, aw = 0.f;
-#pragma unroll
+#pragma unroll 8
         for (int i = Lay::kGroups - 1; i >= 0; --i) {
             const float a = sa[i][SH ? c / V : c];
             aw = step_of(a, aw, sw[i][c]);
@@ -197,7 +231,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
         const bool fresh = R && (R->last[kRecurTile - 1] != -1 || R->start[kRecurTile - 1] == -2);
         float b = 0.f;
         if (A.tiles > 1) b = pass_state(A, back, ct, am, aw, fresh, back == A.tiles - 1);
-#pragma unroll
+#pragma unroll 8
         for (int i = Lay::kGroups - 1; i >= 0; --i) {
             const float next = step_of(sa[i][SH ? c / V : c], b, sw[i][c]);
             sw[i][c] = b;  // gradient entering group i from the rows after it
@@ -210,8 +244,12 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
         h[v] = sh[th.group][th.lane * V + v];
         w[v] = sw[th.group][th.lane * V + v];
     }
-    if (care) write_grads<true>(A, R, th, dy, ct, h, w);
-    else write_grads<false>(A, R, th, dy, ct, h, w);
+    if (care) write_grads<true>(A, R, th, dy, ct, h, w, s_sum);
+    else write_grads<false>(A, R, th, dy, ct, h, w, s_sum);
+    if (kSums && A.dg) {
+        __syncthreads();
+        tile_sums<TG, V, Lay::kThreads, kSumPitch>(A, tile, ct, s_sum);
+    }
 }
 
 // Sums of decays whose channels span several channel tiles: a tile and a
