@@ -1934,7 +1934,8 @@ laplex_status laplex_recur(int64_t n, int64_t seqs, const int32_t* offsets, int6
     const Rows ins[4] = {{x, n, ldx, width, e}, {g, n, ldg, heads, eg}, {h0, seqs, width, width, 4},
                          {offsets, 1, seqs + 1, seqs + 1, 4}};
     for (const Rows& r : {outs[0], outs[1], ins[0], ins[1], ins[2]})
-        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+        if (!rows_ok(r) || (r.rows > 1 && r.ld > lx::kRecurMaxPitch))
+            return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
     if (const char* m = check_outputs(outs, 4, ins, 4)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
     const laplex_status st = check_device();
     if (st != LAPLEX_OK) return st;
@@ -1971,7 +1972,8 @@ laplex_status laplex_recur_backward(int64_t n, int64_t seqs, const int32_t* offs
                          {offsets, 1, seqs + 1, seqs + 1, 4}, {dy, n, lddy, width, e},
                          {dfinal, seqs, width, width, 4}, {ns > 0 ? states : nullptr, 1, ns, ns, 4}};
     for (const Rows& r : {outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[4], ins[5], ins[6]})
-        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+        if (!rows_ok(r) || (r.rows > 1 && r.ld > lx::kRecurMaxPitch))
+            return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
     if (const char* m = check_outputs(outs, 4, ins, 7)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
     const laplex_status st = check_device();
     if (st != LAPLEX_OK) return st;

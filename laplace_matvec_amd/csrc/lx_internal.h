@@ -394,6 +394,7 @@ hipError_t move_rows_launch(MoveKind kind, int dtype, const MoveArgs& a, hipStre
 // ---- gated recurrence (recur.hip, recur_grad.hip) ----
 constexpr int kRecurTile = 256;  // rows of a tile
 constexpr int kRecurCols = 64;   // channels of a tile
+constexpr int64_t kRecurMaxPitch = (int64_t)1 << 24;  // values between rows
 struct RecurArgs {
     int64_t n = 0;         // rows
     int64_t seqs = 0;      // sequences

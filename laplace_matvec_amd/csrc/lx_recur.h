@@ -40,6 +40,10 @@ __device__ __forceinline__ float decay_of(float g)
 // a h + x, forgetting h where a is 0.
 __device__ __forceinline__ float step_of(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
 
+// A condition that is the same in every lane, as a scalar: a branch on it is
+// then one for the whole wave, and neither side keeps the other's registers.
+__device__ __forceinline__ bool uniform(bool c) { return __builtin_amdgcn_readfirstlane((int)c) != 0; }
+
 // What is special about a tile's rows.
 struct RecurRows {
     int start[kRecurTile];  // sequence whose first row this is; -1: none; -2: a row of no sequence
@@ -56,7 +60,7 @@ __device__ __forceinline__ int64_t lower_bound64(const int32_t* v, int64_t n, in
         const int64_t step = (hi - lo + kWave - 1) / kWave;
         const int64_t at = lo + (int64_t)lane_id() * step;
         const bool below = at < hi && (int64_t)v[at] < key;
-        const int c = __popcll(__ballot(below));
+        const int c = __builtin_amdgcn_readfirstlane(__popcll(__ballot(below)));
         if (c == 0) break;
         const int64_t next = lo + (int64_t)c * step;
         lo += (int64_t)(c - 1) * step + 1;
@@ -116,6 +120,34 @@ __device__ __forceinline__ bool recur_rows(const RecurArgs& A, int64_t t0, Recur
     return true;
 }
 
+// Where a thread's rows of one array are: a base that is the same for the
+// wave (row j is j pitches further, in scalar registers) and a 32-bit offset
+// of the lane, so that an address takes one vector register for all rows.
+// A wave spans at most 64 rows of one array; a pitch of at most 2^24 values
+// (kRecurMaxPitch) keeps the offset within 32 bits.
+template <class T, int V>
+struct RowAt {
+    char* base;
+    int64_t pitch;  // bytes
+    uint32_t off;
+
+    // wave_row: the wave's first row; lane_row: of the lane, from there;
+    // col: of the wave; lane_col: of the lane, from there
+    __device__ __forceinline__ RowAt(const void* p, int64_t ld, int64_t wave_row, int lane_row, int64_t col,
+                                     int lane_col)
+        : base((char*)p + (wave_row * ld + col) * (int64_t)sizeof(T)),
+          pitch(ld * (int64_t)sizeof(T)),
+          off(((uint32_t)lane_row * (uint32_t)ld + (uint32_t)lane_col) * (uint32_t)sizeof(T))
+    {
+    }
+    __device__ __forceinline__ T* row(int j) const
+    {
+        char* b = base + j * pitch;
+        asm volatile("" : "+s"(b));  // stays in scalar registers, apart from the lane's offset
+        return reinterpret_cast<T*>(b + off);
+    }
+};
+
 // L rows of V channels of one array as stored, in 32-bit words (a vector of
 // 16-bit values would be taken apart into a register for each); 0 outside.
 template <class T, int V, int L>
@@ -134,18 +166,18 @@ struct RowPack {
             for (int i = 0; i < kWords; ++i) w[j][i] = q.v[i];
         }
     }
-    __device__ __forceinline__ void load(const void* base, int64_t ld, int64_t row0, int64_t n, int64_t col, bool in)
+    // rows: how many of the L are there (0 outside the width)
+    __device__ __forceinline__ void load(const RowAt<T, V>& at, int rows)
     {
-        const T* p = (const T*)base + row0 * ld + col;
-        if (in && row0 + L <= n) {
+        if (rows >= L) {
 #pragma unroll
-            for (int j = 0; j < L; ++j) load_row(j, p + j * ld);
+            for (int j = 0; j < L; ++j) load_row(j, at.row(j));
         } else {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) w[j][i] = 0;
-                if (in && row0 + j < n) load_row(j, p + j * ld);
+                if (j < rows) load_row(j, at.row(j));
             }
         }
     }
@@ -190,20 +222,43 @@ struct RecurThread {
     static constexpr int D = SH ? 1 : V;
     RowPack<T, V, L> x;
     RowPack<TG, D, L> g;
-    int64_t row0, col;
-    int r0, lane, group;  // first row within the tile, thread of the row, row group
+    int64_t wave_row;     // the wave's first row
+    int tile_col;         // the tile's first channel
+    int lane_row;         // the thread's first row, from the wave's
+    int r0;               // the same, from the tile's
+    int lane, group;      // thread of the row, row group
+    int rows;             // of the thread's L: those that exist, 0 outside the width
     bool in;              // channels inside the width
 
     __device__ __forceinline__ void load(const RecurArgs& A, int64_t tile, int ct)
     {
-        lane = (int)threadIdx.x % RecurLayout<V, L>::kLanes;
-        group = (int)threadIdx.x / RecurLayout<V, L>::kLanes;
-        r0 = group * L;
-        row0 = tile * kRecurTile + r0;
-        col = (int64_t)ct * kRecurCols + lane * V;
-        in = col < A.width;
-        x.load(A.x, A.ldx, row0, A.n, col, in);
-        g.load(A.g, A.ldg, row0, A.n, SH ? col / A.per : col, in);
+        using Lay = RecurLayout<V, L>;
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+        const int wave_r0 = wave * (kWave / Lay::kLanes) * L;
+        lane = (int)threadIdx.x % Lay::kLanes;
+        group = (int)threadIdx.x / Lay::kLanes;
+        lane_row = lane_id() / Lay::kLanes * L;
+        r0 = wave_r0 + lane_row;
+        wave_row = tile * kRecurTile + wave_r0;
+        tile_col = ct * kRecurCols;
+        in = col() < A.width;
+        const int64_t left = A.n - wave_row - lane_row;
+        rows = !in || left < 0 ? 0 : (left < L ? (int)left : L);
+        x.load(at<T, V>(A.x, A.ldx), rows);
+        g.load(gate_at<TG>(A, A.g, A.ldg), rows);
+    }
+    __device__ __forceinline__ int col() const { return tile_col + lane * V; }
+    template <class U, int N>
+    __device__ __forceinline__ RowAt<U, N> at(const void* p, int64_t ld) const
+    {
+        return RowAt<U, N>(p, ld, wave_row, lane_row, tile_col, lane * V);
+    }
+    // g or dg
+    template <class U>
+    __device__ __forceinline__ RowAt<U, D> gate_at(const RecurArgs& A, const void* p, int64_t ld) const
+    {
+        return SH ? RowAt<U, D>(p, ld, wave_row, lane_row, 0, in ? col() / A.per : 0)
+                  : RowAt<U, D>(p, ld, wave_row, lane_row, tile_col, lane * V);
     }
     // Row j: its decays and terms.  CARE: the tile has special rows or a
     // decay of 0 (or too small for the plain exponential) may be among them:
@@ -214,7 +269,6 @@ struct RecurThread {
     {
         // one row at a time: all rows' converted values at once would take
         // more registers than the rows themselves
-        x.forget(j);
         g.forget(j);
         g.get(j, a);
 #pragma unroll
@@ -228,6 +282,7 @@ struct RecurThread {
     template <bool CARE>
     __device__ __forceinline__ void terms(const RecurArgs& A, const RecurRows* R, int j, float (&t)[V])
     {
+        x.forget(j);
         x.get(j, t);
         if (!CARE || !R) return;
         const int q = R->start[r0 + j];
@@ -236,7 +291,7 @@ struct RecurThread {
             for (int v = 0; v < V; ++v) t[v] = 0.f;
         } else if (q >= 0 && A.h0 && in) {
             float h[V], a[D];
-            load_vec<V>(A.h0 + (int64_t)q * A.width + col, h);
+            load_vec<V>(A.h0 + (int64_t)q * A.width + col(), h);
             g.get(j, a);
 #pragma unroll
             for (int v = 0; v < V; ++v) t[v] = step_of(decay_of(a[SH ? 0 : v]), h[v], t[v]);
@@ -281,7 +336,7 @@ __device__ __forceinline__ bool any_zero(const float (&m)[D])
     bool z = false;
 #pragma unroll
     for (int d = 0; d < D; ++d) z |= m[d] == 0.f;
-    return __any(z);
+    return uniform(__any(z));
 }
 
 // ---- between tiles -------------------------------------------------------

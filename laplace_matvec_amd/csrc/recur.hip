@@ -12,17 +12,16 @@ namespace {
 template <bool CARE, class Th, class T, int V>
 __device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* R, Th& th, float (&h)[V])
 {
-    T* p = (T*)A.y + th.row0 * A.ldy + th.col;
-    const bool whole = th.row0 + Th::L <= A.n;
+    const RowAt<T, V> y = th.template at<T, V>(A.y, A.ldy);
 #pragma unroll
     for (int j = 0; j < Th::L; ++j) {
         float a[Th::D];
         th.template decays<CARE>(R, j, a);
         th.template step<CARE>(A, R, j, a, h);
-        if (th.in && (whole || th.row0 + j < A.n)) store_vec<V>(p + j * A.ldy, h);
+        if (j < th.rows) store_vec<V>(y.row(j), h);
         if (CARE && R && A.final && th.in) {
             const int q = R->last[th.r0 + j];
-            if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col, h);
+            if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col(), h);
         }
     }
 }
@@ -40,7 +39,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     const int ct = (int)(turn % (uint32_t)A.cols);
     Th th;
     th.load(A, tile, ct);
-    const RecurRows* R = recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows) ? &rows : nullptr;
+    const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows)) ? &rows : nullptr;
     float m[Th::D], h[V];
     bool care = R != nullptr;
     if (!care) {

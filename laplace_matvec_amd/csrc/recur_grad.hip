@@ -32,7 +32,7 @@ __device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, T
     const int q = R->last[th.r0 + j];
     if (q >= 0 && A.dfinal && th.in) {
         float f[V];
-        load_vec<V>(A.dfinal + (int64_t)q * A.width + th.col, f);
+        load_vec<V>(A.dfinal + (int64_t)q * A.width + th.col(), f);
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] += f[v];
     }
@@ -92,20 +92,20 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
 #pragma unroll
     for (int j = 0; j < L; ++j) {
         float a[D];
+        __builtin_amdgcn_sched_barrier(0);
         th.template decays<CARE>(R, j, a);
 #pragma unroll
         for (int v = 0; v < V; ++v) before[j][v] = h[v];
         th.template step<CARE>(A, R, j, a, h);
     }
-    const bool whole = th.row0 + L <= A.n;
     const bool own = V == 1 ? A.per == 1 : !SH;  // a decay for each channel
-    T* dx = (T*)A.dx + th.row0 * A.lddx + th.col;
-    TG* dg = (TG*)A.dg + th.row0 * A.lddg + th.col;
+    const RowAt<T, V> dx = th.template at<T, V>(A.dx, A.lddx);
+    const RowAt<TG, V> dg = th.template at<TG, V>(A.dg, A.lddg);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
-        const int64_t row = th.row0 + j;
-        const bool here = th.in && (whole || row < A.n);
+        const bool here = j < th.rows;
         float a[D], u[V], p[V];
+        __builtin_amdgcn_sched_barrier(0);
         th.template decays<CARE>(R, j, a);
         row_dy<CARE, Th, T, V>(A, R, th, dy, j, u);
         const int q = CARE && R ? R->start[th.r0 + j] : -1;
@@ -115,7 +115,7 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             th.g.get(j, g);
 #pragma unroll
             for (int v = 0; v < V; ++v) h0[v] = 0.f;
-            if (A.h0 && th.in) load_vec<V>(A.h0 + (int64_t)q * A.width + th.col, h0);
+            if (A.h0 && th.in) load_vec<V>(A.h0 + (int64_t)q * A.width + th.col(), h0);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float av = decay_of(g[SH ? 0 : v]);
@@ -124,7 +124,7 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
                 p[v] = av == 0.f ? 0.f : out[v] * h0[v];
                 w[v] = 0.f;
             }
-            if (A.dh0 && th.in) store_vec<V>(A.dh0 + (int64_t)q * A.width + th.col, out);
+            if (A.dh0 && th.in) store_vec<V>(A.dh0 + (int64_t)q * A.width + th.col(), out);
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -135,16 +135,16 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             }
         }
         settle(w);
-        if (A.dx && here) store_vec<V>(dx + j * A.lddx, u);
+        if (A.dx && here) store_vec<V>(dx.row(j), u);
         if (own) {
-            if (A.dg && here) store_vec<V>(dg + j * A.lddg, p);
+            if (A.dg && here) store_vec<V>(dg.row(j), p);
         } else if (V > 1) {
             float sum = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) sum += p[v];
             s_sum[th.r0 + j][th.lane] = sum;
         } else if (A.dg) {
-            head_sum<TG>(A, row, here, ct, th.lane, p[0]);
+            head_sum<TG>(A, th.wave_row + th.lane_row + j, here, ct, th.lane, p[0]);
         }
     }
 }
@@ -190,8 +190,8 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
     Th th;
     RowPack<T, V, L> dy;
     th.load(A, tile, ct);
-    dy.load(A.dy, A.lddy, th.row0, A.n, th.col, th.in);
-    const RecurRows* R = recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows) ? &rows : nullptr;
+    dy.load(th.template at<T, V>(A.dy, A.lddy), th.rows);
+    const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows)) ? &rows : nullptr;
     float m[Th::D], h[V], w[V];
     bool care = R != nullptr;
     if (!care) {
@@ -292,7 +292,7 @@ hipError_t grad_type(const RecurArgs& a, hipStream_t s)
                       (sh ? a.per % 4 == 0
                           : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4) && vec_ok(a.dg, a.lddg, a.width, sizeof(TG), 4));
     if (wide) return sh ? grad_go<T, TG, 4, 8, true>(a, s) : grad_go<T, TG, 4, 8, false>(a, s);
-    return grad_go<T, TG, 1, 32, true>(a, s);
+    return grad_go<T, TG, 1, 16, true>(a, s);
 }
 
 }  // namespace
