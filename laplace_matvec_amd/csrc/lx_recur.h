@@ -142,61 +142,64 @@ struct RowAt {
     }
     __device__ __forceinline__ T* row(int j) const
     {
-        char* b = base + j * pitch;
-        asm volatile("" : "+s"(b));  // stays in scalar registers, apart from the lane's offset
-        return reinterpret_cast<T*>(b + off);
+        int64_t o = j * pitch;
+        asm volatile("" : "+s"(o));  // stays in scalar registers, apart from the lane's offset
+        return reinterpret_cast<T*>(base + o + off);
     }
 };
 
-// L rows of V channels of one array as stored, in 32-bit words (a vector of
-// 16-bit values would be taken apart into a register for each); 0 outside.
+// What holds N bytes of a row: a register tuple as it is loaded.
+template <int N>
+struct RowWord;
+template <>
+struct RowWord<2> { typedef uint16_t Mem; typedef uint32_t Reg; };
+template <>
+struct RowWord<4> { typedef uint32_t Mem; typedef uint32_t Reg; };
+template <>
+struct RowWord<8> { typedef uint32_t Mem __attribute__((ext_vector_type(2))); typedef Mem Reg; };
+template <>
+struct RowWord<16> { typedef uint32_t Mem __attribute__((ext_vector_type(4))); typedef Mem Reg; };
+
+// L rows of V channels of one array as stored (a vector of 16-bit values
+// would be taken apart into a register for each); 0 outside.
 template <class T, int V, int L>
 struct RowPack {
     static constexpr int kBytes = V * (int)sizeof(T);
-    static constexpr int kWords = (kBytes + 3) / 4;
-    uint32_t w[L][kWords];
+    typedef typename RowWord<kBytes>::Mem Mem;
+    typedef typename RowWord<kBytes>::Reg Reg;
+    Reg w[L];
 
-    __device__ __forceinline__ void load_row(int j, const T* p)
-    {
-        if constexpr (kBytes == 2) {
-            w[j][0] = *reinterpret_cast<const uint16_t*>(p);
-        } else {
-            const Pack<uint32_t, kWords> q = *reinterpret_cast<const Pack<uint32_t, kWords>*>(p);
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) w[j][i] = q.v[i];
-        }
-    }
     // rows: how many of the L are there (0 outside the width)
     __device__ __forceinline__ void load(const RowAt<T, V>& at, int rows)
     {
         if (rows >= L) {
 #pragma unroll
-            for (int j = 0; j < L; ++j) load_row(j, at.row(j));
+            for (int j = 0; j < L; ++j) w[j] = *reinterpret_cast<const Mem*>(at.row(j));
         } else {
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-#pragma unroll
-                for (int i = 0; i < kWords; ++i) w[j][i] = 0;
-                if (j < rows) load_row(j, at.row(j));
+                w[j] = Reg(0);
+                if (j < rows) w[j] = *reinterpret_cast<const Mem*>(at.row(j));
             }
         }
     }
     // Makes the compiler forget what it has worked out from a row: a later
     // use converts it again (and takes the exponentials again) instead of
     // holding every result in registers in between.
-    __device__ __forceinline__ void forget(int j)
+    __device__ __forceinline__ void forget(int j) { asm volatile("" : "+v"(w[j])); }
+    __device__ __forceinline__ uint32_t word(int j, int i) const
     {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[j][i]));
+        if constexpr (kBytes <= 4) return w[j];
+        else return w[j][i];
     }
     __device__ __forceinline__ void get(int j, float (&out)[V]) const
     {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if constexpr (sizeof(T) == 4) {
-                out[v] = __uint_as_float(w[j][v]);
+                out[v] = __uint_as_float(word(j, v));
             } else {
-                const uint32_t q = w[j][v / 2];
+                const uint32_t q = word(j, v / 2);
                 if constexpr (__is_same(T, bf16_t)) {
                     out[v] = __uint_as_float(v & 1 ? q & 0xFFFF0000u : q << 16);
                 } else {

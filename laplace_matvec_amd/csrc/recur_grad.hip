@@ -38,26 +38,32 @@ __device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, T
     }
 }
 
-// Gradient of the thread's rows towards the row before them, from none
-// after them (their map is w -> m w + W, m as in the forward direction).
-// The first row of a sequence passes nothing on.
+// Both maps of the thread's rows: the state after them, h -> m h + H, and the
+// gradient before them, w -> m w + W.  In row order W is the sum of dy_j
+// times the product of the decays up to row j, so one sweep gives both.
 template <bool CARE, class Th, class T, int V>
-__device__ __forceinline__ void compose_grad(const RecurArgs& A, const RecurRows* R, Th& th,
-                                             RowPack<T, V, Th::L>& dy, float (&w)[V])
+__device__ __forceinline__ void compose_both(const RecurArgs& A, const RecurRows* R, Th& th,
+                                             RowPack<T, V, Th::L>& dy, float (&m)[Th::D], float (&H)[V], float (&W)[V])
 {
 #pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = 0.f;
+    for (int d = 0; d < Th::D; ++d) m[d] = 1.f;
 #pragma unroll
-    for (int j = Th::L - 1; j >= 0; --j) {
+    for (int v = 0; v < V; ++v) H[v] = W[v] = 0.f;
+#pragma unroll
+    for (int j = 0; j < Th::L; ++j) {
         float a[Th::D], d[V];
         th.template decays<CARE>(R, j, a);
+        th.template step<CARE>(A, R, j, a, H);
         row_dy<CARE, Th, T, V>(A, R, th, dy, j, d);
 #pragma unroll
+        for (int i = 0; i < Th::D; ++i) m[i] *= a[i];
+#pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float av = a[Th::D == 1 ? 0 : v];
-            w[v] = CARE && av == 0.f ? 0.f : av * (d[v] + w[v]);
+            const float mv = m[Th::D == 1 ? 0 : v];
+            W[v] = CARE && mv == 0.f ? W[v] : fmaf(mv, d[v], W[v]);
         }
-        settle(w);
+        settle(m);
+        settle(W);
     }
 }
 
@@ -134,7 +140,7 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
                 p[v] = CARE && av == 0.f ? 0.f : w[v] * before[j][v];
             }
         }
-        settle(w);
+        if (CARE) settle(w);
         if (A.dx && here) store_vec<V>(dx.row(j), u);
         if (own) {
             if (A.dg && here) store_vec<V>(dg.row(j), p);
@@ -195,14 +201,10 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
     float m[Th::D], h[V], w[V];
     bool care = R != nullptr;
     if (!care) {
-        th.template compose<false>(A, R, m, h);
-        compose_grad<false, Th, T, V>(A, R, th, dy, w);
+        compose_both<false, Th, T, V>(A, R, th, dy, m, h, w);
         care = any_zero(m);
     }
-    if (care) {
-        th.template compose<true>(A, R, m, h);
-        compose_grad<true, Th, T, V>(A, R, th, dy, w);
-    }
+    if (care) compose_both<true, Th, T, V>(A, R, th, dy, m, h, w);
 #pragma unroll
     for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
 #pragma unroll
@@ -211,15 +213,9 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
         sw[th.group][th.lane * V + v] = w[v];
     }
     __syncthreads();
-    if (threadIdx.x < kRecurCols) {
-        const int c = threadIdx.x;
-        float e = tile > 0 ? A.states_in[((tile - 1) * A.cols + ct) * kRecurCols + c] : 0.f;
-#pragma unroll 8
-        for (int i = 0; i < Lay::kGroups; ++i) {
-            const float next = step_of(sa[i][SH ? c / V : c], e, sh[i][c]);
-            sh[i][c] = e;  // state entering group i
-            e = next;
-        }
+    // one wave carries the gradient, another the state
+    const int c = lane_id();
+    if (threadIdx.x < kWave) {
         float am = 1.f, aw = 0.f;
 #pragma unroll 8
         for (int i = Lay::kGroups - 1; i >= 0; --i) {
@@ -236,6 +232,14 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
             const float next = step_of(sa[i][SH ? c / V : c], b, sw[i][c]);
             sw[i][c] = b;  // gradient entering group i from the rows after it
             b = next;
+        }
+    } else if (threadIdx.x < 2 * kWave) {
+        float e = tile > 0 ? A.states_in[((tile - 1) * A.cols + ct) * kRecurCols + c] : 0.f;
+#pragma unroll 8
+        for (int i = 0; i < Lay::kGroups; ++i) {
+            const float next = step_of(sa[i][SH ? c / V : c], e, sh[i][c]);
+            sh[i][c] = e;  // state entering group i
+            e = next;
         }
     }
     __syncthreads();
