@@ -48,6 +48,7 @@ __device__ __forceinline__ bool uniform(bool c) { return __builtin_amdgcn_readfi
 struct RecurRows {
     int start[kRecurTile];  // sequence whose first row this is; -1: none; -2: a row of no sequence
     int last[kRecurTile];   // sequence whose last row this is; -1: none
+    uint64_t odd[kRecurTile / kWave];  // bit per row: either of them is not -1
 };
 
 // Index of the first of n values that is not below `key` (values ascend),
@@ -117,6 +118,11 @@ __device__ __forceinline__ bool recur_rows(const RecurArgs& A, int64_t t0, Recur
         }
         __syncthreads();
     }
+    if (tid < kRecurTile) {
+        const uint64_t odd = __ballot(R.start[tid] != -1 || R.last[tid] != -1);
+        if (tid % kWave == 0) R.odd[tid / kWave] = odd;
+    }
+    __syncthreads();
     return true;
 }
 
@@ -146,6 +152,7 @@ struct RowAt {
         asm volatile("" : "+s"(o));  // stays in scalar registers, apart from the lane's offset
         return reinterpret_cast<T*>(base + o + off);
     }
+    __device__ __forceinline__ T* any_row(int64_t j) const { return reinterpret_cast<T*>(base + j * pitch + off); }
 };
 
 // What holds N bytes of a row: a register tuple as it is loaded.
@@ -161,7 +168,7 @@ template <>
 struct RowWord<16> { typedef uint32_t Mem __attribute__((ext_vector_type(4))); typedef Mem Reg; };
 
 // L rows of V channels of one array as stored (a vector of 16-bit values
-// would be taken apart into a register for each); 0 outside.
+// would be taken apart into a register for each).
 template <class T, int V, int L>
 struct RowPack {
     static constexpr int kBytes = V * (int)sizeof(T);
@@ -169,42 +176,36 @@ struct RowPack {
     typedef typename RowWord<kBytes>::Reg Reg;
     Reg w[L];
 
-    // rows: how many of the L are there (0 outside the width)
-    __device__ __forceinline__ void load(const RowAt<T, V>& at, int rows)
+    // whole: all of the tile's rows are there; else the last one (`last`
+    // from the thread's first, perhaps before it) stands for those past it
+    __device__ __forceinline__ void load(const RowAt<T, V>& at, bool whole, int64_t last)
     {
-        if (rows >= L) {
+        if (whole) {
 #pragma unroll
             for (int j = 0; j < L; ++j) w[j] = *reinterpret_cast<const Mem*>(at.row(j));
         } else {
 #pragma unroll
-            for (int j = 0; j < L; ++j) {
-                w[j] = Reg(0);
-                if (j < rows) w[j] = *reinterpret_cast<const Mem*>(at.row(j));
-            }
+            for (int j = 0; j < L; ++j) w[j] = *reinterpret_cast<const Mem*>(at.any_row(j < last ? j : last));
         }
     }
-    // Makes the compiler forget what it has worked out from a row: a later
-    // use converts it again (and takes the exponentials again) instead of
-    // holding every result in registers in between.
-    __device__ __forceinline__ void forget(int j) { asm volatile("" : "+v"(w[j])); }
-    __device__ __forceinline__ uint32_t word(int j, int i) const
-    {
-        if constexpr (kBytes <= 4) return w[j];
-        else return w[j][i];
-    }
+    // Row j in float32.  The copy hides that every call gives the same: the
+    // compiler would hold all converted values (and all exponentials) in
+    // registers from their first use to their last instead of the rows.
     __device__ __forceinline__ void get(int j, float (&out)[V]) const
     {
+        Reg t = w[j];
+        asm volatile("" : "+v"(t));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            uint32_t q;
+            if constexpr (kBytes <= 4) q = t;
+            else q = t[v * (int)sizeof(T) / 4];
             if constexpr (sizeof(T) == 4) {
-                out[v] = __uint_as_float(word(j, v));
+                out[v] = __uint_as_float(q);
+            } else if constexpr (__is_same(T, bf16_t)) {
+                out[v] = __uint_as_float(v & 1 ? q & 0xFFFF0000u : q << 16);
             } else {
-                const uint32_t q = word(j, v / 2);
-                if constexpr (__is_same(T, bf16_t)) {
-                    out[v] = __uint_as_float(v & 1 ? q & 0xFFFF0000u : q << 16);
-                } else {
-                    out[v] = (float)__builtin_bit_cast(f16_t, (uint16_t)(v & 1 ? q >> 16 : q));
-                }
+                out[v] = (float)__builtin_bit_cast(f16_t, (uint16_t)(v & 1 ? q >> 16 : q));
             }
         }
     }
@@ -218,6 +219,12 @@ __device__ __forceinline__ void settle(float (&v)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
 }
 
+// How a wave goes through its rows: kCareNone if every decay is above 0;
+// kCareZero if one may be 0 or too small for the plain exponential;
+// kCareRows if it has special rows too: first rows take h0 in and forget
+// what came before, rows of no sequence are 0.
+enum { kCareNone = 0, kCareZero = 1, kCareRows = 2 };
+
 // A thread's rows of x and g.  SH: one decay serves the V channels.
 template <class T, class TG, int V, int LL, bool SH>
 struct RecurThread {
@@ -230,8 +237,11 @@ struct RecurThread {
     int lane_row;         // the thread's first row, from the wave's
     int r0;               // the same, from the tile's
     int lane, group;      // thread of the row, row group
-    int rows;             // of the thread's L: those that exist, 0 outside the width
-    bool in;              // channels inside the width
+    int rows;             // of the thread's L: those that exist and are inside the width
+    bool in;              // channels inside the width; others read the tile's first
+    bool whole;           // all rows of the tile exist
+    int64_t last;         // the array's last row, from the thread's first
+    uint32_t odd;         // special rows
 
     __device__ __forceinline__ void load(const RecurArgs& A, int64_t tile, int ct)
     {
@@ -245,76 +255,77 @@ struct RecurThread {
         wave_row = tile * kRecurTile + wave_r0;
         tile_col = ct * kRecurCols;
         in = col() < A.width;
-        const int64_t left = A.n - wave_row - lane_row;
-        rows = !in || left < 0 ? 0 : (left < L ? (int)left : L);
-        x.load(at<T, V>(A.x, A.ldx), rows);
-        g.load(gate_at<TG>(A, A.g, A.ldg), rows);
+        whole = (tile + 1) * kRecurTile <= A.n;
+        last = A.n - 1 - wave_row - lane_row;
+        rows = !in || last < 0 ? 0 : (last < L - 1 ? (int)last + 1 : L);
+        x.load(at<T, V>(A.x, A.ldx), whole, last);
+        g.load(gate_at<TG>(A, A.g, A.ldg), whole, last);
     }
     __device__ __forceinline__ int col() const { return tile_col + lane * V; }
     template <class U, int N>
     __device__ __forceinline__ RowAt<U, N> at(const void* p, int64_t ld) const
     {
-        return RowAt<U, N>(p, ld, wave_row, lane_row, tile_col, lane * V);
+        return RowAt<U, N>(p, ld, wave_row, lane_row, tile_col, in ? lane * V : 0);
     }
     // g or dg
     template <class U>
     __device__ __forceinline__ RowAt<U, D> gate_at(const RecurArgs& A, const void* p, int64_t ld) const
     {
-        return SH ? RowAt<U, D>(p, ld, wave_row, lane_row, 0, in ? col() / A.per : 0)
-                  : RowAt<U, D>(p, ld, wave_row, lane_row, tile_col, lane * V);
+        return SH ? RowAt<U, D>(p, ld, wave_row, lane_row, 0, (in ? col() : tile_col) / A.per)
+                  : RowAt<U, D>(p, ld, wave_row, lane_row, tile_col, in ? lane * V : 0);
     }
-    // Row j: its decays and terms.  CARE: the tile has special rows or a
-    // decay of 0 (or too small for the plain exponential) may be among them:
-    // first rows take h0 in and forget what came before, rows of no
-    // sequence are 0.
-    template <bool CARE>
-    __device__ __forceinline__ void decays(const RecurRows* R, int j, float (&a)[D])
+    // The thread's special rows, a bit each, and whether its wave has any.
+    __device__ __forceinline__ bool find_odd(const RecurRows* R)
     {
-        // one row at a time: all rows' converted values at once would take
-        // more registers than the rows themselves
-        g.forget(j);
+        static_assert(L <= 32 && kWave % L == 0, "a thread's rows lie in one word");
+        odd = R ? (uint32_t)(R->odd[r0 / kWave] >> (r0 % kWave)) & (uint32_t)((1ull << L) - 1) : 0u;
+        return uniform(__any(odd != 0));
+    }
+    template <int CARE>
+    __device__ __forceinline__ bool special(int j) const
+    {
+        return CARE == kCareRows && (odd >> j & 1u);
+    }
+    // Row j: its decays, and h -> a h + x.
+    template <int CARE>
+    __device__ __forceinline__ void decays(const RecurRows* R, int j, float (&a)[D]) const
+    {
         g.get(j, a);
 #pragma unroll
         for (int d = 0; d < D; ++d)
             a[d] = CARE ? decay_of(a[d]) : __builtin_amdgcn_exp2f(a[d] * 1.44269504088896341f);
-        if (CARE && R && R->start[r0 + j] != -1) {
+        if (special<CARE>(j) && R->start[r0 + j] != -1) {
 #pragma unroll
             for (int d = 0; d < D; ++d) a[d] = 0.f;
         }
     }
-    template <bool CARE>
-    __device__ __forceinline__ void terms(const RecurArgs& A, const RecurRows* R, int j, float (&t)[V])
-    {
-        x.forget(j);
-        x.get(j, t);
-        if (!CARE || !R) return;
-        const int q = R->start[r0 + j];
-        if (q == -2) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) t[v] = 0.f;
-        } else if (q >= 0 && A.h0 && in) {
-            float h[V], a[D];
-            load_vec<V>(A.h0 + (int64_t)q * A.width + col(), h);
-            g.get(j, a);
-#pragma unroll
-            for (int v = 0; v < V; ++v) t[v] = step_of(decay_of(a[SH ? 0 : v]), h[v], t[v]);
-        }
-    }
-    // h -> a h + t for row j
-    template <bool CARE>
+    template <int CARE>
     __device__ __forceinline__ void step(const RecurArgs& A, const RecurRows* R, int j, const float (&a)[D],
-                                         float (&h)[V])
+                                         float (&h)[V]) const
     {
         float t[V];
-        terms<CARE>(A, R, j, t);
+        x.get(j, t);
+        if (special<CARE>(j)) {
+            const int q = R->start[r0 + j];
+            if (q == -2) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) t[v] = 0.f;
+            } else if (q >= 0 && A.h0 && in) {
+                float h0[V], b[D];
+                load_vec<V>(A.h0 + (int64_t)q * A.width + col(), h0);
+                g.get(j, b);
+#pragma unroll
+                for (int v = 0; v < V; ++v) t[v] = step_of(decay_of(b[SH ? 0 : v]), h0[v], t[v]);
+            }
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v)
             h[v] = CARE ? step_of(a[SH ? 0 : v], h[v], t[v]) : fmaf(a[SH ? 0 : v], h[v], t[v]);
         settle(h);
     }
     // Composed map of the thread's rows: h -> m h + H.
-    template <bool CARE>
-    __device__ __forceinline__ void compose(const RecurArgs& A, const RecurRows* R, float (&m)[D], float (&H)[V])
+    template <int CARE>
+    __device__ __forceinline__ void compose(const RecurArgs& A, const RecurRows* R, float (&m)[D], float (&H)[V]) const
     {
 #pragma unroll
         for (int d = 0; d < D; ++d) m[d] = 1.f;

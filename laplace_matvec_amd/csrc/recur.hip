@@ -9,8 +9,8 @@ namespace lx {
 namespace {
 
 // Rows of y (and final states) of one thread from the state entering it.
-template <bool CARE, class Th, class T, int V>
-__device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* R, Th& th, float (&h)[V])
+template <int CARE, class Th, class T, int V>
+__device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* R, const Th& th, float (&h)[V])
 {
     const RowAt<T, V> y = th.template at<T, V>(A.y, A.ldy);
 #pragma unroll
@@ -18,8 +18,8 @@ __device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* 
         float a[Th::D];
         th.template decays<CARE>(R, j, a);
         th.template step<CARE>(A, R, j, a, h);
-        if (j < th.rows) store_vec<V>(y.row(j), h);
-        if (CARE && R && A.final && th.in) {
+        if (CARE == kCareRows ? j < th.rows : th.in) store_vec<V>(y.row(j), h);
+        if (th.template special<CARE>(j) && A.final && th.in) {
             const int q = R->last[th.r0 + j];
             if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col(), h);
         }
@@ -41,12 +41,13 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     th.load(A, tile, ct);
     const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows)) ? &rows : nullptr;
     float m[Th::D], h[V];
-    bool care = R != nullptr;
-    if (!care) {
-        th.template compose<false>(A, R, m, h);
-        care = any_zero(m);
+    int care = th.find_odd(R) ? kCareRows : kCareNone;
+    if (care == kCareNone) {
+        th.template compose<kCareNone>(A, R, m, h);
+        if (any_zero(m)) care = kCareZero;
     }
-    if (care) th.template compose<true>(A, R, m, h);
+    if (care == kCareZero) th.template compose<kCareZero>(A, R, m, h);
+    if (care == kCareRows) th.template compose<kCareRows>(A, R, m, h);
 #pragma unroll
     for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
 #pragma unroll
@@ -73,8 +74,9 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = sh[th.group][th.lane * V + v];
-    if (care) write_rows<true, Th, T>(A, R, th, h);
-    else write_rows<false, Th, T>(A, R, th, h);
+    if (care == kCareNone) write_rows<kCareNone, Th, T>(A, R, th, h);
+    else if (care == kCareZero) write_rows<kCareZero, Th, T>(A, R, th, h);
+    else write_rows<kCareRows, Th, T>(A, R, th, h);
 }
 
 // Blocks [0, fill): 16 bytes of all ones per thread over the published

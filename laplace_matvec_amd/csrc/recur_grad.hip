@@ -18,13 +18,12 @@ namespace {
 constexpr int kSumPitch = kRecurCols / 4 + 1;  // sums of four channels per row, rows on different banks
 
 // dy of row j, plus dfinal on a last row; 0 on a row of no sequence.
-template <bool CARE, class Th, class T, int V>
-__device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, Th& th,
-                                       RowPack<T, V, Th::L>& dy, int j, float (&d)[V])
+template <int CARE, class Th, class T, int V>
+__device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, const Th& th,
+                                       const RowPack<T, V, Th::L>& dy, int j, float (&d)[V])
 {
-    dy.forget(j);
     dy.get(j, d);
-    if (!CARE || !R) return;
+    if (!th.template special<CARE>(j)) return;
     if (R->start[th.r0 + j] == -2) {
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = 0.f;
@@ -41,9 +40,9 @@ __device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, T
 // Both maps of the thread's rows: the state after them, h -> m h + H, and the
 // gradient before them, w -> m w + W.  In row order W is the sum of dy_j
 // times the product of the decays up to row j, so one sweep gives both.
-template <bool CARE, class Th, class T, int V>
-__device__ __forceinline__ void compose_both(const RecurArgs& A, const RecurRows* R, Th& th,
-                                             RowPack<T, V, Th::L>& dy, float (&m)[Th::D], float (&H)[V], float (&W)[V])
+template <int CARE, class Th, class T, int V>
+__device__ __forceinline__ void compose_both(const RecurArgs& A, const RecurRows* R, const Th& th,
+                                             const RowPack<T, V, Th::L>& dy, float (&m)[Th::D], float (&H)[V], float (&W)[V])
 {
 #pragma unroll
     for (int d = 0; d < Th::D; ++d) m[d] = 1.f;
@@ -87,9 +86,9 @@ __device__ __forceinline__ void head_sum(const RecurArgs& A, int64_t row, bool h
 
 // dx, dg and dh0 of the thread's rows from the state h entering them and the
 // gradient w from the rows after them.
-template <bool CARE, class T, class TG, int V, int L, bool SH>
+template <int CARE, class T, class TG, int V, int L, bool SH>
 __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows* R,
-                                            RecurThread<T, TG, V, L, SH>& th, RowPack<T, V, L>& dy,
+                                            const RecurThread<T, TG, V, L, SH>& th, const RowPack<T, V, L>& dy,
                                             int ct, float (&h)[V], float (&w)[V], float (*s_sum)[kSumPitch])
 {
     using Th = RecurThread<T, TG, V, L, SH>;
@@ -109,12 +108,12 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
     const RowAt<TG, V> dg = th.template at<TG, V>(A.dg, A.lddg);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
-        const bool here = j < th.rows;
+        const bool here = CARE == kCareRows ? j < th.rows : th.in;
         float a[D], u[V], p[V];
         __builtin_amdgcn_sched_barrier(0);
         th.template decays<CARE>(R, j, a);
         row_dy<CARE, Th, T, V>(A, R, th, dy, j, u);
-        const int q = CARE && R ? R->start[th.r0 + j] : -1;
+        const int q = th.template special<CARE>(j) ? R->start[th.r0 + j] : -1;
         if (q >= 0) {
             // the decay of a first row acts on h0 alone
             float g[D], h0[V], out[V];
@@ -196,15 +195,16 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
     Th th;
     RowPack<T, V, L> dy;
     th.load(A, tile, ct);
-    dy.load(th.template at<T, V>(A.dy, A.lddy), th.rows);
+    dy.load(th.template at<T, V>(A.dy, A.lddy), th.whole, th.last);
     const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows)) ? &rows : nullptr;
     float m[Th::D], h[V], w[V];
-    bool care = R != nullptr;
-    if (!care) {
-        compose_both<false, Th, T, V>(A, R, th, dy, m, h, w);
-        care = any_zero(m);
+    int care = th.find_odd(R) ? kCareRows : kCareNone;
+    if (care == kCareNone) {
+        compose_both<kCareNone, Th, T, V>(A, R, th, dy, m, h, w);
+        if (any_zero(m)) care = kCareZero;
     }
-    if (care) compose_both<true, Th, T, V>(A, R, th, dy, m, h, w);
+    if (care == kCareZero) compose_both<kCareZero, Th, T, V>(A, R, th, dy, m, h, w);
+    if (care == kCareRows) compose_both<kCareRows, Th, T, V>(A, R, th, dy, m, h, w);
 #pragma unroll
     for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
 #pragma unroll
@@ -248,8 +248,9 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
         h[v] = sh[th.group][th.lane * V + v];
         w[v] = sw[th.group][th.lane * V + v];
     }
-    if (care) write_grads<true>(A, R, th, dy, ct, h, w, s_sum);
-    else write_grads<false>(A, R, th, dy, ct, h, w, s_sum);
+    if (care == kCareNone) write_grads<kCareNone>(A, R, th, dy, ct, h, w, s_sum);
+    else if (care == kCareZero) write_grads<kCareZero>(A, R, th, dy, ct, h, w, s_sum);
+    else write_grads<kCareRows>(A, R, th, dy, ct, h, w, s_sum);
     if (kSums && A.dg) {
         __syncthreads();
         tile_sums<TG, V, Lay::kThreads, kSumPitch>(A, tile, ct, s_sum);
