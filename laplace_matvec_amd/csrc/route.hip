@@ -230,17 +230,15 @@ __global__ __launch_bounds__(kRouteThreads) void lx_route_place(RouteArgs A)
     }
 }
 
-// Rows past the last kept slot, offsets[E] .. n - 1: at most K per token,
-// row offsets[E] + t + i T for i = 0, 1, ... by token t's threads.
+// Rows past the last kept slot, `kept` .. n - 1: at most K per token, row
+// kept + t + i T for i = 0, 1, ... by token t's threads.
 template <int V, class T>
-__device__ __forceinline__ void zero_tail(const MoveArgs& A, T* rows, int64_t ld, int64_t t, int col)
+__device__ __forceinline__ void zero_tail(const MoveArgs& A, T* rows, int64_t ld, int64_t kept, int64_t t)
 {
     float z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) z[i] = 0.f;
-    int64_t r = (int64_t)A.offsets[A.experts];
-    r = (r < 0 ? 0 : r) + t;
-    for (; r < A.tokens * A.slots; r += A.tokens) store_vec<V>(rows + r * ld + (int64_t)col * V, z);
+    for (int64_t r = (kept < 0 ? 0 : kept) + t; r < A.tokens * A.slots; r += A.tokens) store_vec<V>(rows + r * ld, z);
 }
 
 // Token and column group of this thread: the flat index over
@@ -257,113 +255,138 @@ __device__ __forceinline__ bool token_group(const MoveArgs& A, int64_t* t, int* 
     return *t < A.tokens;
 }
 
-template <int V, class T>
+// Rows of KC slots of a token, from slot k0 on; -1 where there is none.
+template <int KC>
+__device__ __forceinline__ void slot_rows(const MoveArgs& A, int64_t t, int64_t k0, int (&row)[KC])
+{
+    const int64_t rows = A.tokens * A.slots;
+    const int32_t* place = A.place + t * A.slots + k0;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+        const int r = k0 + k < A.slots ? place[k] : -1;
+        row[k] = r >= 0 && r < rows ? r : -1;
+    }
+}
+
+// KC: slots whose rows are in flight together; more are done KC at a time.
+template <int V, class T, int KC>
 __global__ __launch_bounds__(256) void lx_dispatch(MoveArgs A)
 {
     int64_t t;
     int col;
     if (!token_group(A, &t, &col)) return;
-    const T* x = (const T*)A.in;
-    T* xs = (T*)A.out;
-    const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>(x + t * A.ld_in + (int64_t)col * V);
-    const int64_t rows = A.tokens * A.slots;
-    const int32_t* place = A.place + t * A.slots;
-#pragma unroll 4
-    for (int64_t k = 0; k < A.slots; ++k) {
-        const int64_t r = place[k];
-        if (r >= 0 && r < rows) *reinterpret_cast<Pack<T, V>*>(xs + r * A.ld_out + (int64_t)col * V) = v;
+    const int64_t at = (int64_t)col * V;
+    const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>((const T*)A.in + t * A.ld_in + at);
+    const int64_t kept = A.offsets[A.experts];
+    T* xs = (T*)A.out + at;
+    for (int64_t k0 = 0; k0 < A.slots; k0 += KC) {
+        int row[KC];
+        slot_rows<KC>(A, t, k0, row);
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+            if (row[k] >= 0) *reinterpret_cast<Pack<T, V>*>(xs + row[k] * A.ld_out) = v;
     }
-    zero_tail<V>(A, xs, A.ld_out, t, col);
+    zero_tail<V>(A, xs, A.ld_out, kept, t);
 }
 
-template <int V, class T>
+template <int V, class T, int KC>
 __global__ __launch_bounds__(256) void lx_combine(MoveArgs A)
 {
     int64_t t;
     int col;
     if (!token_group(A, &t, &col)) return;
-    const T* ys = (const T*)A.in;
-    T* y = (T*)A.out;
-    const int64_t rows = A.tokens * A.slots;
-    const int32_t* place = A.place + t * A.slots;
-    const float* weight = A.weights ? A.weights + t * A.slots : nullptr;
+    const int64_t at = (int64_t)col * V;
+    const T* ys = (const T*)A.in + at;
     float acc[V];
 #pragma unroll
     for (int q = 0; q < V; ++q) acc[q] = 0.f;
-#pragma unroll 4
-    for (int64_t k = 0; k < A.slots; ++k) {
-        const int64_t r = place[k];
-        const bool kept = r >= 0 && r < rows;
-        const float w = weight && kept ? weight[k] : 1.f;
-        float v[V];
-        load_vec<V>(ys + (kept ? r : 0) * A.ld_in + (int64_t)col * V, v);
+    for (int64_t k0 = 0; k0 < A.slots; k0 += KC) {
+        int row[KC];
+        float w[KC];
+        Pack<T, V> v[KC];
+        slot_rows<KC>(A, t, k0, row);
 #pragma unroll
-        for (int q = 0; q < V; ++q) acc[q] = fmaf(w, kept ? v[q] : 0.f, acc[q]);
+        for (int k = 0; k < KC; ++k) {
+            const bool kept = row[k] >= 0;
+            w[k] = A.weights && kept ? A.weights[t * A.slots + k0 + k] : 1.f;
+            // a dropped slot reads row 0 and takes nothing from it
+            v[k] = *reinterpret_cast<const Pack<T, V>*>(ys + (kept ? row[k] : 0) * A.ld_in);
+        }
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+#pragma unroll
+            for (int q = 0; q < V; ++q) acc[q] = row[k] >= 0 ? fmaf(w[k], (float)v[k].v[q], acc[q]) : acc[q];
     }
-    store_vec<V>(y + t * A.ld_out + (int64_t)col * V, acc);
+    store_vec<V>((T*)A.out + t * A.ld_out + at, acc);
 }
 
-// G threads of a 256-thread workgroup per token; up to kDots slots' dot
-// products are carried along one pass over the row.
-constexpr int kDots = 8;
-template <int V, class T, int G>
+// G threads of a 256-thread workgroup per token; the dot products of KC
+// slots are carried along one pass over the row.
+template <int V, class T, int KC, int G>
 __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
 {
-    __shared__ float s_dot[256 / kWave][kDots];
+    __shared__ float s_dot[256 / kWave][KC];
     const int part = (int)threadIdx.x % G;
     const int64_t t = (int64_t)blockIdx.x * (256 / G) + (int)threadIdx.x / G;
     const bool live = t < A.tokens;
     const int lane = lane_id(), w = (int)threadIdx.x / kWave;
-    const T* dy = (const T*)A.dy;
+    const T* dy = (const T*)A.dy + (live ? t : 0) * A.ld_dy;
     const T* ys = (const T*)A.in;
     T* dys = (T*)A.out;
-    const int64_t rows = A.tokens * A.slots;
-    for (int64_t k0 = 0; k0 < A.slots; k0 += kDots) {
-        int64_t row[kDots];
-        float weight[kDots], dot[kDots];
+    for (int64_t k0 = 0; k0 < A.slots; k0 += KC) {
+        int row[KC];
+        float weight[KC], dot[KC];
 #pragma unroll
-        for (int k = 0; k < kDots; ++k) {
-            const bool has = live && k0 + k < A.slots;
-            const int64_t r = has ? A.place[t * A.slots + k0 + k] : -1;
-            row[k] = r >= 0 && r < rows ? r : -1;
+        for (int k = 0; k < KC; ++k) row[k] = -1;
+        if (live) slot_rows<KC>(A, t, k0, row);
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
             weight[k] = row[k] >= 0 && A.weights ? A.weights[t * A.slots + k0 + k] : 0.f;
             dot[k] = 0.f;
         }
         if (live) {
             for (int col = part; col < A.groups; col += G) {
+                const int64_t at = (int64_t)col * V;
+                Pack<T, V> v[KC];
                 float d[V];
-                load_vec<V>(dy + t * A.ld_dy + (int64_t)col * V, d);
+                load_vec<V>(dy + at, d);
+                if (A.dw) {
 #pragma unroll
-                for (int k = 0; k < kDots; ++k) {
-                    if (row[k] < 0) continue;
-                    if (A.dw) {
-                        float v[V];
-                        load_vec<V>(ys + row[k] * A.ld_in + (int64_t)col * V, v);
+                    for (int k = 0; k < KC; ++k)
+                        v[k] = *reinterpret_cast<const Pack<T, V>*>(ys + (row[k] >= 0 ? row[k] : 0) * A.ld_in + at);
+                }
+                if (dys) {
 #pragma unroll
-                        for (int q = 0; q < V; ++q) dot[k] = fmaf(d[q], v[q], dot[k]);
-                    }
-                    if (dys) {
+                    for (int k = 0; k < KC; ++k) {
+                        if (row[k] < 0) continue;
                         float o[V];
 #pragma unroll
                         for (int q = 0; q < V; ++q) o[q] = weight[k] * d[q];
-                        store_vec<V>(dys + row[k] * A.ld_out + (int64_t)col * V, o);
+                        store_vec<V>(dys + row[k] * A.ld_out + at, o);
                     }
+                }
+                if (A.dw) {
+#pragma unroll
+                    for (int k = 0; k < KC; ++k)
+#pragma unroll
+                        for (int q = 0; q < V; ++q)
+                            dot[k] = row[k] >= 0 ? fmaf(d[q], (float)v[k].v[q], dot[k]) : dot[k];
                 }
             }
         }
         if (A.dw) {
 #pragma unroll
-            for (int k = 0; k < kDots; ++k) {
+            for (int k = 0; k < KC; ++k) {
 #pragma unroll
                 for (int m = 1; m < kWave; m <<= 1) dot[k] += __shfl_xor(dot[k], m);
             }
             if (G > kWave) {
                 if (lane == 0) {
 #pragma unroll
-                    for (int k = 0; k < kDots; ++k) s_dot[w][k] = dot[k];
+                    for (int k = 0; k < KC; ++k) s_dot[w][k] = dot[k];
                 }
                 __syncthreads();
-                if ((int)threadIdx.x < kDots && live && k0 + (int)threadIdx.x < A.slots) {
+                if ((int)threadIdx.x < KC && live && k0 + (int)threadIdx.x < A.slots) {
                     float sum = 0.f;
 #pragma unroll
                     for (int i = 0; i < 256 / kWave; ++i) sum += s_dot[i][threadIdx.x];
@@ -372,13 +395,15 @@ __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
                 __syncthreads();
             } else if (lane == 0 && live) {
 #pragma unroll
-                for (int k = 0; k < kDots; ++k)
+                for (int k = 0; k < KC; ++k)
                     if (k0 + k < A.slots) A.dw[t * A.slots + k0 + k] = dot[k];
             }
         }
     }
-    if (dys && live)
-        for (int col = part; col < A.groups; col += G) zero_tail<V>(A, dys, A.ld_out, t, col);
+    if (dys && live) {
+        const int64_t kept = A.offsets[A.experts];
+        for (int col = part; col < A.groups; col += G) zero_tail<V>(A, dys + (int64_t)col * V, A.ld_out, kept, t);
+    }
 }
 
 template <int BITS>
@@ -393,7 +418,7 @@ hipError_t place_launch(const RouteArgs& a, hipStream_t s)
     return hipSuccess;
 }
 
-template <int V, class T>
+template <int V, class T, int KC>
 hipError_t move_launch(MoveKind kind, MoveArgs a, hipStream_t s)
 {
     a.groups = (int)(a.width / V);
@@ -401,21 +426,30 @@ hipError_t move_launch(MoveKind kind, MoveArgs a, hipStream_t s)
     if (blocks > 0x7FFFFFFFll || a.tokens > 0x7FFFFFFFll) return hipErrorInvalidValue;
     switch (kind) {
         case kMoveDispatch:
-            LX_LAUNCH("dispatch", s, (lx_dispatch<V, T><<<(unsigned)blocks, 256, 0, s>>>(a)));
+            LX_LAUNCH("dispatch", s, (lx_dispatch<V, T, KC><<<(unsigned)blocks, 256, 0, s>>>(a)));
             return hipSuccess;
         case kMoveCombine:
-            LX_LAUNCH("combine", s, (lx_combine<V, T><<<(unsigned)blocks, 256, 0, s>>>(a)));
+            LX_LAUNCH("combine", s, (lx_combine<V, T, KC><<<(unsigned)blocks, 256, 0, s>>>(a)));
             return hipSuccess;
         case kMoveCombineGrad:
             // a wave per token while a row is at most two loads per lane
             if (a.groups <= 2 * kWave)
                 LX_LAUNCH("combine_grad", s,
-                          (lx_combine_grad<V, T, 64><<<(unsigned)((a.tokens + 3) / 4), 256, 0, s>>>(a)));
+                          (lx_combine_grad<V, T, KC, 64><<<(unsigned)((a.tokens + 3) / 4), 256, 0, s>>>(a)));
             else
-                LX_LAUNCH("combine_grad", s, (lx_combine_grad<V, T, 256><<<(unsigned)a.tokens, 256, 0, s>>>(a)));
+                LX_LAUNCH("combine_grad", s, (lx_combine_grad<V, T, KC, 256><<<(unsigned)a.tokens, 256, 0, s>>>(a)));
             return hipSuccess;
     }
     return hipErrorInvalidValue;
+}
+
+template <int V, class T>
+hipError_t move_slots(MoveKind kind, const MoveArgs& a, hipStream_t s)
+{
+    // the smallest chunk that holds the token's slots: rows in flight that
+    // are not there cost registers
+    return a.slots <= 2 ? move_launch<V, T, 2>(kind, a, s)
+                        : a.slots <= 4 ? move_launch<V, T, 4>(kind, a, s) : move_launch<V, T, 8>(kind, a, s);
 }
 
 template <class T>
@@ -426,7 +460,7 @@ hipError_t move_type(MoveKind kind, const MoveArgs& a, hipStream_t s)
     // 16 bytes, one value at a time otherwise
     const bool wide = vec_ok(a.in, a.ld_in, a.width, sizeof(T), V) && vec_ok(a.out, a.ld_out, a.width, sizeof(T), V) &&
                       vec_ok(a.dy, a.ld_dy, a.width, sizeof(T), V);
-    return wide ? move_launch<V, T>(kind, a, s) : move_launch<1, T>(kind, a, s);
+    return wide ? move_slots<V, T>(kind, a, s) : move_slots<1, T>(kind, a, s);
 }
 
 }  // namespace

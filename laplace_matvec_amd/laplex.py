@@ -338,20 +338,20 @@ def _rows(t, name, dtype=None, shape=None):
     leading dimensions step evenly through memory."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if dtype is None:
-        if t.dtype not in _DTYPES:
-            raise TypeError(f"{name} must be float32, bfloat16 or float16")
-    elif t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if shape is not None and t.shape != shape:
+    if (t.dtype not in _DTYPES) if dtype is None else (t.dtype is not dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}")
+    sizes = t.shape
+    if shape is not None and sizes != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    width = t.shape[-1]
+    if len(sizes) == 0:
+        raise ValueError(f"{name} must have a last dimension")
+    width = sizes[-1]
     if t.is_contiguous():
-        return t.numel() // max(width, 1), width, max(width, 1)
-    st, sz = t.stride(), t.shape
-    ok = width == 1 or st[-1] == 1
+        return (sizes[0] if len(sizes) == 2 else t.numel() // max(width, 1)), width, max(width, 1)
+    steps = t.stride()
+    ok = width == 1 or steps[-1] == 1
     ld, rows = None, 1  # pitch of the rows so far, from the innermost leading dimension
-    for n, step in zip(reversed(sz[:-1]), reversed(st[:-1])):
+    for n, step in zip(reversed(sizes[:-1]), reversed(steps[:-1])):
         if n != 1:
             if ld is None:
                 ld = step
@@ -368,30 +368,36 @@ def _flat(t, name, dtype, shape, device):
     """A contiguous tensor of one type and shape, or None."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     return t
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+_HERE = contextlib.nullcontext()
 
 
 def _launch(stream, device):
     """(stream handle, context in which outputs and scratch are allocated):
     with a stream other than the current one they come from its own pool."""
     if stream is None:
-        p = torch.cuda.current_stream(device).cuda_stream
-        if device.index == torch.cuda.current_device():
-            return ctypes.c_void_p(p), contextlib.nullcontext()
-        return ctypes.c_void_p(p), torch.cuda.device(device)
+        # the handle alone: a Stream object would cost as much as the launch
+        s = torch._C._cuda_getCurrentRawStream(device.index)
+        return s, _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _at(t):
+    """A tensor's address, None for no tensor."""
+    return None if t is None else t.data_ptr()
+
+
+def _new_like(t):
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _scratch(nbytes, device):
@@ -406,11 +412,14 @@ def _size(value, where):
 
 def _route_parts(route, device):
     place, offsets = route.place, route.offsets
-    for name, t, dim in (("place", place, 2), ("offsets", offsets, 1)):
-        if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and t.dim() == dim
-                and t.is_contiguous()):
-            raise TypeError(f"route.{name} must be a contiguous {dim}-D int32 tensor on {device}")
-    return place, offsets, place.shape[0], place.shape[1], offsets.numel() - 1
+    if not (isinstance(place, torch.Tensor) and place.dtype is torch.int32 and place.device == device
+            and place.dim() == 2 and place.is_contiguous()):
+        raise TypeError(f"route.place must be a contiguous 2-D int32 tensor on {device}")
+    if not (isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.device == device
+            and offsets.dim() == 1 and offsets.is_contiguous()):
+        raise TypeError(f"route.offsets must be a contiguous 1-D int32 tensor on {device}")
+    tokens, slots = place.shape
+    return place, offsets, tokens, slots, offsets.shape[0] - 1
 
 
 def laplex_route(experts, n_experts: int, stream=None) -> Route:
@@ -428,8 +437,8 @@ def laplex_route(experts, n_experts: int, stream=None) -> Route:
         place = torch.empty((tokens, slots), dtype=torch.int32, device=dev)
         offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
         ws = _scratch(need, dev)
-        _check(lib.laplex_route(_ptr(experts), int(experts.dtype == torch.int64), tokens, slots, n_experts,
-                                _ptr(order), _ptr(place), _ptr(offsets), _ptr(ws), need, s), "laplex_route")
+        _check(lib.laplex_route(_at(experts), int(experts.dtype == torch.int64), tokens, slots, n_experts,
+                                _at(order), _at(place), _at(offsets), _at(ws), need, s), "laplex_route")
     return Route(order, place, offsets)
 
 
@@ -443,9 +452,9 @@ def laplex_dispatch(route: Route, x, stream=None):
         raise ValueError(f"x must have shape [{tokens}][width]")
     s, ctx = _launch(stream, x.device)
     with ctx:
-        xs = torch.empty((tokens * slots, width), dtype=x.dtype, device=x.device)
-        _check(load().laplex_dispatch(tokens, slots, experts, _ptr(place), _ptr(offsets), _DTYPES[x.dtype], width,
-                                      _ptr(x), ld, _ptr(xs), width, s), "laplex_dispatch")
+        xs = x.new_empty((tokens * slots, width))
+        _check(load().laplex_dispatch(tokens, slots, experts, _at(place), _at(offsets), _DTYPES[x.dtype], width,
+                                      _at(x), ld, _at(xs), width, s), "laplex_dispatch")
     return xs
 
 
@@ -459,9 +468,9 @@ def laplex_combine(route: Route, ys, weights=None, stream=None):
     weights = _flat(weights, "weights", torch.float32, (tokens, slots), ys.device)
     s, ctx = _launch(stream, ys.device)
     with ctx:
-        y = torch.empty((tokens, width), dtype=ys.dtype, device=ys.device)
-        _check(load().laplex_combine(tokens, slots, _ptr(place), _DTYPES[ys.dtype], width, _ptr(ys), ld,
-                                     _ptr(weights), _ptr(y), width, s), "laplex_combine")
+        y = ys.new_empty((tokens, width))
+        _check(load().laplex_combine(tokens, slots, _at(place), _DTYPES[ys.dtype], width, _at(ys), ld,
+                                     _at(weights), _at(y), width, s), "laplex_combine")
     return y
 
 
@@ -472,17 +481,18 @@ def laplex_combine_backward(route: Route, dy, ys, weights, stream=None):
     if dy.dim() != 2 or rows != tokens:
         raise ValueError(f"dy must have shape [{tokens}][width]")
     _, _, ldys = _rows(ys, "ys", dy.dtype, (tokens * slots, width))
-    _same_device(dy.device, ys=ys)
+    if ys.device != dy.device:
+        raise ValueError(f"ys must be on {dy.device}")
     if weights is None:
         raise TypeError("weights must be given")
     weights = _flat(weights, "weights", torch.float32, (tokens, slots), dy.device)
     s, ctx = _launch(stream, dy.device)
     with ctx:
-        dys = torch.empty((tokens * slots, width), dtype=dy.dtype, device=dy.device)
-        dw = torch.empty((tokens, slots), dtype=torch.float32, device=dy.device)
-        _check(load().laplex_combine_backward(tokens, slots, experts, _ptr(place), _ptr(offsets), _DTYPES[dy.dtype],
-                                              width, _ptr(dy), ld, _ptr(ys), ldys, _ptr(weights), _ptr(dys), width,
-                                              _ptr(dw), s), "laplex_combine_backward")
+        dys = dy.new_empty((tokens * slots, width))
+        dw = weights.new_empty((tokens, slots))
+        _check(load().laplex_combine_backward(tokens, slots, experts, _at(place), _at(offsets), _DTYPES[dy.dtype],
+                                              width, _at(dy), ld, _at(ys), ldys, _at(weights), _at(dys), width,
+                                              _at(dw), s), "laplex_combine_backward")
     return dys, dw
 
 
@@ -506,7 +516,8 @@ def _recur_parts(x, g, offsets, h0):
         seqs = offsets.numel() - 1
     else:
         seqs = x.shape[0] if x.dim() == 3 else 1
-    _same_device(dev, g=g)
+    if g.device != dev:
+        raise ValueError(f"g must be on {dev}")
     _flat(h0, "h0", torch.float32, (seqs, width), dev)
     return n, seqs, width, heads, ldx, ldg
 
@@ -524,19 +535,14 @@ def laplex_recur(x, g, offsets=None, h0=None, final: bool = False, keep: bool = 
     need = _size(lib.laplex_recur_workspace(n, width, heads, 0), "laplex_recur")
     s, ctx = _launch(stream, dev)
     with ctx:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _new_like(x)
         hf = torch.empty((seqs, width), dtype=torch.float32, device=dev) if final else None
         states = torch.empty(lib.laplex_recur_states(n, width), dtype=torch.float32, device=dev) if keep else None
         ws = _scratch(need, dev)
-        _check(lib.laplex_recur(n, seqs, _ptr(offsets), width, heads, _DTYPES[x.dtype], _DTYPES[g.dtype], _ptr(x), ldx,
-                                _ptr(g), ldg, _ptr(h0), _ptr(y), width, _ptr(hf), _some(states), _ptr(ws), need, s),
+        _check(lib.laplex_recur(n, seqs, _at(offsets), width, heads, _DTYPES[x.dtype], _DTYPES[g.dtype], _at(x), ldx,
+                                _at(g), ldg, _at(h0), _at(y), width, _at(hf), _at(states), _at(ws), need, s),
                "laplex_recur")
     return Recurrence(y, hf, states)
-
-
-def _some(t):
-    """A tensor's pointer, None if it has no values."""
-    return None if t is None or t.numel() == 0 else ctypes.c_void_p(t.data_ptr())
 
 
 def laplex_recur_backward(x, g, dy, states, offsets=None, h0=None, dfinal=None, want=("dx", "dg", "dh0"),
@@ -548,7 +554,8 @@ def laplex_recur_backward(x, g, dy, states, offsets=None, h0=None, dfinal=None, 
     n, seqs, width, heads, ldx, ldg = _recur_parts(x, g, offsets, h0)
     dev = x.device
     _, _, lddy = _rows(dy, "dy", x.dtype, x.shape)
-    _same_device(dev, dy=dy)
+    if dy.device != dev:
+        raise ValueError(f"dy must be on {dev}")
     lib = load()
     need = _size(lib.laplex_recur_workspace(n, width, heads, 1), "laplex_recur_backward")
     if not isinstance(states, torch.Tensor):
@@ -559,16 +566,16 @@ def laplex_recur_backward(x, g, dy, states, offsets=None, h0=None, dfinal=None, 
     out = {}
     with ctx:
         if "dx" in want:
-            out["dx"] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            out["dx"] = _new_like(x)
         if "dg" in want:
-            out["dg"] = torch.empty(g.shape, dtype=g.dtype, device=dev)
+            out["dg"] = _new_like(g)
         if "dh0" in want:
             out["dh0"] = torch.empty((seqs, width), dtype=torch.float32, device=dev)
         ws = _scratch(need, dev)
-        _check(lib.laplex_recur_backward(n, seqs, _ptr(offsets), width, heads, _DTYPES[x.dtype], _DTYPES[g.dtype],
-                                         _ptr(x), ldx, _ptr(g), ldg, _ptr(h0), _some(states), _ptr(dy), lddy,
-                                         _ptr(dfinal), _ptr(out.get("dx")), width, _ptr(out.get("dg")), heads,
-                                         _ptr(out.get("dh0")), _ptr(ws), need, s), "laplex_recur_backward")
+        _check(lib.laplex_recur_backward(n, seqs, _at(offsets), width, heads, _DTYPES[x.dtype], _DTYPES[g.dtype],
+                                         _at(x), ldx, _at(g), ldg, _at(h0), _at(states), _at(dy), lddy,
+                                         _at(dfinal), _at(out.get("dx")), width, _at(out.get("dg")), heads,
+                                         _at(out.get("dh0")), _at(ws), need, s), "laplex_recur_backward")
     return out
 
 
@@ -590,12 +597,13 @@ def laplex_recur_step(x, g, state, slots=None, stream=None):
         raise TypeError("state must be a float32 tensor [pool][width]")
     _flat(state, "state", torch.float32, (state.shape[0], width), dev)
     _flat(slots, "slots", torch.int32, (n,), dev)
-    _same_device(dev, g=g)
+    if g.device != dev:
+        raise ValueError(f"g must be on {dev}")
     s, ctx = _launch(stream, dev)
     with ctx:
-        y = torch.empty((n, width), dtype=x.dtype, device=dev)
-        _check(load().laplex_recur_step(n, state.shape[0], _ptr(slots), width, heads, _DTYPES[x.dtype],
-                                        _DTYPES[g.dtype], _ptr(x), ldx, _ptr(g), ldg, _ptr(state), _ptr(y), width, s),
+        y = _new_like(x)
+        _check(load().laplex_recur_step(n, state.shape[0], _at(slots), width, heads, _DTYPES[x.dtype],
+                                        _DTYPES[g.dtype], _at(x), ldx, _at(g), ldg, _at(state), _at(y), width, s),
                "laplex_recur_step")
     return y
 
