@@ -1717,6 +1717,9 @@ const char* recur_common(lx::RecurArgs& A, int64_t n, int64_t seqs, const int32_
     A.width = (int)width;
     A.heads = (int)heads;
     A.per = (int)(width / heads);
+    // an array as large as the last-level cache (256 MB) is out of it again
+    // before anyone else reads it
+    A.stream = (double)n * (double)width * (double)dtype_size(type) >= 268435456.0;
     A.tiles = tiles;
     A.cols = (int)cols;
     A.x = x;

@@ -401,6 +401,7 @@ struct RecurArgs {
     int64_t seq_len = 0;   // rows of each, without offsets
     const int32_t* offsets = nullptr;  // [seqs + 1], or null: equal sequences
     int width = 0, heads = 0, per = 0;  // channels, decays per row, channels per decay
+    bool stream = false;   // rows go past the caches
     int64_t tiles = 0;     // row tiles
     int cols = 0;          // channel tiles
     const void* x = nullptr;

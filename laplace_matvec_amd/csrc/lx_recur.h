@@ -155,32 +155,23 @@ struct RowAt {
     __device__ __forceinline__ T* any_row(int64_t j) const { return reinterpret_cast<T*>(base + j * pitch + off); }
 };
 
-// What holds N bytes of a row: a register tuple as it is loaded.
-template <int N>
-struct RowWord;
-template <>
-struct RowWord<2> { typedef uint16_t Mem; typedef uint32_t Reg; };
-template <>
-struct RowWord<4> { typedef uint32_t Mem; typedef uint32_t Reg; };
-template <>
-struct RowWord<8> { typedef uint32_t Mem __attribute__((ext_vector_type(2))); typedef Mem Reg; };
-template <>
-struct RowWord<16> { typedef uint32_t Mem __attribute__((ext_vector_type(4))); typedef Mem Reg; };
-
 // L rows of V channels of one array as stored (a vector of 16-bit values
 // would be taken apart into a register for each).
 template <class T, int V, int L>
 struct RowPack {
     static constexpr int kBytes = V * (int)sizeof(T);
-    typedef typename RowWord<kBytes>::Mem Mem;
-    typedef typename RowWord<kBytes>::Reg Reg;
+    typedef typename Words<kBytes>::T Mem;
+    typedef typename Words<kBytes == 2 ? 4 : kBytes>::T Reg;  // a register tuple as it is loaded
     Reg w[L];
 
     // whole: all of the tile's rows are there; else the last one (`last`
     // from the thread's first, perhaps before it) stands for those past it
-    __device__ __forceinline__ void load(const RowAt<T, V>& at, bool whole, int64_t last)
+    __device__ __forceinline__ void load(const RowAt<T, V>& at, bool whole, int64_t last, bool once)
     {
-        if (whole) {
+        if (whole && once) {
+#pragma unroll
+            for (int j = 0; j < L; ++j) w[j] = __builtin_nontemporal_load(reinterpret_cast<const Mem*>(at.row(j)));
+        } else if (whole) {
 #pragma unroll
             for (int j = 0; j < L; ++j) w[j] = *reinterpret_cast<const Mem*>(at.row(j));
         } else {
@@ -258,8 +249,8 @@ struct RecurThread {
         whole = (tile + 1) * kRecurTile <= A.n;
         last = A.n - 1 - wave_row - lane_row;
         rows = !in || last < 0 ? 0 : (last < L - 1 ? (int)last + 1 : L);
-        x.load(at<T, V>(A.x, A.ldx), whole, last);
-        g.load(gate_at<TG>(A, A.g, A.ldg), whole, last);
+        x.load(at<T, V>(A.x, A.ldx), whole, last, A.stream);
+        g.load(gate_at<TG>(A, A.g, A.ldg), whole, last, A.stream && !SH);  // a shared decay is read by many tiles
     }
     __device__ __forceinline__ int col() const { return tile_col + lane * V; }
     template <class U, int N>

@@ -18,7 +18,10 @@ __device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* 
         float a[Th::D];
         th.template decays<CARE>(R, j, a);
         th.template step<CARE>(A, R, j, a, h);
-        if (CARE == kCareRows ? j < th.rows : th.in) store_vec<V>(y.row(j), h);
+        if (CARE == kCareRows ? j < th.rows : th.in) {
+            if (A.stream) store_vec_once<V>(y.row(j), h);
+            else store_vec<V>(y.row(j), h);
+        }
         if (th.template special<CARE>(j) && A.final && th.in) {
             const int q = R->last[th.r0 + j];
             if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col(), h);

@@ -140,9 +140,15 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             }
         }
         if (CARE) settle(w);
-        if (A.dx && here) store_vec<V>(dx.row(j), u);
+        if (A.dx && here) {
+            if (A.stream) store_vec_once<V>(dx.row(j), u);
+            else store_vec<V>(dx.row(j), u);
+        }
         if (own) {
-            if (A.dg && here) store_vec<V>(dg.row(j), p);
+            if (A.dg && here) {
+                if (A.stream) store_vec_once<V>(dg.row(j), p);
+                else store_vec<V>(dg.row(j), p);
+            }
         } else if (V > 1) {
             float sum = 0.f;
 #pragma unroll
@@ -195,7 +201,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
     Th th;
     RowPack<T, V, L> dy;
     th.load(A, tile, ct);
-    dy.load(th.template at<T, V>(A.dy, A.lddy), th.whole, th.last);
+    dy.load(th.template at<T, V>(A.dy, A.lddy), th.whole, th.last, A.stream);
     const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows)) ? &rows : nullptr;
     float m[Th::D], h[V], w[V];
     int care = th.find_odd(R) ? kCareRows : kCareNone;
