@@ -1730,9 +1730,9 @@ const char* recur_common(lx::RecurArgs& A, int64_t n, int64_t seqs, const int32_
     return nullptr;
 }
 
-// Scratch of a pass: 256 bytes with the ticket, the maps, the states; none
-// for a single row tile.
-constexpr size_t kTicketBytes = 256;
+// Scratch of a pass: tickets, marks, maps, states; none for a single row tile.
+size_t recur_ticket_bytes(int64_t width) { return align256((size_t)recur_cols(width) * lx::kRecurTicketPitch * 4); }
+size_t recur_mark_bytes(int64_t n) { return align256((size_t)recur_tiles(n) * 4); }
 size_t recur_map_bytes(int64_t n, int64_t width)
 {
     const int64_t t = recur_tiles(n);
@@ -1741,14 +1741,17 @@ size_t recur_map_bytes(int64_t n, int64_t width)
 size_t recur_pass_bytes(int64_t n, int64_t width)
 {
     const size_t m = recur_map_bytes(n, width);
-    return m ? kTicketBytes + m + align256(m / 2) : 0;
+    return m ? recur_ticket_bytes(width) + recur_mark_bytes(n) + m + align256(m / 2) : 0;
 }
 void recur_scratch(lx::RecurArgs& A, void* ws)
 {
-    const size_t m = recur_map_bytes(A.n, A.width);
-    A.ticket = (uint32_t*)ws;
-    A.maps = (uint64_t*)((char*)ws + kTicketBytes);
-    A.states = (uint32_t*)((char*)ws + kTicketBytes + m);
+    char* p = (char*)ws;
+    A.tickets = (uint32_t*)p;
+    p += recur_ticket_bytes(A.width);
+    A.marks = (int32_t*)p;
+    p += recur_mark_bytes(A.n);
+    A.maps = (uint64_t*)p;
+    A.states = (uint32_t*)(p + recur_map_bytes(A.n, A.width));
     A.part = (float*)((char*)ws + recur_pass_bytes(A.n, A.width));
 }
 

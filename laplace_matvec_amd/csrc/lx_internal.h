@@ -394,6 +394,7 @@ hipError_t move_rows_launch(MoveKind kind, int dtype, const MoveArgs& a, hipStre
 // ---- gated recurrence (recur.hip, recur_grad.hip) ----
 constexpr int kRecurTile = 256;  // rows of a tile
 constexpr int kRecurCols = 64;   // channels of a tile
+constexpr int kRecurTicketPitch = 32;  // words: each counter on a line of its own
 constexpr int64_t kRecurMaxPitch = (int64_t)1 << 24;  // values between rows
 struct RecurArgs {
     int64_t n = 0;         // rows
@@ -421,7 +422,8 @@ struct RecurArgs {
     int64_t lddx = 0, lddg = 0;
     float* dh0 = nullptr;       // [seqs][width]
     // scratch: [tiles - 1][cols * kRecurCols] each, in the order of the pass
-    uint32_t* ticket = nullptr;
+    uint32_t* tickets = nullptr;  // [cols], kRecurTicketPitch apart
+    int32_t* marks = nullptr;     // [tiles], packed only: see lx_recur.h
     uint64_t* maps = nullptr;   // composed map of each row tile
     uint32_t* states = nullptr; // bits of the state after each row tile (backward: gradient before)
     float* part = nullptr;      // backward: [n][cols + heads] sums of dg within a channel tile

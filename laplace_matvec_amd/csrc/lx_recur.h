@@ -51,37 +51,24 @@ struct RecurRows {
     uint64_t odd[kRecurTile / kWave];  // bit per row: either of them is not -1
 };
 
-// Index of the first of n values that is not below `key` (values ascend),
-// 64 probes at a time; the same in every lane.  For values in any order the
-// result is still in [0, n].
-__device__ __forceinline__ int64_t lower_bound64(const int32_t* v, int64_t n, int64_t key)
+// Packed sequences: the first offset at or past a tile's first row, or -1 if
+// the tile has no special rows.  Made for all tiles before the pass (a search
+// in the pass would wait behind its row loads); a single tile starts at 0.
+__device__ __forceinline__ int tile_mark(const RecurArgs& A, int64_t tile)
 {
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-        const int64_t step = (hi - lo + kWave - 1) / kWave;
-        const int64_t at = lo + (int64_t)lane_id() * step;
-        const bool below = at < hi && (int64_t)v[at] < key;
-        const int c = __builtin_amdgcn_readfirstlane(__popcll(__ballot(below)));
-        if (c == 0) break;
-        const int64_t next = lo + (int64_t)c * step;
-        lo += (int64_t)(c - 1) * step + 1;
-        if (next < hi) hi = next;
-        if (step == 1) break;
-    }
-    return lo;
+    return !A.offsets || A.tiles <= 1 ? 0 : A.marks[tile];
 }
 
 // Whether the tile of rows [t0, t0 + kRecurTile) has special rows; then R
 // says which.  All threads; has barriers only if it returns true.
+// `mark` is the tile's of tile_mark().
 template <int THREADS>
-__device__ __forceinline__ bool recur_rows(const RecurArgs& A, int64_t t0, RecurRows& R)
+__device__ __forceinline__ bool recur_rows(const RecurArgs& A, int64_t t0, int mark, RecurRows& R)
 {
     static_assert(THREADS >= kRecurTile, "a thread per row");
     const int64_t end = t0 + kRecurTile;
-    int64_t q_first = 0;  // packed: first offset at or past t0
     if (A.offsets) {
-        q_first = lower_bound64(A.offsets, A.seqs + 1, t0);  // the same in every wave
-        if (end <= A.n && q_first > 0 && q_first <= A.seqs && (int64_t)A.offsets[q_first] > end) return false;
+        if (mark < 0) return false;
     } else {
         const int64_t at = A.seqs == 1 ? t0 : t0 % A.seq_len;
         if (end <= A.n && at != 0 && at + kRecurTile < A.seq_len) return false;
@@ -106,7 +93,7 @@ __device__ __forceinline__ bool recur_rows(const RecurArgs& A, int64_t t0, Recur
     __syncthreads();
     if (A.offsets) {
         // one wave: the offsets in [t0, end], 64 at a time
-        for (int64_t q0 = q_first; tid < kWave && q0 <= A.seqs; q0 += kWave) {
+        for (int64_t q0 = mark; tid < kWave && q0 <= A.seqs; q0 += kWave) {
             const int64_t q = q0 + tid;
             const int64_t o = q <= A.seqs ? (int64_t)A.offsets[q] : end + 1;
             if (o >= t0 && o <= end) {
@@ -346,8 +333,8 @@ __device__ __forceinline__ bool any_zero(const float (&m)[D])
 
 // ---- between tiles -------------------------------------------------------
 //
-// One pass over the data: a workgroup takes the next tile of the pass
-// (ticket order, so the tiles before it have been taken too and their
+// One pass over the data: a workgroup takes the next row tile of its channel
+// tile (in ticket order, so those before it have been taken too and their
 // workgroups run), composes its rows' maps, publishes the tile's map
 // h -> A h + H, finds the state that enters it and publishes the state that
 // leaves it.  Words say by themselves whether they have been written: all
@@ -426,17 +413,31 @@ __device__ __forceinline__ float pass_state(const RecurArgs& A, int64_t tile, in
     return in;
 }
 
-// The next tile of the pass.  All threads; has a barrier.
-__device__ __forceinline__ uint32_t next_tile(uint32_t* ticket)
+// The workgroup's channel tile.  Workgroup b runs on die b % 8; taken as they
+// come, each die would keep to every eighth tile's 128 bytes of a row, which
+// use a quarter of its L2's channels.  One tile further in each round of the
+// channels spreads every die over all of them.
+__device__ __forceinline__ int channel_tile(const RecurArgs& A)
+{
+    const uint32_t cols = (uint32_t)A.cols, round = blockIdx.x / cols;
+    return (int)((blockIdx.x - round * cols + round) % cols);
+}
+
+// The workgroup's row tile in the order of the pass: the next of its channel
+// tile (a counter for each: one for all made the first of 1280 workgroups
+// wait up to 10 us for their turns).  All threads; has a barrier.
+__device__ __forceinline__ uint32_t next_tile(const RecurArgs& A, int ct)
 {
     __shared__ uint32_t s_ticket;
-    if (threadIdx.x == 0) s_ticket = atomicAdd(ticket, 1u);
+    if (A.tiles <= 1) return 0;
+    if (threadIdx.x == 0) s_ticket = atomicAdd(A.tickets + (int64_t)ct * kRecurTicketPitch, 1u);
     __syncthreads();
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)s_ticket);
 }
 
-// Clears what a pass publishes (with more than one tile) and gives sequences
-// without rows their result: to[q] = from[q], or 0 without `from`.
+// Clears what a pass publishes and marks the tiles (with more than one tile),
+// and gives sequences without rows their result: to[q] = from[q], or 0
+// without `from`.
 hipError_t recur_begin(const RecurArgs& a, const float* from, float* to, hipStream_t s);
 
 }  // namespace lx

@@ -37,12 +37,12 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     __shared__ RecurRows rows;
     __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
     __shared__ float sh[Lay::kGroups][kRecurCols];
-    const uint32_t turn = A.tiles > 1 ? next_tile(A.ticket) : blockIdx.x;
-    const int64_t tile = turn / (uint32_t)A.cols;
-    const int ct = (int)(turn % (uint32_t)A.cols);
+    const int ct = channel_tile(A);
+    const int64_t tile = next_tile(A, ct);
+    const int mark = tile_mark(A, tile);
     Th th;
     th.load(A, tile, ct);
-    const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows)) ? &rows : nullptr;
+    const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, mark, rows)) ? &rows : nullptr;
     float m[Th::D], h[V];
     int care = th.find_odd(R) ? kCareRows : kCareNone;
     if (care == kCareNone) {
@@ -83,7 +83,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
 }
 
 // Blocks [0, fill): 16 bytes of all ones per thread over the published
-// words; the rest: one sequence each.
+// words, the tickets and the marks; the rest: one sequence each.
 __global__ __launch_bounds__(256) void lx_recur_begin(RecurArgs A, int64_t maps16, int64_t states16, unsigned fill,
                                                       const float* __restrict__ from, float* __restrict__ to)
 {
@@ -92,7 +92,18 @@ __global__ __launch_bounds__(256) void lx_recur_begin(RecurArgs A, int64_t maps1
         const uint4 ones = make_uint4(~0u, ~0u, ~0u, ~0u);
         if (i < maps16) reinterpret_cast<uint4*>(A.maps)[i] = ones;
         else if (i - maps16 < states16) reinterpret_cast<uint4*>(A.states)[i - maps16] = ones;
-        if (i == 0) *A.ticket = 0;
+        if (i < A.cols) A.tickets[i * kRecurTicketPitch] = 0;
+        if (A.offsets && i < A.tiles) {
+            const int64_t t0 = i * kRecurTile, end = t0 + kRecurTile;
+            int64_t lo = 0, hi = A.seqs + 1;  // the first offset at or past t0
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) / 2;
+                if ((int64_t)A.offsets[mid] < t0) lo = mid + 1;
+                else hi = mid;
+            }
+            const bool plain = end <= A.n && lo > 0 && lo <= A.seqs && (int64_t)A.offsets[lo] > end;
+            A.marks[i] = plain ? -1 : (int)lo;
+        }
         return;
     }
     const int64_t q = blockIdx.x - fill;

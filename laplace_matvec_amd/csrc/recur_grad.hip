@@ -183,8 +183,16 @@ __device__ __forceinline__ void tile_sums(const RecurArgs& A, int64_t tile, int 
     }
 }
 
+// Waves per SIMD to compile for: 4, two workgroups per CU, also where that
+// spills a few registers (bf16 rows with float32 decays of their own 380 ->
+// 308 us at 4 x 8192 x 4096, shared float32 330 -> 277); float32 rows with
+// decays of their own would spill too many (461 -> 549).
+template <class T, bool SH>
+constexpr int kGradWaves = sizeof(T) == 4 && !SH ? 2 : 4;
+
 template <class T, class TG, int V, int L, bool SH>
-__global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_pass(RecurArgs A)
+__global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
+    amdgpu_waves_per_eu((kGradWaves<T, SH>)))) void lx_recur_grad_pass(RecurArgs A)
 {
     using Th = RecurThread<T, TG, V, L, SH>;
     using Lay = RecurLayout<V, L>;
@@ -194,15 +202,15 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_grad_p
     __shared__ float sw[Lay::kGroups][kRecurCols];
     constexpr bool kSums = SH && V > 1;
     __shared__ float s_sum[kSums ? kRecurTile : 1][kSumPitch];
-    const uint32_t turn = A.tiles > 1 ? next_tile(A.ticket) : blockIdx.x;
-    const int64_t back = turn / (uint32_t)A.cols;  // tiles before this one in the pass: from the last rows on
+    const int ct = channel_tile(A);
+    const int64_t back = next_tile(A, ct);  // tiles before this one in the pass: from the last rows on
     const int64_t tile = A.tiles - 1 - back;
-    const int ct = (int)(turn % (uint32_t)A.cols);
+    const int mark = tile_mark(A, tile);
     Th th;
     RowPack<T, V, L> dy;
     th.load(A, tile, ct);
     dy.load(th.template at<T, V>(A.dy, A.lddy), th.whole, th.last, A.stream);
-    const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, rows)) ? &rows : nullptr;
+    const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, mark, rows)) ? &rows : nullptr;
     float m[Th::D], h[V], w[V];
     int care = th.find_odd(R) ? kCareRows : kCareNone;
     if (care == kCareNone) {
