@@ -183,12 +183,17 @@ __device__ __forceinline__ void tile_sums(const RecurArgs& A, int64_t tile, int 
     }
 }
 
-// Waves per SIMD to compile for: 4, two workgroups per CU, also where that
-// spills a few registers (bf16 rows with float32 decays of their own 380 ->
-// 308 us at 4 x 8192 x 4096, shared float32 330 -> 277); float32 rows with
-// decays of their own would spill too many (461 -> 549).
+// Rows of a thread and waves per SIMD to compile for.  What counts is bytes
+// in flight per CU: half rows with shared decays take 16 rows per thread,
+// three workgroups of 256 threads (225 -> 205 us packed 32768 x 4096); the
+// others 8 rows, two workgroups of 512, also where that spills a few
+// registers (bf16 rows with float32 decays of their own 380 -> 308 us at
+// 4 x 8192 x 4096, shared float32 330 -> 277).  float32 rows with decays of
+// their own would spill too many (461 -> 549).
 template <class T, bool SH>
-constexpr int kGradWaves = sizeof(T) == 4 && !SH ? 2 : 4;
+constexpr int kGradRows = sizeof(T) == 2 && SH ? 16 : 8;
+template <class T, bool SH>
+constexpr int kGradWaves = !SH ? (sizeof(T) == 4 ? 2 : 4) : (sizeof(T) == 2 ? 3 : 4);
 
 template <class T, class TG, int V, int L, bool SH>
 __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
@@ -310,7 +315,9 @@ hipError_t grad_type(const RecurArgs& a, hipStream_t s)
                       vec_ok(a.dfinal, a.width, a.width, 4, 4) && vec_ok(a.dh0, a.width, a.width, 4, 4) &&
                       (sh ? a.per % 4 == 0
                           : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4) && vec_ok(a.dg, a.lddg, a.width, sizeof(TG), 4));
-    if (wide) return sh ? grad_go<T, TG, 4, 8, true>(a, s) : grad_go<T, TG, 4, 8, false>(a, s);
+    if (wide)
+        return sh ? grad_go<T, TG, 4, kGradRows<T, true>, true>(a, s)
+                  : grad_go<T, TG, 4, kGradRows<T, false>, false>(a, s);
     return grad_go<T, TG, 1, 16, true>(a, s);
 }
 
