@@ -1763,7 +1763,7 @@ int64_t laplex_route_workspace(int64_t tokens, int64_t slots, int64_t n_experts)
 {
     if (!route_sizes_ok(tokens, slots) || n_experts < 1 || n_experts > lx::kRouteMaxExperts) return -1;
     const int64_t tiles = (tokens * slots + lx::kRouteTile - 1) / lx::kRouteTile;
-    return tiles > 1 ? (tiles + 1) * n_experts * 4 : 0;
+    return tokens * slots > lx::kRouteSingle ? (tiles + 1) * n_experts * 4 : 0;
 }
 
 laplex_status laplex_route(const void* experts, int wide, int64_t tokens, int64_t slots, int64_t n_experts,

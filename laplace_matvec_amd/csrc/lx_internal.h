@@ -359,7 +359,8 @@ hipError_t gram_ranks_launch(const uint32_t* perm, int64_t n, uint32_t* rank, hi
 hipError_t gram_launch(const GramArgs& a, hipStream_t s);
 
 // ---- token routing (route.hip) ----
-constexpr int kRouteTile = 4096;        // slots per workgroup
+constexpr int kRouteTile = 2048;        // slots per workgroup
+constexpr int kRouteSingle = 4096;      // slots up to which one workgroup does everything
 constexpr int kRouteMaxExperts = 4096;  // 80 KB of counters in LDS
 struct RouteArgs {
     const void* ids = nullptr;  // [n] int32, or int64 if wide

@@ -9,12 +9,16 @@
 // row; order is -1 past the last row.  No atomics on global memory, so the
 // result does not depend on the order in which workgroups run.
 //
-// Ranking: a workgroup takes kRouteTile consecutive slots, each wave a
-// quarter of them in order, 64 at a time; lanes of one id find each other by
-// ballots over the id's bits and count the lanes below, a counter per wave
-// and id in LDS carries the rest.  Up to kRouteTile slots one launch does
-// everything; above, the tiles' counts are scanned along the tiles between
-// two launches (the scan has E columns of `tiles` counts).
+// Ranking: a workgroup takes a tile of consecutive slots, each wave a quarter
+// of them in order, 64 at a time; lanes of one id find each other by ballots
+// over the id's bits and count the lanes below, a counter per wave and id in
+// LDS carries the rest.  Up to kRouteSingle slots one launch does everything
+// (bound by its latency: 13 us a call with the host's part); above, tiles of
+// kRouteTile slots are counted, their counts scanned along the tiles (E
+// columns of `tiles` counts) and the slots placed, three launches.  A wave's
+// rounds wait for each other's counters, so shorter tiles, more of them at a
+// time, are faster: 2^20 slots, 256 experts, 28 us at 4096 slots a tile, 24
+// at 2048, 26 at 1024 (the scan grows).
 //
 // The data movement has one thread per token and 16 bytes of its row, so a
 // token's row is read (written) once and its K copies are in flight together:
@@ -38,7 +42,6 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWaves = kRouteThreads / kWave;
-constexpr int kRouteRounds = kRouteTile / kRouteThreads;  // 64-slot rounds per wave
 
 __device__ __forceinline__ int route_id(const void* ids, int wide, int64_t s, int experts)
 {
@@ -55,7 +58,7 @@ __global__ __launch_bounds__(kRouteThreads) void lx_route_count(RouteArgs A)
     __syncthreads();
     const int64_t s0 = (int64_t)blockIdx.x * kRouteTile + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < kRouteRounds; ++j) {
+    for (int j = 0; j < kRouteTile / kRouteThreads; ++j) {
         const int64_t s = s0 + j * kRouteThreads;
         const int id = s < A.n ? route_id(A.ids, A.wide, s, E) : -1;
         if (id >= 0) atomicAdd(&s_cnt[id], 1u);
@@ -66,11 +69,11 @@ __global__ __launch_bounds__(kRouteThreads) void lx_route_count(RouteArgs A)
 }
 
 // Exclusive scan of hist along the tiles, in place; total[e] the column sum.
-// A workgroup has 16 columns by 64 runs of 4 tiles.
+// A workgroup has 16 columns by 64 runs of 8 tiles.
 constexpr int kColThreads = 1024;
 constexpr int kCols = 16;
 constexpr int kRuns = kColThreads / kCols;
-constexpr int kRunLen = 4;
+constexpr int kRunLen = 8;
 __global__ __launch_bounds__(kColThreads) void lx_route_scan(RouteArgs A)
 {
     __shared__ uint32_t s_run[kRuns][kCols];
@@ -154,20 +157,22 @@ __device__ __forceinline__ uint32_t scan_experts(uint32_t* s_base, uint32_t* s_w
 template <int BITS, bool SINGLE>
 __global__ __launch_bounds__(kRouteThreads) void lx_route_place(RouteArgs A)
 {
+    constexpr int kTile = SINGLE ? kRouteSingle : kRouteTile;
+    constexpr int kRounds = kTile / kRouteThreads;  // of 64 slots per wave
     extern __shared__ uint32_t s_dyn[];
     __shared__ uint32_t s_wave[kRouteWaves];
     const int E = A.experts;
     uint32_t* cnt = s_dyn;
     uint32_t* base = s_dyn + kRouteWaves * E;
     const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
-    const int64_t tile0 = (int64_t)blockIdx.x * kRouteTile;
+    const int64_t tile0 = (int64_t)blockIdx.x * kTile;
     const int64_t left = A.n - tile0;
-    const int room = (int)(left < kRouteTile ? left : kRouteTile);  // slots of this tile
-    const int w0 = w * (kRouteTile / kRouteWaves);
+    const int room = (int)(left < kTile ? left : kTile);  // slots of this tile
+    const int w0 = w * (kTile / kRouteWaves);
 
-    int id[kRouteRounds];
+    int id[kRounds];
 #pragma unroll
-    for (int j = 0; j < kRouteRounds; ++j) {
+    for (int j = 0; j < kRounds; ++j) {
         const int i = w0 + j * kWave + lane;
         id[j] = i < room ? route_id(A.ids, A.wide, tile0 + i, E) : -1;
     }
@@ -178,10 +183,10 @@ __global__ __launch_bounds__(kRouteThreads) void lx_route_place(RouteArgs A)
 
     // rank within the wave's quarter, 64 slots at a time; one wave alone
     // touches its counters, in order
-    uint32_t rank[kRouteRounds];
+    uint32_t rank[kRounds];
     uint32_t* mine = cnt + w * E;
 #pragma unroll
-    for (int j = 0; j < kRouteRounds; ++j) {
+    for (int j = 0; j < kRounds; ++j) {
         rank[j] = 0;
         if (w0 + j * kWave < room) {
             const uint64_t kept = __ballot(id[j] >= 0);
@@ -221,7 +226,7 @@ __global__ __launch_bounds__(kRouteThreads) void lx_route_place(RouteArgs A)
         __syncthreads();
     }
 #pragma unroll
-    for (int j = 0; j < kRouteRounds; ++j) {
+    for (int j = 0; j < kRounds; ++j) {
         const int i = w0 + j * kWave + lane;
         if (i < room) {
             int p = -1;
@@ -416,7 +421,7 @@ template <int BITS>
 hipError_t place_launch(const RouteArgs& a, hipStream_t s)
 {
     const size_t lds = (size_t)(kRouteWaves + 1) * a.experts * 4;
-    if (a.tiles <= 1) {
+    if (a.n <= kRouteSingle) {
         LX_LAUNCH("route", s, (lx_route_place<BITS, true><<<1, kRouteThreads, lds, s>>>(a)));
         return hipSuccess;
     }
@@ -473,7 +478,7 @@ hipError_t move_type(MoveKind kind, const MoveArgs& a, hipStream_t s)
 
 hipError_t route_launch(const RouteArgs& a, hipStream_t s)
 {
-    if (a.tiles > 1) {
+    if (a.n > kRouteSingle) {
         LX_LAUNCH("route_count", s,
                   (lx_route_count<<<(unsigned)a.tiles, kRouteThreads, (size_t)a.experts * 4, s>>>(a)));
         LX_LAUNCH("route_scan", s, (lx_route_scan<<<(unsigned)((a.experts + kCols - 1) / kCols), kColThreads, 0, s>>>(a)));
