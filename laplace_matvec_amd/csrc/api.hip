@@ -48,14 +48,17 @@ laplex_status fail(laplex_status st, const char* msg) noexcept
     return st;
 }
 
-laplex_status from_hip(hipError_t e, const char* where)
+laplex_status from_hip(hipError_t e, const char* where) noexcept
 {
     if (e == hipSuccess) return LAPLEX_OK;
-    if (e == hipErrorOutOfMemory || e == hipErrorMemoryAllocation)
-        return fail(LAPLEX_ERR_OUT_OF_MEMORY, std::string(where) + ": " + hipGetErrorString(e));
-    if (e == hipErrorNoDevice || e == hipErrorInvalidDevice)
-        return fail(LAPLEX_ERR_NO_DEVICE, std::string(where) + ": " + hipGetErrorString(e));
-    return fail(LAPLEX_ERR_DEVICE, std::string(where) + ": " + hipGetErrorString(e));
+    laplex_status st = LAPLEX_ERR_DEVICE;
+    if (e == hipErrorOutOfMemory || e == hipErrorMemoryAllocation) st = LAPLEX_ERR_OUT_OF_MEMORY;
+    if (e == hipErrorNoDevice || e == hipErrorInvalidDevice) st = LAPLEX_ERR_NO_DEVICE;
+    try {
+        return fail(st, std::string(where) + ": " + hipGetErrorString(e));
+    } catch (...) {
+        return st;
+    }
 }
 
 #define LX_TRY(call, where)                                          \
