@@ -166,6 +166,11 @@ struct RowPack {
             for (int j = 0; j < L; ++j) w[j] = *reinterpret_cast<const Mem*>(at.any_row(j < last ? j : last));
         }
     }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int j = 0; j < L; ++j) w[j] = Reg(0);
+    }
     // Row j in float32.  The copy hides that every call gives the same: the
     // compiler would hold all converted values (and all exponentials) in
     // registers from their first use to their last instead of the rows.
@@ -200,8 +205,9 @@ __device__ __forceinline__ void settle(float (&v)[N])
 // How a wave goes through its rows: kCareNone if every decay is above 0;
 // kCareZero if one may be 0 or too small for the plain exponential;
 // kCareRows if it has special rows too: first rows take h0 in and forget
-// what came before, rows of no sequence are 0.
-enum { kCareNone = 0, kCareZero = 1, kCareRows = 2 };
+// what came before, rows of no sequence are 0.  kCareGone: all of the wave's
+// rows are past the last one, nothing is read or written.
+enum { kCareNone = 0, kCareZero = 1, kCareRows = 2, kCareGone = 3 };
 
 // A thread's rows of x and g.  SH: one decay serves the V channels.
 template <class T, class TG, int V, int LL, bool SH>
@@ -236,9 +242,15 @@ struct RecurThread {
         whole = (tile + 1) * kRecurTile <= A.n;
         last = A.n - 1 - wave_row - lane_row;
         rows = !in || last < 0 ? 0 : (last < L - 1 ? (int)last + 1 : L);
+        if (gone(A)) {
+            x.clear();
+            g.clear();
+            return;
+        }
         x.load(at<T, V>(A.x, A.ldx), whole, last, A.stream);
         g.load(gate_at<TG>(A, A.g, A.ldg), whole, last, A.stream && !SH);  // a shared decay is read by many tiles
     }
+    __device__ __forceinline__ bool gone(const RecurArgs& A) const { return wave_row >= A.n; }
     __device__ __forceinline__ int col() const { return tile_col + lane * V; }
     template <class U, int N>
     __device__ __forceinline__ RowAt<U, N> at(const void* p, int64_t ld) const
@@ -252,12 +264,12 @@ struct RecurThread {
         return SH ? RowAt<U, D>(p, ld, wave_row, lane_row, 0, (in ? col() : tile_col) / A.per)
                   : RowAt<U, D>(p, ld, wave_row, lane_row, tile_col, in ? lane * V : 0);
     }
-    // The thread's special rows, a bit each, and whether its wave has any.
-    __device__ __forceinline__ bool find_odd(const RecurRows* R)
+    // The thread's special rows, a bit each; the care its wave takes, as far as known.
+    __device__ __forceinline__ int find_odd(const RecurArgs& A, const RecurRows* R)
     {
         static_assert(L <= 32 && kWave % L == 0, "a thread's rows lie in one word");
         odd = R ? (uint32_t)(R->odd[r0 / kWave] >> (r0 % kWave)) & (uint32_t)((1ull << L) - 1) : 0u;
-        return uniform(__any(odd != 0));
+        return gone(A) ? kCareGone : uniform(__any(odd != 0)) ? kCareRows : kCareNone;
     }
     template <int CARE>
     __device__ __forceinline__ bool special(int j) const
@@ -434,6 +446,13 @@ __device__ __forceinline__ uint32_t next_tile(const RecurArgs& A, int ct)
     __syncthreads();
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)s_ticket);
 }
+
+// With no more than a workgroup per CU the pass is bound by one tile's
+// latency: 1024 threads of 4 rows instead of 256 of 16, whose straight code
+// is four times as long to fetch.  777 x 512 bf16 forward 17.4 -> 10.5 us,
+// 2048 x 2048 16.8 -> 14.1; at 512 workgroups it is slower (float32
+// 2048 x 4096 24.7 -> 29.8).
+inline bool recur_few(const RecurArgs& a) { return a.tiles * a.cols <= 256; }
 
 // Clears what a pass publishes and marks the tiles (with more than one tile),
 // and gives sequences without rows their result: to[q] = from[q], or 0

@@ -44,7 +44,11 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     th.load(A, tile, ct);
     const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, mark, rows)) ? &rows : nullptr;
     float m[Th::D], h[V];
-    int care = th.find_odd(R) ? kCareRows : kCareNone;
+    int care = th.find_odd(A, R);
+#pragma unroll
+    for (int d = 0; d < Th::D; ++d) m[d] = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = 0.f;
     if (care == kCareNone) {
         th.template compose<kCareNone>(A, R, m, h);
         if (any_zero(m)) care = kCareZero;
@@ -79,7 +83,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     for (int v = 0; v < V; ++v) h[v] = sh[th.group][th.lane * V + v];
     if (care == kCareNone) write_rows<kCareNone, Th, T>(A, R, th, h);
     else if (care == kCareZero) write_rows<kCareZero, Th, T>(A, R, th, h);
-    else write_rows<kCareRows, Th, T>(A, R, th, h);
+    else if (care == kCareRows) write_rows<kCareRows, Th, T>(A, R, th, h);
 }
 
 // Blocks [0, fill): 16 bytes of all ones per thread over the published
@@ -129,8 +133,9 @@ hipError_t recur_type(const RecurArgs& a, hipStream_t s)
     const bool wide = vec_ok(a.x, a.ldx, a.width, sizeof(T), 4) && vec_ok(a.y, a.ldy, a.width, sizeof(T), 4) &&
                       vec_ok(a.h0, a.width, a.width, 4, 4) && vec_ok(a.final, a.width, a.width, 4, 4) &&
                       (sh ? a.per % 4 == 0 : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4));
+    if (wide && recur_few(a)) return sh ? recur_go<T, TG, 4, 4, true>(a, s) : recur_go<T, TG, 4, 4, false>(a, s);
     if (wide) return sh ? recur_go<T, TG, 4, 16, true>(a, s) : recur_go<T, TG, 4, 16, false>(a, s);
-    return recur_go<T, TG, 1, 32, true>(a, s);
+    return recur_go<T, TG, 1, 16, true>(a, s);
 }
 
 // One token for each request: state[slot] = e^g state[slot] + x, y = the new state.

@@ -214,10 +214,15 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     Th th;
     RowPack<T, V, L> dy;
     th.load(A, tile, ct);
-    dy.load(th.template at<T, V>(A.dy, A.lddy), th.whole, th.last, A.stream);
+    if (th.gone(A)) dy.clear();
+    else dy.load(th.template at<T, V>(A.dy, A.lddy), th.whole, th.last, A.stream);
     const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, mark, rows)) ? &rows : nullptr;
     float m[Th::D], h[V], w[V];
-    int care = th.find_odd(R) ? kCareRows : kCareNone;
+    int care = th.find_odd(A, R);
+#pragma unroll
+    for (int d = 0; d < Th::D; ++d) m[d] = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = w[v] = 0.f;
     if (care == kCareNone) {
         compose_both<kCareNone, Th, T, V>(A, R, th, dy, m, h, w);
         if (any_zero(m)) care = kCareZero;
@@ -269,7 +274,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     }
     if (care == kCareNone) write_grads<kCareNone>(A, R, th, dy, ct, h, w, s_sum);
     else if (care == kCareZero) write_grads<kCareZero>(A, R, th, dy, ct, h, w, s_sum);
-    else write_grads<kCareRows>(A, R, th, dy, ct, h, w, s_sum);
+    else if (care == kCareRows) write_grads<kCareRows>(A, R, th, dy, ct, h, w, s_sum);
     if (kSums && A.dg) {
         __syncthreads();
         tile_sums<TG, V, Lay::kThreads, kSumPitch>(A, tile, ct, s_sum);
@@ -315,6 +320,7 @@ hipError_t grad_type(const RecurArgs& a, hipStream_t s)
                       vec_ok(a.dfinal, a.width, a.width, 4, 4) && vec_ok(a.dh0, a.width, a.width, 4, 4) &&
                       (sh ? a.per % 4 == 0
                           : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4) && vec_ok(a.dg, a.lddg, a.width, sizeof(TG), 4));
+    if (wide && recur_few(a)) return sh ? grad_go<T, TG, 4, 4, true>(a, s) : grad_go<T, TG, 4, 4, false>(a, s);
     if (wide)
         return sh ? grad_go<T, TG, 4, kGradRows<T, true>, true>(a, s)
                   : grad_go<T, TG, 4, kGradRows<T, false>, false>(a, s);
