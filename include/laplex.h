@@ -321,7 +321,8 @@ laplex_status laplex_combine_backward(int64_t tokens, int64_t slots, int64_t n_e
 /*
  * laplex_recur -- y_t = h_t = exp(g_t) h_{t-1} + x_t along each sequence.
  *
- *   n, seqs   rows of all sequences together, and sequences.  offsets device
+ *   n, seqs   rows of all sequences together, and sequences (at most 2^30).
+ *             offsets device
  *             int32[seqs + 1], ascending: sequence q is rows offsets[q] ..
  *             offsets[q + 1] - 1 (none if equal); rows outside all sequences
  *             get y = 0.  NULL: seqs sequences of n / seqs rows each.

@@ -1707,7 +1707,7 @@ const char* recur_common(lx::RecurArgs& A, int64_t n, int64_t seqs, const int32_
                          const void* g, int64_t ldg, const float* h0)
 {
     if (!recur_sizes_ok(n, width, heads)) return "bad sizes: 0 <= n < 2^31, 1 <= width <= 2^24, heads divides width";
-    if (seqs < 1 || seqs > 0x7FFFFFFE) return "seqs must be in [1, 2^31 - 2]";
+    if (seqs < 1 || seqs > kMaxLen) return "seqs must be in [1, 2^30]";
     if (!offsets && n % seqs) return "without offsets n must be a multiple of seqs";
     if (!dtype_ok(type) || (gate_type != type && gate_type != LAPLEX_F32)) return "bad type or gate_type";
     if (n > 0 && (!x || !g)) return "x or g is NULL";

@@ -40,6 +40,9 @@ __device__ __forceinline__ float decay_of(float g)
 // a h + x, forgetting h where a is 0.
 __device__ __forceinline__ float step_of(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
 
+// Product of decays: 0, forgetting, wherever one of them is, an infinite one too.
+__device__ __forceinline__ float both_of(float a, float b) { return a == 0.f || b == 0.f ? 0.f : a * b; }
+
 // A condition that is the same in every lane, as a scalar: a branch on it is
 // then one for the whole wave, and neither side keeps the other's registers.
 __device__ __forceinline__ bool uniform(bool c) { return __builtin_amdgcn_readfirstlane((int)c) != 0; }
@@ -327,19 +330,20 @@ struct RecurThread {
             decays<CARE>(R, j, a);
             step<CARE>(A, R, j, a, H);
 #pragma unroll
-            for (int d = 0; d < D; ++d) m[d] *= a[d];
+            for (int d = 0; d < D; ++d) m[d] = CARE ? both_of(m[d], a[d]) : m[d] * a[d];
             settle(m);
         }
     }
 };
 
-// Whether any of a wave's products of decays is 0: some decay may be.
+// Whether any of a wave's products of decays is 0, so that some decay may
+// be, or NaN (a decay of 0 times one that is infinite).
 template <int D>
 __device__ __forceinline__ bool any_zero(const float (&m)[D])
 {
     bool z = false;
 #pragma unroll
-    for (int d = 0; d < D; ++d) z |= m[d] == 0.f;
+    for (int d = 0; d < D; ++d) z |= !(m[d] > 0.f);
     return uniform(__any(z));
 }
 

@@ -67,7 +67,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
         for (int i = 0; i < Lay::kGroups; ++i) {
             const float a = sa[i][SH ? c / V : c];
             ah = step_of(a, ah, sh[i][c]);
-            am *= a;
+            am = both_of(am, a);
         }
         float e = 0.f;
         if (A.tiles > 1) e = pass_state(A, tile, ct, am, ah, R && R->start[0] != -1, tile == A.tiles - 1);

@@ -55,7 +55,7 @@ __device__ __forceinline__ void compose_both(const RecurArgs& A, const RecurRows
         th.template step<CARE>(A, R, j, a, H);
         row_dy<CARE, Th, T, V>(A, R, th, dy, j, d);
 #pragma unroll
-        for (int i = 0; i < Th::D; ++i) m[i] *= a[i];
+        for (int i = 0; i < Th::D; ++i) m[i] = CARE ? both_of(m[i], a[i]) : m[i] * a[i];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float mv = m[Th::D == 1 ? 0 : v];
@@ -245,7 +245,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
         for (int i = Lay::kGroups - 1; i >= 0; --i) {
             const float a = sa[i][SH ? c / V : c];
             aw = step_of(a, aw, sw[i][c]);
-            am *= a;
+            am = both_of(am, a);
         }
         // nothing comes back into a tile whose last row ends a sequence or has none
         const bool fresh = R && (R->last[kRecurTile - 1] != -1 || R->start[kRecurTile - 1] == -2);

@@ -133,6 +133,19 @@ def test_a_decay_of_zero_forgets_inf_and_nan(gpu, at):
     assert (d["dg"][at] == 0).all()
 
 
+@pytest.mark.parametrize("at", [3, 150, 255])
+def test_a_reset_after_an_infinite_decay(gpu, at):
+    """exp(g) overflows at one row and is 0 at the next: what follows is finite."""
+    x, g, dy, _ = inputs(300, 64, 8, COMBOS[0], at)
+    g[at], g[at + 1] = 200.0, -math.inf
+    r = lx.laplex_recur(x.to(gpu), g.to(gpu), keep=True)
+    want = ref.Recur(x[at + 1:], g[at + 1:], [0, 299 - at], None, dy[at + 1:])
+    ref.assert_within(r.y[at + 1:], want.y, want.ey)
+    d = lx.laplex_recur_backward(x.to(gpu), g.to(gpu), dy.to(gpu), r.states)
+    ref.assert_within(d["dx"][at + 1:], want.dx, want.edx)
+    assert torch.isfinite(d["dg"][at + 2:]).all() and (d["dg"][at + 1] == 0).all()
+
+
 def test_sequences_do_not_leak(gpu):
     """inf and NaN in one sequence stay there, both ways."""
     x, g, dy, _ = inputs(400, 64, 64, COMBOS[0], 9)
