@@ -127,13 +127,12 @@ struct RowAt {
     int64_t pitch;  // bytes
     uint32_t off;
 
-    // wave_row: the wave's first row; lane_row: of the lane, from there;
-    // col: of the wave; lane_col: of the lane, from there
-    __device__ __forceinline__ RowAt(const void* p, int64_t ld, int64_t wave_row, int lane_row, int64_t col,
-                                     int lane_col)
-        : base((char*)p + (wave_row * ld + col) * (int64_t)sizeof(T)),
+    // wave_row: the wave's first row; lane_row: the lane's, from there; col:
+    // the lane's
+    __device__ __forceinline__ RowAt(const void* p, int64_t ld, int64_t wave_row, int lane_row, int col)
+        : base((char*)p + wave_row * ld * (int64_t)sizeof(T)),
           pitch(ld * (int64_t)sizeof(T)),
-          off(((uint32_t)lane_row * (uint32_t)ld + (uint32_t)lane_col) * (uint32_t)sizeof(T))
+          off(((uint32_t)lane_row * (uint32_t)ld + (uint32_t)col) * (uint32_t)sizeof(T))
     {
     }
     __device__ __forceinline__ T* row(int j) const
@@ -150,7 +149,7 @@ struct RowAt {
 template <class T, int V, int L>
 struct RowPack {
     static constexpr int kBytes = V * (int)sizeof(T);
-    typedef typename Words<kBytes>::T Mem;
+    typedef MemOf<T, V> Mem;
     typedef typename Words<kBytes == 2 ? 4 : kBytes>::T Reg;  // a register tuple as it is loaded
     Reg w[L];
 
@@ -221,11 +220,12 @@ struct RecurThread {
     RowPack<TG, D, L> g;
     int64_t wave_row;     // the wave's first row
     int tile_col;         // the tile's first channel
+    int first_col;        // the thread's
     int lane_row;         // the thread's first row, from the wave's
     int r0;               // the same, from the tile's
     int lane, group;      // thread of the row, row group
     int rows;             // of the thread's L: those that exist and are inside the width
-    bool in;              // channels inside the width; others read the tile's first
+    bool in;              // channels inside the width
     bool whole;           // all rows of the tile exist
     int64_t last;         // the array's last row, from the thread's first
     uint32_t odd;         // special rows
@@ -241,7 +241,12 @@ struct RecurThread {
         r0 = wave_r0 + lane_row;
         wave_row = tile * kRecurTile + wave_r0;
         tile_col = ct * kRecurCols;
-        in = col() < A.width;
+        // the last group of a row that V does not divide takes the row's last
+        // V channels: what two groups have is worked out twice, alike, and
+        // written twice; lanes past the width do the same and write nothing
+        const int c = tile_col + lane * V;
+        in = c < A.width;
+        first_col = c < A.width - V ? c : A.width - V;
         whole = (tile + 1) * kRecurTile <= A.n;
         last = A.n - 1 - wave_row - lane_row;
         rows = !in || last < 0 ? 0 : (last < L - 1 ? (int)last + 1 : L);
@@ -254,18 +259,17 @@ struct RecurThread {
         g.load(gate_at<TG>(A, A.g, A.ldg), whole, last, A.stream && !SH);  // a shared decay is read by many tiles
     }
     __device__ __forceinline__ bool gone(const RecurArgs& A) const { return wave_row >= A.n; }
-    __device__ __forceinline__ int col() const { return tile_col + lane * V; }
+    __device__ __forceinline__ int col() const { return first_col; }
     template <class U, int N>
     __device__ __forceinline__ RowAt<U, N> at(const void* p, int64_t ld) const
     {
-        return RowAt<U, N>(p, ld, wave_row, lane_row, tile_col, in ? lane * V : 0);
+        return RowAt<U, N>(p, ld, wave_row, lane_row, col());
     }
     // g or dg
     template <class U>
     __device__ __forceinline__ RowAt<U, D> gate_at(const RecurArgs& A, const void* p, int64_t ld) const
     {
-        return SH ? RowAt<U, D>(p, ld, wave_row, lane_row, 0, (in ? col() : tile_col) / A.per)
-                  : RowAt<U, D>(p, ld, wave_row, lane_row, tile_col, in ? lane * V : 0);
+        return RowAt<U, D>(p, ld, wave_row, lane_row, SH ? col() / A.per : col());
     }
     // The thread's special rows, a bit each; the care its wave takes, as far as known.
     __device__ __forceinline__ int find_odd(const RecurArgs& A, const RecurRows* R)
@@ -450,6 +454,9 @@ __device__ __forceinline__ uint32_t next_tile(const RecurArgs& A, int ct)
     __syncthreads();
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)s_ticket);
 }
+
+// Four channels per thread, unless a decay serves some other number of them.
+inline bool recur_wide(const RecurArgs& a) { return a.width >= 4 && (a.per == 1 || a.per % 4 == 0); }
 
 // With no more than a workgroup per CU the pass is bound by one tile's
 // latency: 1024 threads of 4 rows instead of 256 of 16, whose straight code

@@ -16,7 +16,8 @@ struct alignas(sizeof(T) * V) Pack {
     T v[V];
 };
 
-// What N bytes are moved as.
+// What N bytes are moved as, in a register and in memory: there only as
+// aligned as their values of A bytes (the hardware takes any address).
 template <int N>
 struct Words;
 template <>
@@ -27,26 +28,44 @@ template <>
 struct Words<8> { typedef uint32_t T __attribute__((ext_vector_type(2))); };
 template <>
 struct Words<16> { typedef uint32_t T __attribute__((ext_vector_type(4))); };
+template <int N, int A>
+struct Mem {
+    typedef typename Words<N>::T T __attribute__((aligned(A)));
+};
+template <class T, int V>
+using MemOf = typename Mem<(int)sizeof(T) * V, (int)sizeof(T)>::T;
 
-// Moves that leave the caches to others (non-temporal), for data that is not
-// used again before it would have left them anyway.
-template <class P>
-__device__ __forceinline__ P load_once(const P* p)
+// V neighbouring values from p on.  The `once` forms leave the caches to
+// others (non-temporal), for data that is not used again before it would
+// have left them anyway.
+template <int V, class T>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p)
 {
-    typedef typename Words<(int)sizeof(P)>::T W;
-    return __builtin_bit_cast(P, __builtin_nontemporal_load(reinterpret_cast<const W*>(p)));
+    const typename Words<(int)sizeof(T) * V>::T w = *reinterpret_cast<const MemOf<T, V>*>(p);
+    return __builtin_bit_cast(Pack<T, V>, w);
 }
-template <class P>
-__device__ __forceinline__ void store_once(P* p, const P& v)
+template <int V, class T>
+__device__ __forceinline__ Pack<T, V> load_once(const T* p)
 {
-    typedef typename Words<(int)sizeof(P)>::T W;
-    __builtin_nontemporal_store(__builtin_bit_cast(W, v), reinterpret_cast<W*>(p));
+    const typename Words<(int)sizeof(T) * V>::T w = __builtin_nontemporal_load(reinterpret_cast<const MemOf<T, V>*>(p));
+    return __builtin_bit_cast(Pack<T, V>, w);
+}
+template <int V, class T>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& v)
+{
+    *reinterpret_cast<MemOf<T, V>*>(p) = __builtin_bit_cast(typename Words<(int)sizeof(T) * V>::T, v);
+}
+template <int V, class T>
+__device__ __forceinline__ void store_once(T* p, const Pack<T, V>& v)
+{
+    __builtin_nontemporal_store(__builtin_bit_cast(typename Words<(int)sizeof(T) * V>::T, v),
+                                reinterpret_cast<MemOf<T, V>*>(p));
 }
 
 template <int V, class T>
 __device__ __forceinline__ void load_vec(const T* p, float (&out)[V])
 {
-    const Pack<T, V> q = *reinterpret_cast<const Pack<T, V>*>(p);
+    const Pack<T, V> q = load_pack<V>(p);
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = (float)q.v[i];
 }
@@ -63,20 +82,28 @@ __device__ __forceinline__ Pack<T, V> round_vec(const float (&in)[V])
 template <int V, class T>
 __device__ __forceinline__ void store_vec(T* p, const float (&in)[V])
 {
-    *reinterpret_cast<Pack<T, V>*>(p) = round_vec<V, T>(in);
+    store_pack<V>(p, round_vec<V, T>(in));
 }
 
 template <int V, class T>
 __device__ __forceinline__ void store_vec_once(T* p, const float (&in)[V])
 {
-    store_once(reinterpret_cast<Pack<T, V>*>(p), round_vec<V, T>(in));
+    store_once<V>(p, round_vec<V, T>(in));
 }
 
-// Whether rows of `width` values of `size` bytes, `ld` values apart from p
-// on, can be moved in groups of v values.
-inline bool vec_ok(const void* p, int64_t ld, int64_t width, size_t size, int v)
+// Either, as `once` says.  The empty statements keep the two stores apart:
+// the compiler would make one of them and drop the hint.
+template <int V, class T>
+__device__ __forceinline__ void store_vec_as(T* p, const float (&in)[V], bool once)
 {
-    return p == nullptr || (width % v == 0 && ld % v == 0 && (uintptr_t)p % (size * (size_t)v) == 0);
+    const Pack<T, V> q = round_vec<V, T>(in);
+    if (once) {
+        asm volatile("");
+        store_once<V>(p, q);
+        asm volatile("");
+    } else {
+        store_pack<V>(p, q);
+    }
 }
 
 }  // namespace lx

@@ -22,10 +22,7 @@ __device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* 
         float a[Th::D];
         th.template decays<CARE>(R, j, a);
         th.template step<CARE>(A, R, j, a, h);
-        if (CARE == kCareRows ? j < th.rows : th.in) {
-            if (A.stream) store_vec_once<V>(y.row(j), h);
-            else store_vec<V>(y.row(j), h);
-        }
+        if (CARE == kCareRows ? j < th.rows : th.in) store_vec_as<V>(y.row(j), h, A.stream);
         if (th.template special<CARE>(j) && A.final && th.in) {
             const int q = R->last[th.r0 + j];
             if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col(), h);
@@ -132,11 +129,7 @@ template <class T, class TG>
 hipError_t recur_type(const RecurArgs& a, hipStream_t s)
 {
     const bool sh = a.per > 1;
-    // four channels at a time where rows are aligned for it and a decay
-    // serves one channel or whole groups of four
-    const bool wide = vec_ok(a.x, a.ldx, a.width, sizeof(T), 4) && vec_ok(a.y, a.ldy, a.width, sizeof(T), 4) &&
-                      vec_ok(a.h0, a.width, a.width, 4, 4) && vec_ok(a.final, a.width, a.width, 4, 4) &&
-                      (sh ? a.per % 4 == 0 : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4));
+    const bool wide = recur_wide(a);
     if (wide && recur_few(a)) return sh ? recur_go<T, TG, 4, 4, true>(a, s) : recur_go<T, TG, 4, 4, false>(a, s);
     if (wide) return sh ? recur_go<T, TG, 4, 16, true>(a, s) : recur_go<T, TG, 4, 16, false>(a, s);
     return recur_go<T, TG, 1, 16, true>(a, s);
@@ -184,9 +177,8 @@ __global__ __launch_bounds__(256) void lx_recur_step(RecurStepArgs A)
 template <class T, class TG>
 hipError_t step_type(RecurStepArgs a, hipStream_t s)
 {
-    const bool wide = vec_ok(a.x, a.ldx, a.width, sizeof(T), 4) && vec_ok(a.y, a.ldy, a.width, sizeof(T), 4) &&
-                      vec_ok(a.state, a.width, a.width, 4, 4) &&
-                      (a.per > 1 ? a.per % 4 == 0 : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4));
+    // no two threads may share a channel here: each steps its state once
+    const bool wide = a.width % 4 == 0 && (a.per == 1 || a.per % 4 == 0);
     const int v = wide ? 4 : 1;
     a.groups = a.width / v;
     const int64_t blocks = (a.n * a.groups + 255) / 256;

@@ -143,15 +143,9 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             }
         }
         if (CARE) settle(w);
-        if (A.dx && here) {
-            if (A.stream) store_vec_once<V>(dx.row(j), u);
-            else store_vec<V>(dx.row(j), u);
-        }
+        if (A.dx && here) store_vec_as<V>(dx.row(j), u, A.stream);
         if (own) {
-            if (A.dg && here) {
-                if (A.stream) store_vec_once<V>(dg.row(j), p);
-                else store_vec<V>(dg.row(j), p);
-            }
+            if (A.dg && here) store_vec_as<V>(dg.row(j), p, A.stream);
         } else if (V > 1) {
             float sum = 0.f;
 #pragma unroll
@@ -318,11 +312,7 @@ template <class T, class TG>
 hipError_t grad_type(const RecurArgs& a, hipStream_t s)
 {
     const bool sh = a.per > 1;
-    const bool wide = vec_ok(a.x, a.ldx, a.width, sizeof(T), 4) && vec_ok(a.dy, a.lddy, a.width, sizeof(T), 4) &&
-                      vec_ok(a.dx, a.lddx, a.width, sizeof(T), 4) && vec_ok(a.h0, a.width, a.width, 4, 4) &&
-                      vec_ok(a.dfinal, a.width, a.width, 4, 4) && vec_ok(a.dh0, a.width, a.width, 4, 4) &&
-                      (sh ? a.per % 4 == 0
-                          : vec_ok(a.g, a.ldg, a.width, sizeof(TG), 4) && vec_ok(a.dg, a.lddg, a.width, sizeof(TG), 4));
+    const bool wide = recur_wide(a);
     if (wide && recur_few(a)) return sh ? grad_go<T, TG, 4, 4, true>(a, s) : grad_go<T, TG, 4, 4, false>(a, s);
     if (wide)
         return sh ? grad_go<T, TG, 4, kGradRows<T, true>, true>(a, s)

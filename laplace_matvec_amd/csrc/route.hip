@@ -22,8 +22,10 @@
 // grows).  What is left is the placing's chain of counters and its scattered
 // 4-byte writes.
 //
-// The data movement has one thread per token and 16 bytes of its row, so a
-// token's row is read (written) once and its K copies are in flight together:
+// The data movement has one thread per token and 16 bytes of its row (at any
+// address; the last thread of a row takes its last 16 bytes, some of them a
+// second time), so a token's row is read (written) once and its K copies are
+// in flight together:
 //     dispatch      xs[place[t,k]] = x[t]
 //     combine       y[t] = sum_k w[t,k] ys[place[t,k]]
 //     combine_grad  dys[place[t,k]] = w[t,k] dy[t], dw[t,k] = <dy[t], ys[place[t,k]]>
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(kRouteThreads) void lx_route_place(RouteArgs A)
     uint32_t* cnt = s_dyn;
     uint32_t* base = s_dyn + kRouteWaves * E;
     const int tid = threadIdx.x, lane = lane_id(), w = tid / kWave;
-    const int64_t tile0 = (int64_t)blockIdx.x * kTile;
+    const int64_t tile = blockIdx.x, tile0 = tile * kTile;
     const int64_t left = A.n - tile0;
     const int room = (int)(left < kTile ? left : kTile);  // slots of this tile
     const int w0 = w * (kTile / kRouteWaves);
@@ -218,13 +220,13 @@ __global__ __launch_bounds__(kRouteThreads) void lx_route_place(RouteArgs A)
     }
     __syncthreads();
     const uint32_t total = scan_experts(base, s_wave, E);
-    if (blockIdx.x == 0) {
+    if (tile == 0) {
         for (int e = tid; e < E; e += kRouteThreads) A.offsets[e] = (int32_t)base[e];
         if (tid == 0) A.offsets[E] = (int32_t)total;
     }
     if (!SINGLE) {
         __syncthreads();
-        for (int e = tid; e < E; e += kRouteThreads) base[e] += A.hist[(int64_t)blockIdx.x * E + e];
+        for (int e = tid; e < E; e += kRouteThreads) base[e] += A.hist[tile * E + e];
         __syncthreads();
     }
 #pragma unroll
@@ -253,17 +255,26 @@ __device__ __forceinline__ void zero_tail(const MoveArgs& A, T* rows, int64_t ld
     for (int64_t r = (kept < 0 ? 0 : kept) + t; r < A.tokens * A.slots; r += A.tokens) store_vec<V>(rows + r * ld, z);
 }
 
-// Token and column group of this thread: the flat index over
+// First column of group i of V: the last one ends with the row.
+template <int V>
+__device__ __forceinline__ int64_t group_col(const MoveArgs& A, int i)
+{
+    const int64_t at = (int64_t)i * V;
+    return at < A.width - V ? at : A.width - V;
+}
+
+// Token and first column of this thread: the flat index over
 // [tokens][groups], divided in 64 bits once per workgroup and in 32 bits per
 // thread.  False past the last token.
-__device__ __forceinline__ bool token_group(const MoveArgs& A, int64_t* t, int* col)
+template <int V>
+__device__ __forceinline__ bool token_group(const MoveArgs& A, int64_t* t, int64_t* at)
 {
     const int64_t i0 = (int64_t)blockIdx.x * 256;
     const int64_t t0 = i0 / A.groups;
     const uint32_t rest = (uint32_t)(i0 - t0 * A.groups) + threadIdx.x;
     const uint32_t more = rest / (uint32_t)A.groups;
     *t = t0 + more;
-    *col = (int)(rest - more * (uint32_t)A.groups);
+    *at = group_col<V>(A, (int)(rest - more * (uint32_t)A.groups));
     return *t < A.tokens;
 }
 
@@ -284,11 +295,9 @@ __device__ __forceinline__ void slot_rows(const MoveArgs& A, int64_t t, int64_t 
 template <int V, class T, int KC>
 __global__ __launch_bounds__(256) void lx_dispatch(MoveArgs A)
 {
-    int64_t t;
-    int col;
-    if (!token_group(A, &t, &col)) return;
-    const int64_t at = (int64_t)col * V;
-    const Pack<T, V> v = *reinterpret_cast<const Pack<T, V>*>((const T*)A.in + t * A.ld_in + at);
+    int64_t t, at;
+    if (!token_group<V>(A, &t, &at)) return;
+    const Pack<T, V> v = load_pack<V>((const T*)A.in + t * A.ld_in + at);
     const int64_t kept = A.offsets[A.experts];
     T* xs = (T*)A.out + at;
     for (int64_t k0 = 0; k0 < A.slots; k0 += KC) {
@@ -296,7 +305,7 @@ __global__ __launch_bounds__(256) void lx_dispatch(MoveArgs A)
         slot_rows<KC>(A, t, k0, row);
 #pragma unroll
         for (int k = 0; k < KC; ++k)
-            if (row[k] >= 0) store_once(reinterpret_cast<Pack<T, V>*>(xs + row[k] * A.ld_out), v);
+            if (row[k] >= 0) store_once<V>(xs + row[k] * A.ld_out, v);
     }
     zero_tail<V>(A, xs, A.ld_out, kept, t);
 }
@@ -305,10 +314,8 @@ __global__ __launch_bounds__(256) void lx_dispatch(MoveArgs A)
 template <int V, class T, int KC>
 __global__ __launch_bounds__(256) void lx_combine(MoveArgs A)
 {
-    int64_t t;
-    int col;
-    if (!token_group(A, &t, &col)) return;
-    const int64_t at = (int64_t)col * V;
+    int64_t t, at;
+    if (!token_group<V>(A, &t, &at)) return;
     const T* ys = (const T*)A.in + at;
     float acc[V];
 #pragma unroll
@@ -323,7 +330,7 @@ __global__ __launch_bounds__(256) void lx_combine(MoveArgs A)
             const bool kept = row[k] >= 0;
             w[k] = A.weights && kept ? A.weights[t * A.slots + k0 + k] : 1.f;
             // a dropped slot reads row 0 and takes nothing from it
-            v[k] = load_once(reinterpret_cast<const Pack<T, V>*>(ys + (kept ? row[k] : 0) * A.ld_in));
+            v[k] = load_once<V>(ys + (kept ? row[k] : 0) * A.ld_in);
         }
 #pragma unroll
         for (int k = 0; k < KC; ++k)
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(256) void lx_combine(MoveArgs A)
 
 // G threads of a 256-thread workgroup per token; the dot products of KC
 // slots are carried along one pass over the row.  16384 tokens x 4 rows of
-// 2048 bf16: 110 us, 5.5 TB/s (a wave per token there: 135).
+// 2048 bf16: 105 us, 5.8 TB/s (a wave per token there: 135).
 template <int V, class T, int KC, int G>
 __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
 {
@@ -360,15 +367,15 @@ __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
         }
         if (live) {
             for (int col = part; col < A.groups; col += G) {
-                const int64_t at = (int64_t)col * V;
+                const int64_t at = group_col<V>(A, col);
+                const int again = (int)((int64_t)col * V - at);  // values that another thread has too
                 Pack<T, V> v[KC];
                 float d[V];
                 load_vec<V>(dy + at, d);
                 if (A.dw) {
 #pragma unroll
                     for (int k = 0; k < KC; ++k)
-                        v[k] = load_once(
-                            reinterpret_cast<const Pack<T, V>*>(ys + (row[k] >= 0 ? row[k] : 0) * A.ld_in + at));
+                        v[k] = load_once<V>(ys + (row[k] >= 0 ? row[k] : 0) * A.ld_in + at);
                 }
                 if (dys) {
 #pragma unroll
@@ -385,7 +392,7 @@ __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
                     for (int k = 0; k < KC; ++k)
 #pragma unroll
                         for (int q = 0; q < V; ++q)
-                            dot[k] = row[k] >= 0 ? fmaf(d[q], (float)v[k].v[q], dot[k]) : dot[k];
+                            dot[k] = row[k] >= 0 && q >= again ? fmaf(d[q], (float)v[k].v[q], dot[k]) : dot[k];
                 }
             }
         }
@@ -417,7 +424,7 @@ __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
     }
     if (dys && live) {
         const int64_t kept = A.offsets[A.experts];
-        for (int col = part; col < A.groups; col += G) zero_tail<V>(A, dys + (int64_t)col * V, A.ld_out, kept, t);
+        for (int col = part; col < A.groups; col += G) zero_tail<V>(A, dys + group_col<V>(A, col), A.ld_out, kept, t);
     }
 }
 
@@ -436,7 +443,7 @@ hipError_t place_launch(const RouteArgs& a, hipStream_t s)
 template <int V, class T, int KC>
 hipError_t move_launch(MoveKind kind, MoveArgs a, hipStream_t s)
 {
-    a.groups = (int)(a.width / V);
+    a.groups = (int)((a.width + V - 1) / V);
     const int64_t blocks = (a.tokens * a.groups + 255) / 256;
     if (blocks > 0x7FFFFFFFll || a.tokens > 0x7FFFFFFFll) return hipErrorInvalidValue;
     switch (kind) {
@@ -472,11 +479,7 @@ template <class T>
 hipError_t move_type(MoveKind kind, const MoveArgs& a, hipStream_t s)
 {
     constexpr int V = 16 / (int)sizeof(T);
-    // 16 bytes at a time where every row of every array starts and ends on
-    // 16 bytes, one value at a time otherwise
-    const bool wide = vec_ok(a.in, a.ld_in, a.width, sizeof(T), V) && vec_ok(a.out, a.ld_out, a.width, sizeof(T), V) &&
-                      vec_ok(a.dy, a.ld_dy, a.width, sizeof(T), V);
-    return wide ? move_slots<V, T>(kind, a, s) : move_slots<1, T>(kind, a, s);
+    return a.width >= V ? move_slots<V, T>(kind, a, s) : move_slots<1, T>(kind, a, s);
 }
 
 }  // namespace

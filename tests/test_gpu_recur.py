@@ -58,6 +58,32 @@ def test_head_layouts(gpu, types, width, heads):
     check(gpu, x, g, dy, [0, 90, 200], torch.randn(2, width, generator=gen), torch.randn(2, width, generator=gen))
 
 
+@pytest.mark.parametrize("types", COMBOS[:3])
+@pytest.mark.parametrize("width", [2, 3, 4, 5, 7, 61, 65, 66, 67, 129, 191])
+def test_widths_that_four_does_not_divide(gpu, types, width):
+    """A decay per channel; the last group of four of a row starts before where it would."""
+    x, g, dy, gen = inputs(290, width, width, types, width, resets=0.01)
+    check(gpu, x, g, dy, [0, 100, 290], torch.randn(2, width, generator=gen), torch.randn(2, width, generator=gen))
+
+
+def test_odd_width_over_many_tiles(gpu):
+    """More tiles than the few that take the short form, odd rows, twice the same."""
+    n, width = 4200, 1027
+    gen = torch.Generator(device=gpu).manual_seed(5)
+    x = torch.randn(n, width, device=gpu, generator=gen).to(torch.bfloat16)
+    g = -torch.rand(n, width, device=gpu, generator=gen)
+    dy = torch.randn(n, width, device=gpu, generator=gen).to(torch.bfloat16)
+    r = lx.laplex_recur(x, g, final=True, keep=True)
+    d = lx.laplex_recur_backward(x, g, dy, r.states)
+    again = lx.laplex_recur(x, g, final=True, keep=True)
+    assert torch.equal(r.y, again.y) and torch.equal(r.final, again.final)
+    cols = [0, 63, 64, 1022, 1023, 1024, 1025, 1026]
+    want = ref.Recur(x[-600:, cols], g[-600:, cols], [0, 600], None, dy[-600:, cols])  # 0.5 a row
+    ref.assert_within(r.y[-300:, cols], want.y[-300:], want.ey[-300:])
+    ref.assert_within(d["dx"][-600:, cols], want.dx, want.edx)
+    ref.assert_within(d["dg"][-300:, cols], want.dg[-300:], want.edg[-300:])
+
+
 @pytest.mark.parametrize("types", COMBOS[1:3])
 @pytest.mark.parametrize("offsets", [
     [0, 0, 1, 2, 2, 2, 60, 128, 128, 256, 257, 700, 700],  # empty ones, borders of tiles
