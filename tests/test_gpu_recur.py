@@ -275,6 +275,36 @@ def test_long_rows_repeat_bit_for_bit(gpu):
     ref.assert_within(d0["dg"][:1000, cols], want.dg[:1000], want.edg[:1000])
 
 
+@pytest.mark.parametrize("seqs", [1, 7])
+def test_one_narrow_chain(gpu, seqs):
+    """400 tiles that all hang on the ones before them, next to another such pass on a second stream."""
+    gen = torch.Generator(device=gpu).manual_seed(seqs)
+    n, width = 102400, 64
+    x = torch.randn(n, width, device=gpu, generator=gen)
+    g = -torch.rand(n, 1, device=gpu, generator=gen) - 0.1
+    dy = torch.randn(n, width, device=gpu, generator=gen)
+    at = torch.linspace(0, n, seqs + 1, device=gpu).to(torch.int32)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    both = []
+    for stream in (None, side):
+        r = lx.laplex_recur(x, g, offsets=at, final=True, keep=True, stream=stream)
+        both.append((r, lx.laplex_recur_backward(x, g, dy, r.states, offsets=at, stream=stream)))
+    torch.cuda.synchronize()
+    (r, d), (r2, d2) = both
+    assert torch.equal(r.y, r2.y) and all(torch.equal(d[k], d2[k]) for k in d)
+    first = int(at[-2])
+    m = min(500, n - first)  # 0.6 a row: nothing older is left after 200
+    want = ref.Recur(x[-m:], g[-m:], [0, m], None, dy[-m:])
+    ref.assert_within(r.y[-300:], want.y[-300:], want.ey[-300:])
+    ref.assert_within(d["dx"][-m:], want.dx, want.edx)
+    ref.assert_within(d["dg"][-300:], want.dg[-300:], want.edg[-300:])
+    want = ref.Recur(x[:500], g[:500], [0, 500], None, dy[:500])
+    ref.assert_within(r.y[:500], want.y, want.ey)
+    ref.assert_within(d["dx"][:300], want.dx[:300], want.edx[:300])
+    ref.assert_within(d["dg"][:300], want.dg[:300], want.edg[:300])
+
+
 def test_rows_past_32_bit_offsets(gpu):
     """Rows far apart: the last ones are past 2^32 bytes and 2^31 values."""
     n, pitch, width = 140, 1 << 24, 64
