@@ -8,10 +8,10 @@
 // serves several channels is the sum over them.  The states h_{t-1} are made
 // again in float32 from x and the saved states between row tiles (1/256 of
 // x's values), which reads no more than a saved y would and loses nothing to
-// y's rounding.  Packed 32768 x 4096 bf16 with a decay per 64 channels: 205
-// us, 3.9 TB/s of x, dy and dx, bound by what a tile waits for (loads 3 us,
-// hand-over 3, writing 4 of 12, three workgroups per CU); a decay per channel:
-// 5.7 TB/s.  Where a_t is 0 the state was forgotten and w_t and dg_t are 0.
+// y's rounding.  Packed 32768 x 4096 bf16 with a decay per 64 channels: 213
+// to 222 us, 3.7 TB/s of x, dy and dx, bound by what a tile waits for (loads
+// 3 us, hand-over 3, writing 4 of 12, three workgroups per CU); a decay per
+// channel: 5.7 TB/s.  Where a_t is 0 the state was forgotten and w_t and dg_t are 0.
 #include "lx_recur.h"
 
 namespace lx {
