@@ -1726,9 +1726,9 @@ const char* recur_common(lx::RecurArgs& A, int64_t n, int64_t seqs, const int32_
     A.tiles = tiles;
     A.cols = (int)cols;
     A.x = x;
-    A.ldx = ldx;
+    A.ldx = lx::recur_pitch(n, width, ldx);
     A.g = g;
-    A.ldg = ldg;
+    A.ldg = lx::recur_pitch(n, heads, ldg);
     A.h0 = h0;
     return nullptr;
 }
@@ -1950,7 +1950,7 @@ laplex_status laplex_recur(int64_t n, int64_t seqs, const int32_t* offsets, int6
     if (st != LAPLEX_OK) return st;
     hipStream_t s = (hipStream_t)stream;
     A.y = y;
-    A.ldy = ldy;
+    A.ldy = lx::recur_pitch(n, width, ldy);
     A.final = final;
     recur_scratch(A, ws);
     if (states) A.states = (uint32_t*)states;
@@ -1988,13 +1988,13 @@ laplex_status laplex_recur_backward(int64_t n, int64_t seqs, const int32_t* offs
     if (st != LAPLEX_OK) return st;
     hipStream_t s = (hipStream_t)stream;
     A.dy = dy;
-    A.lddy = lddy;
+    A.lddy = lx::recur_pitch(n, width, lddy);
     A.dfinal = dfinal;
     A.states_in = states;
     A.dx = dx;
-    A.lddx = lddx;
+    A.lddx = lx::recur_pitch(n, width, lddx);
     A.dg = dg;
-    A.lddg = lddg;
+    A.lddg = lx::recur_pitch(n, heads, lddg);
     A.dh0 = dh0;
     recur_scratch(A, ws);
     LX_TRY(lx::recur_grad_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, s), "recurrence backward");

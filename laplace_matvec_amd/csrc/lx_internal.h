@@ -397,6 +397,10 @@ constexpr int kRecurTile = 256;  // rows of a tile
 constexpr int kRecurCols = 64;   // channels of a tile
 constexpr int kRecurTicketPitch = 32;  // words: each counter on a line of its own
 constexpr int64_t kRecurMaxPitch = (int64_t)1 << 24;  // values between rows
+// The pitch that the kernels get.  Lanes whose rows are not there reckon from
+// their own rows' addresses back to the last row, in 32 bits, so it must be
+// within kRecurMaxPitch also where a single row leaves it open.
+inline int64_t recur_pitch(int64_t n, int64_t width, int64_t ld) { return n > 1 ? ld : width; }
 struct RecurArgs {
     int64_t n = 0;         // rows
     int64_t seqs = 0;      // sequences

@@ -120,7 +120,7 @@ __device__ __forceinline__ bool recur_rows(const RecurArgs& A, int64_t t0, int m
 // wave (row j is j pitches further, in scalar registers) and a 32-bit offset
 // of the lane, so that an address takes one vector register for all rows.
 // A wave spans at most 64 rows of one array; a pitch of at most 2^24 values
-// (kRecurMaxPitch) keeps the offset within 32 bits.
+// (kRecurMaxPitch, see recur_pitch) keeps the offset within 32 bits.
 template <class T, int V>
 struct RowAt {
     char* base;
@@ -129,7 +129,7 @@ struct RowAt {
 
     // wave_row: the wave's first row; lane_row: the lane's, from there; col:
     // the lane's
-    __device__ __forceinline__ RowAt(const void* p, int64_t ld, int64_t wave_row, int lane_row, int col)
+    __host__ __device__ __forceinline__ RowAt(const void* p, int64_t ld, int64_t wave_row, int lane_row, int col)
         : base((char*)p + wave_row * ld * (int64_t)sizeof(T)),
           pitch(ld * (int64_t)sizeof(T)),
           off(((uint32_t)lane_row * (uint32_t)ld + (uint32_t)col) * (uint32_t)sizeof(T))
@@ -141,7 +141,7 @@ struct RowAt {
         asm volatile("" : "+s"(o));  // stays in scalar registers, apart from the lane's offset
         return reinterpret_cast<T*>(base + o + off);
     }
-    __device__ __forceinline__ T* any_row(int64_t j) const { return reinterpret_cast<T*>(base + j * pitch + off); }
+    __host__ __device__ __forceinline__ T* any_row(int64_t j) const { return reinterpret_cast<T*>(base + j * pitch + off); }
 };
 
 // L rows of V channels of one array as stored (a vector of 16-bit values
