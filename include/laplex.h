@@ -354,8 +354,8 @@ laplex_status laplex_combine_backward(int64_t tokens, int64_t slots, int64_t n_e
  *
  * laplex_recur_workspace and laplex_recur_states return -1 for sizes out of
  * range: 0 <= n < 2^31, 1 <= width <= 2^24, heads dividing width.  In the
- * first two calls rows are at most 2^24 values apart (the pitch of a single
- * row is not used).
+ * first two calls n * width is at most 2^38 and rows are at most 2^24 values
+ * apart (the pitch of a single row is not used).
  * Outputs may not overlap each other or an input (state apart).  Results
  * repeat bit for bit.
  */

@@ -31,6 +31,24 @@ void prof_end(int token, hipStream_t s);
         if (lx_e_ != hipSuccess) return lx_e_;                \
     } while (0)
 
+// ---- grids of more than 2^32 threads ----
+// A launch counts its threads along x in 32 bits (more are cut off without an
+// error, unless none are left), so workgroups past kGridThreads of them go
+// along y.  A kernel numbers its workgroups by group_id<THREADS>() and leaves
+// where there is no work: the last row of the grid may be longer than needed.
+constexpr int64_t kGridThreads = (int64_t)1 << 30;
+template <int THREADS>
+inline dim3 grid_of(int64_t groups)
+{
+    constexpr int64_t x = kGridThreads / THREADS;
+    return groups <= x ? dim3((unsigned)groups) : dim3((unsigned)x, (unsigned)((groups + x - 1) / x));
+}
+template <int THREADS>
+__device__ __forceinline__ int64_t group_id()
+{
+    return (int64_t)blockIdx.y * (kGridThreads / THREADS) + blockIdx.x;
+}
+
 // ---- utilities ----
 hipError_t fill_u32(uint32_t* p, uint32_t v, int64_t count, hipStream_t s);
 

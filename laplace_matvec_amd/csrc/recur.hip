@@ -38,8 +38,9 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     __shared__ RecurRows rows;
     __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
     __shared__ float sh[Lay::kGroups][kRecurCols];
-    const int ct = channel_tile(A);
+    const int ct = channel_tile(A, (uint32_t)group_id<Lay::kThreads>());
     const int64_t tile = next_tile(A, ct);
+    if (past_tiles(A, tile)) return;
     const int mark = tile_mark(A, tile);
     Th th;
     th.load(A, tile, ct);
@@ -88,7 +89,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
 }
 
 // Blocks [0, fill): 16 bytes of all ones per thread over the published
-// words, the tickets and the marks; the rest: one sequence each.
+// words, the tickets and the marks; the rest: a sequence each, in turn.
 __global__ __launch_bounds__(256) void lx_recur_begin(RecurArgs A, int64_t maps16, int64_t states16, unsigned fill,
                                                       const float* __restrict__ from, float* __restrict__ to)
 {
@@ -111,9 +112,10 @@ __global__ __launch_bounds__(256) void lx_recur_begin(RecurArgs A, int64_t maps1
         }
         return;
     }
-    const int64_t q = blockIdx.x - fill;
-    if (A.offsets && A.offsets[q + 1] > A.offsets[q]) return;
-    for (int c = threadIdx.x; c < A.width; c += 256) to[q * A.width + c] = from ? from[q * A.width + c] : 0.f;
+    for (int64_t q = blockIdx.x - fill; q < A.seqs; q += gridDim.x - fill) {
+        if (A.offsets && A.offsets[q + 1] > A.offsets[q]) continue;
+        for (int c = threadIdx.x; c < A.width; c += 256) to[q * A.width + c] = from ? from[q * A.width + c] : 0.f;
+    }
 }
 
 template <class T, class TG, int V, int L, bool SH>
@@ -121,7 +123,7 @@ hipError_t recur_go(const RecurArgs& a, hipStream_t s)
 {
     LX_LAUNCH("recur", s,
               (lx_recur_pass<T, TG, V, L, SH>
-               <<<(unsigned)(a.tiles * a.cols), RecurLayout<V, L>::kThreads, 0, s>>>(a)));
+               <<<grid_of<RecurLayout<V, L>::kThreads>(a.tiles * a.cols), RecurLayout<V, L>::kThreads, 0, s>>>(a)));
     return hipSuccess;
 }
 
@@ -140,7 +142,7 @@ hipError_t recur_type(const RecurArgs& a, hipStream_t s)
 template <class T, class TG, int V>
 __global__ __launch_bounds__(256) void lx_recur_step(RecurStepArgs A)
 {
-    const int64_t i0 = (int64_t)blockIdx.x * 256;
+    const int64_t i0 = group_id<256>() * 256;
     const int64_t b0 = i0 / A.groups;
     const uint32_t rest = (uint32_t)(i0 - b0 * A.groups) + threadIdx.x;
     const uint32_t more = rest / (uint32_t)A.groups;
@@ -182,11 +184,10 @@ hipError_t step_type(RecurStepArgs a, hipStream_t s)
     const int v = wide ? 4 : 1;
     a.groups = a.width / v;
     const int64_t blocks = (a.n * a.groups + 255) / 256;
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
     if (wide)
-        LX_LAUNCH("recur_step", s, (lx_recur_step<T, TG, 4><<<(unsigned)blocks, 256, 0, s>>>(a)));
+        LX_LAUNCH("recur_step", s, (lx_recur_step<T, TG, 4><<<grid_of<256>(blocks), 256, 0, s>>>(a)));
     else
-        LX_LAUNCH("recur_step", s, (lx_recur_step<T, TG, 1><<<(unsigned)blocks, 256, 0, s>>>(a)));
+        LX_LAUNCH("recur_step", s, (lx_recur_step<T, TG, 1><<<grid_of<256>(blocks), 256, 0, s>>>(a)));
     return hipSuccess;
 }
 
@@ -197,7 +198,8 @@ hipError_t recur_begin(const RecurArgs& a, const float* from, float* to, hipStre
     const int64_t words = a.tiles > 1 ? (a.tiles - 1) * a.cols * kRecurCols : 0;
     const int64_t maps16 = words / 2, states16 = words / 4;
     const unsigned fill = (unsigned)((maps16 + states16 + 255) / 256);
-    const unsigned each = to && (a.offsets || a.n == 0) ? (unsigned)a.seqs : 0;
+    // n * width <= 2^38 keeps both together below 2^23 workgroups
+    const unsigned each = to && (a.offsets || a.n == 0) ? (unsigned)(a.seqs < 65536 ? a.seqs : 65536) : 0;
     if (fill + each > 0)
         LX_LAUNCH("recur_begin", s, (lx_recur_begin<<<fill + each, 256, 0, s>>>(a, maps16, states16, fill, from, to)));
     return hipSuccess;

@@ -204,8 +204,9 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     __shared__ float sw[Lay::kGroups][kRecurCols];
     constexpr bool kSums = SH && V > 1;
     __shared__ float s_sum[kSums ? kRecurTile : 1][kSumPitch];
-    const int ct = channel_tile(A);
+    const int ct = channel_tile(A, (uint32_t)group_id<Lay::kThreads>());
     const int64_t back = next_tile(A, ct);  // tiles before this one in the pass: from the last rows on
+    if (past_tiles(A, back)) return;
     const int64_t tile = A.tiles - 1 - back;
     const int mark = tile_mark(A, tile);
     Th th;
@@ -284,7 +285,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
 template <class TG>
 __global__ __launch_bounds__(256) void lx_recur_grad_heads(RecurArgs A)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = group_id<256>() * 256 + threadIdx.x;
     const int64_t row = i / A.heads;
     if (row >= A.n) return;
     const int head = (int)(i - row * A.heads);
@@ -301,10 +302,10 @@ hipError_t grad_go(const RecurArgs& a, hipStream_t s)
 {
     LX_LAUNCH("recur_grad", s,
               (lx_recur_grad_pass<T, TG, V, L, SH>
-               <<<(unsigned)(a.tiles * a.cols), RecurLayout<V, L>::kThreads, 0, s>>>(a)));
+               <<<grid_of<RecurLayout<V, L>::kThreads>(a.tiles * a.cols), RecurLayout<V, L>::kThreads, 0, s>>>(a)));
     if (a.dg && a.per > 1 && !recur_heads_inside(a.width, a.per))
         LX_LAUNCH("recur_grad_heads", s,
-                  (lx_recur_grad_heads<TG><<<(unsigned)((a.n * a.heads + 255) / 256), 256, 0, s>>>(a)));
+                  (lx_recur_grad_heads<TG><<<grid_of<256>((a.n * a.heads + 255) / 256), 256, 0, s>>>(a)));
     return hipSuccess;
 }
 

@@ -269,7 +269,7 @@ __device__ __forceinline__ int64_t group_col(const MoveArgs& A, int i)
 template <int V>
 __device__ __forceinline__ bool token_group(const MoveArgs& A, int64_t* t, int64_t* at)
 {
-    const int64_t i0 = (int64_t)blockIdx.x * 256;
+    const int64_t i0 = group_id<256>() * 256;
     const int64_t t0 = i0 / A.groups;
     const uint32_t rest = (uint32_t)(i0 - t0 * A.groups) + threadIdx.x;
     const uint32_t more = rest / (uint32_t)A.groups;
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
 {
     __shared__ float s_dot[256 / kWave][KC];
     const int part = (int)threadIdx.x % G;
-    const int64_t t = (int64_t)blockIdx.x * (256 / G) + (int)threadIdx.x / G;
+    const int64_t t = group_id<256>() * (256 / G) + (int)threadIdx.x / G;
     const bool live = t < A.tokens;
     const int lane = lane_id(), w = (int)threadIdx.x / kWave;
     const T* dy = (const T*)A.dy + (live ? t : 0) * A.ld_dy;
@@ -445,22 +445,22 @@ hipError_t move_launch(MoveKind kind, MoveArgs a, hipStream_t s)
 {
     a.groups = (int)((a.width + V - 1) / V);
     const int64_t blocks = (a.tokens * a.groups + 255) / 256;
-    if (blocks > 0x7FFFFFFFll || a.tokens > 0x7FFFFFFFll) return hipErrorInvalidValue;
     switch (kind) {
         case kMoveDispatch:
-            LX_LAUNCH("dispatch", s, (lx_dispatch<V, T, KC><<<(unsigned)blocks, 256, 0, s>>>(a)));
+            LX_LAUNCH("dispatch", s, (lx_dispatch<V, T, KC><<<grid_of<256>(blocks), 256, 0, s>>>(a)));
             return hipSuccess;
         case kMoveCombine:
-            LX_LAUNCH("combine", s, (lx_combine<V, T, KC><<<(unsigned)blocks, 256, 0, s>>>(a)));
+            LX_LAUNCH("combine", s, (lx_combine<V, T, KC><<<grid_of<256>(blocks), 256, 0, s>>>(a)));
             return hipSuccess;
         case kMoveCombineGrad:
             // a wave per token while a row is at most two loads per lane, a
             // workgroup above: see the kernel
             if (a.groups <= 2 * kWave)
                 LX_LAUNCH("combine_grad", s,
-                          (lx_combine_grad<V, T, KC, 64><<<(unsigned)((a.tokens + 3) / 4), 256, 0, s>>>(a)));
+                          (lx_combine_grad<V, T, KC, 64><<<grid_of<256>((a.tokens + 3) / 4), 256, 0, s>>>(a)));
             else
-                LX_LAUNCH("combine_grad", s, (lx_combine_grad<V, T, KC, 256><<<(unsigned)a.tokens, 256, 0, s>>>(a)));
+                LX_LAUNCH("combine_grad", s,
+                          (lx_combine_grad<V, T, KC, 256><<<grid_of<256>(a.tokens), 256, 0, s>>>(a)));
             return hipSuccess;
     }
     return hipErrorInvalidValue;
