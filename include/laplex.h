@@ -329,8 +329,11 @@ laplex_status laplex_combine_backward(int64_t tokens, int64_t slots, int64_t n_e
  *   x, y      [n][width] of `type`.
  *   g         [n][heads] of `gate_type` (`type` or LAPLEX_F32): logarithms of
  *             the decays, each for width / heads neighbouring channels.
- *             Where exp(g) is 0 (g = -inf) the state is forgotten, whatever
- *             it held.
+ *             Where exp(g) is 0 in float32 (g = -inf, or below -104) the
+ *             state is forgotten, whatever it held; inf and NaN stay under
+ *             any other decay.  exp(g) may be above 1 (from 2^256 on it is
+ *             infinite), also where the products of decays over many rows
+ *             leave float32's range and the states do not.
  *   h0        float32 [seqs][width], the states before the first rows, or
  *             NULL for 0.
  *   final     float32 [seqs][width] or NULL: the states after the last rows

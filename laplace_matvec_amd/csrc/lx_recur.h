@@ -26,22 +26,63 @@ struct RecurLayout {
     static constexpr int kThreads = kLanes * kGroups;
 };
 
-// e^g by the hardware's base-2 exponential (1 ulp), which flushes results
-// below 2^-126: those are made 2^64 larger and scaled back, so only an e^g
-// below the smallest float32 is 0 and forgets the state.
-__device__ __forceinline__ float decay_of(float g)
+// Products of decays leave float32's range where the states that they act on
+// do not: e^-112 times 1e30 is no 0, an infinite state stays infinite under
+// any decay but 0, e^100 times 1e-20 is no infinity and 0 times any growth is
+// 0.  So a product is held as its square root r and applied as r (r h).  Below
+// 2^-298 r is kRootLeast: r (r h) is 0 for any finite h, but inf and NaN stay.
+// Above 2^256 it is kRootMost, which makes any h above 2^-127 infinite.  Such
+// a product stays there, as a state would that it acted on.  0 forgets.
+// (A product with an exponent of its own, in two words, cost up to 15 % of a
+// pass; roots cost no time that was measurable, and precision: float32 rows of
+// 4 sequences of 2048, relative error of y 1.6e-6 -> 1.9e-6.)
+constexpr float kRootLeast = 0x1p-149f, kRootMost = 0x1.fffffep127f;
+
+// Root of a decay e^g, which below the smallest float32 is 0 and from 2^256 on
+// infinite.
+__device__ __forceinline__ float root_of(float g)
 {
-    const float p = g * 1.44269504088896341f;
-    const bool low = p < -126.f;
-    const float e = __builtin_amdgcn_exp2f(low ? p + 64.f : p);
-    return low ? e * 0x1p-64f : e;
+    const float p = g * (0.5f * 1.44269504088896341f);
+    return p <= -75.f ? 0.f : __builtin_amdgcn_exp2f(p);
 }
 
-// a h + x, forgetting h where a is 0.
-__device__ __forceinline__ float step_of(float a, float h, float x) { return a == 0.f ? x : fmaf(a, h, x); }
+// r h, 0 where r is 0, whatever h is
+__device__ __forceinline__ float half_decayed(float r, float h) { return r == 0.f ? 0.f : r * h; }
+__device__ __forceinline__ float decayed(float r, float h) { return r * half_decayed(r, h); }
+// a h + x from the root of a
+__device__ __forceinline__ float step_of(float r, float h, float x) { return fmaf(r, half_decayed(r, h), x); }
 
-// Product of decays: 0, forgetting, wherever one of them is, an infinite one too.
-__device__ __forceinline__ float both_of(float a, float b) { return a == 0.f || b == 0.f ? 0.f : a * b; }
+// The root of the product of decays given by their roots.
+__device__ __forceinline__ float root_within(float m, bool least, bool most)
+{
+    return least || m < kRootLeast ? kRootLeast : most || m > kRootMost ? kRootMost : m;
+}
+struct RowsProduct {
+    float m = 1.f;
+    bool zero = false;
+
+    __device__ __forceinline__ void times(float r)
+    {
+        zero |= r == 0.f;
+        m *= r;
+    }
+    __device__ __forceinline__ float root() const { return zero ? 0.f : root_within(m, false, false); }
+};
+// The same of roots that are products themselves: what left the range stays out.
+struct GroupsProduct {
+    float m = 1.f, least = 1.f, most = 1.f;
+
+    __device__ __forceinline__ void times(float r)
+    {
+        m *= r;
+        least = fminf(least, r);
+        most = fmaxf(most, r);
+    }
+    __device__ __forceinline__ float root() const
+    {
+        return least == 0.f ? 0.f : root_within(m, least == kRootLeast, most == kRootMost);
+    }
+};
 
 // A condition that is the same in every lane, as a scalar: a branch on it is
 // then one for the whole wave, and neither side keeps the other's registers.
@@ -204,12 +245,71 @@ __device__ __forceinline__ void settle(float (&v)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
 }
 
-// How a wave goes through its rows: kCareNone if every decay is above 0;
-// kCareZero if one may be 0 or too small for the plain exponential;
+// How a wave goes through its rows: kCareNone if its decays and their
+// products are ordinary float32 values, which shows when they are composed;
+// kCareRoot if one may be 0 or out of range, so that roots are taken;
 // kCareRows if it has special rows too: first rows take h0 in and forget
 // what came before, rows of no sequence are 0.  kCareGone: all of the wave's
 // rows are past the last one, nothing is read or written.
-enum { kCareNone = 0, kCareZero = 1, kCareRows = 2, kCareGone = 3 };
+enum { kCareNone = 0, kCareRoot = 1, kCareRows = 2, kCareGone = 3 };
+
+// Products of a thread's decays, row by row.
+template <int CARE, int D, int L>
+struct RecurProducts {
+    RowsProduct p[D];
+
+    __device__ __forceinline__ void row(const float (&a)[D])
+    {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            p[d].times(a[d]);
+            asm volatile("" : "+v"(p[d].m));
+        }
+    }
+    // W + (product so far) x
+    __device__ __forceinline__ float add(int d, float x, float W) const { return step_of(p[d].root(), x, W); }
+    __device__ __forceinline__ bool roots(float (&r)[D]) const
+    {
+#pragma unroll
+        for (int d = 0; d < D; ++d) r[d] = p[d].root();
+        return true;
+    }
+};
+// The plain form.  The wave needs care unless every product of neighbouring
+// rows' decays was an ordinary value: with no decay above 4 none of at most
+// 16 exceeds 2^32, and if that of all is at least 2^-94, no part of it is
+// below 2^-126.  (A decay of NaN makes the product NaN.)
+template <int D, int L>
+struct RecurProducts<kCareNone, D, L> {
+    static_assert(L <= 16, "2^-94 and 4 hold for 16 rows");
+    float m[D], most = 0.f;
+
+    __device__ __forceinline__ RecurProducts()
+    {
+#pragma unroll
+        for (int d = 0; d < D; ++d) m[d] = 1.f;
+    }
+    __device__ __forceinline__ void row(const float (&a)[D])
+    {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            m[d] *= a[d];
+            most = fmaxf(most, a[d]);
+        }
+        settle(m);
+    }
+    __device__ __forceinline__ float add(int d, float x, float W) const { return fmaf(m[d], x, W); }
+    __device__ __forceinline__ bool roots(float (&r)[D]) const
+    {
+        bool out = !(most <= 4.f);
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            out |= !(m[d] >= 0x1p-94f);
+            r[d] = __builtin_amdgcn_sqrtf(m[d]);
+        }
+        return !uniform(__any(out));
+    }
+};
 
 // A thread's rows of x and g.  SH: one decay serves the V channels.
 template <class T, class TG, int V, int LL, bool SH>
@@ -283,14 +383,14 @@ struct RecurThread {
     {
         return CARE == kCareRows && (odd >> j & 1u);
     }
-    // Row j: its decays, and h -> a h + x.
+    // Row j: its decays (with care their roots), and h -> a h + x.
     template <int CARE>
     __device__ __forceinline__ void decays(const RecurRows* R, int j, float (&a)[D]) const
     {
         g.get(j, a);
 #pragma unroll
         for (int d = 0; d < D; ++d)
-            a[d] = CARE ? decay_of(a[d]) : __builtin_amdgcn_exp2f(a[d] * 1.44269504088896341f);
+            a[d] = CARE ? root_of(a[d]) : __builtin_amdgcn_exp2f(a[d] * 1.44269504088896341f);
         if (special<CARE>(j) && R->start[r0 + j] != -1) {
 #pragma unroll
             for (int d = 0; d < D; ++d) a[d] = 0.f;
@@ -312,7 +412,7 @@ struct RecurThread {
                 load_vec<V>(A.h0 + (int64_t)q * A.width + col(), h0);
                 g.get(j, b);
 #pragma unroll
-                for (int v = 0; v < V; ++v) t[v] = step_of(decay_of(b[SH ? 0 : v]), h0[v], t[v]);
+                for (int v = 0; v < V; ++v) t[v] = step_of(root_of(b[SH ? 0 : v]), h0[v], t[v]);
             }
         }
 #pragma unroll
@@ -320,12 +420,12 @@ struct RecurThread {
             h[v] = CARE ? step_of(a[SH ? 0 : v], h[v], t[v]) : fmaf(a[SH ? 0 : v], h[v], t[v]);
         settle(h);
     }
-    // Composed map of the thread's rows: h -> m h + H.
+    // Composed map of the thread's rows: h -> r (r h) + H.  False if the wave
+    // has to take care and did not.
     template <int CARE>
-    __device__ __forceinline__ void compose(const RecurArgs& A, const RecurRows* R, float (&m)[D], float (&H)[V]) const
+    __device__ __forceinline__ bool compose(const RecurArgs& A, const RecurRows* R, float (&r)[D], float (&H)[V]) const
     {
-#pragma unroll
-        for (int d = 0; d < D; ++d) m[d] = 1.f;
+        RecurProducts<CARE, D, L> m;
 #pragma unroll
         for (int v = 0; v < V; ++v) H[v] = 0.f;
 #pragma unroll
@@ -333,30 +433,18 @@ struct RecurThread {
             float a[D];
             decays<CARE>(R, j, a);
             step<CARE>(A, R, j, a, H);
-#pragma unroll
-            for (int d = 0; d < D; ++d) m[d] = CARE ? both_of(m[d], a[d]) : m[d] * a[d];
-            settle(m);
+            m.row(a);
         }
+        return m.roots(r);
     }
 };
-
-// Whether any of a wave's products of decays is 0, so that some decay may
-// be, or NaN (a decay of 0 times one that is infinite).
-template <int D>
-__device__ __forceinline__ bool any_zero(const float (&m)[D])
-{
-    bool z = false;
-#pragma unroll
-    for (int d = 0; d < D; ++d) z |= !(m[d] > 0.f);
-    return uniform(__any(z));
-}
 
 // ---- between tiles -------------------------------------------------------
 //
 // One pass over the data: a workgroup takes the next row tile of its channel
 // tile (in ticket order, so those before it have been taken too and their
 // workgroups run), composes its rows' maps, publishes the tile's map
-// h -> A h + H, finds the state that enters it and publishes the state that
+// h -> r (r h) + H, finds the state that enters it and publishes the state that
 // leaves it.  Words say by themselves whether they have been written: all
 // ones, a NaN that is never stored (NaNs are stored as 0x7fc00000), means
 // not yet.  They are moved by relaxed agent-scope atomics, which bypass the
@@ -370,9 +458,9 @@ constexpr uint64_t kNoMap = ~(uint64_t)0;
 constexpr uint32_t kNoState = ~(uint32_t)0;
 
 __device__ __forceinline__ uint32_t state_bits(float h) { return h == h ? __float_as_uint(h) : 0x7fc00000u; }
-__device__ __forceinline__ uint64_t map_bits(float a, float h)
+__device__ __forceinline__ uint64_t map_bits(float r, float h)
 {
-    return (uint64_t)state_bits(h) << 32 | __float_as_uint(a);
+    return (uint64_t)state_bits(h) << 32 | __float_as_uint(r);
 }
 
 // State entering `tile` (> 0) for this lane's channel; maps and states point
@@ -414,22 +502,22 @@ __device__ __forceinline__ float look_back(const uint64_t* maps, const uint32_t*
     }
 }
 
-// The tile's map (a, h) of this lane's channel -> the state entering it.
+// The tile's map (r, h) of this lane's channel -> the state entering it.
 // `fresh`: nothing enters (its first row starts a sequence or has none);
 // `last`: no tile follows.  One whole wave.
-__device__ __forceinline__ float pass_state(const RecurArgs& A, int64_t tile, int ct, float a, float h, bool fresh,
+__device__ __forceinline__ float pass_state(const RecurArgs& A, int64_t tile, int ct, float r, float h, bool fresh,
                                             bool last)
 {
     const int64_t ld = (int64_t)A.cols * kRecurCols;
     const int64_t c = (int64_t)ct * kRecurCols + lane_id();
-    const bool cut = __all(a == 0.f);  // the leaving state does not depend on the entering one
+    const bool cut = __all(r == 0.f);  // the leaving state does not depend on the entering one
     if (!last) {
         if (cut) st_agent(A.states + tile * ld + c, state_bits(h));
-        else st_agent(A.maps + tile * ld + c, map_bits(a, h));
+        else st_agent(A.maps + tile * ld + c, map_bits(r, h));
     }
     float in = 0.f;
     if (!fresh && tile > 0) in = look_back(A.maps + c, A.states + c, ld, tile);
-    if (!last && !cut) st_agent(A.states + tile * ld + c, state_bits(step_of(a, in, h)));
+    if (!last && !cut) st_agent(A.states + tile * ld + c, state_bits(step_of(r, in, h)));
     return in;
 }
 

@@ -36,7 +36,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     using Th = RecurThread<T, TG, V, L, SH>;
     using Lay = RecurLayout<V, L>;
     __shared__ RecurRows rows;
-    __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
+    __shared__ float sr[Lay::kGroups][Lay::kLanes * Th::D];
     __shared__ float sh[Lay::kGroups][kRecurCols];
     const int ct = channel_tile(A, (uint32_t)group_id<Lay::kThreads>());
     const int64_t tile = next_tile(A, ct);
@@ -45,37 +45,37 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     Th th;
     th.load(A, tile, ct);
     const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, mark, rows)) ? &rows : nullptr;
-    float m[Th::D], h[V];
+    float r[Th::D], h[V];
     int care = th.find_odd(A, R);
 #pragma unroll
-    for (int d = 0; d < Th::D; ++d) m[d] = 0.f;
+    for (int d = 0; d < Th::D; ++d) r[d] = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = 0.f;
     if (care == kCareNone) {
-        th.template compose<kCareNone>(A, R, m, h);
-        if (any_zero(m)) care = kCareZero;
+        if (!th.template compose<kCareNone>(A, R, r, h)) care = kCareRoot;
     }
-    if (care == kCareZero) th.template compose<kCareZero>(A, R, m, h);
-    if (care == kCareRows) th.template compose<kCareRows>(A, R, m, h);
+    if (care == kCareRoot) th.template compose<kCareRoot>(A, R, r, h);
+    if (care == kCareRows) th.template compose<kCareRows>(A, R, r, h);
 #pragma unroll
-    for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
+    for (int d = 0; d < Th::D; ++d) sr[th.group][th.lane * Th::D + d] = r[d];
 #pragma unroll
     for (int v = 0; v < V; ++v) sh[th.group][th.lane * V + v] = h[v];
     __syncthreads();
     if (threadIdx.x < kRecurCols) {
         const int c = threadIdx.x;
-        float am = 1.f, ah = 0.f;
+        GroupsProduct all;
+        float ah = 0.f;
 #pragma unroll 8
         for (int i = 0; i < Lay::kGroups; ++i) {
-            const float a = sa[i][SH ? c / V : c];
+            const float a = sr[i][SH ? c / V : c];
             ah = step_of(a, ah, sh[i][c]);
-            am = both_of(am, a);
+            all.times(a);
         }
         float e = 0.f;
-        if (A.tiles > 1) e = pass_state(A, tile, ct, am, ah, R && R->start[0] != -1, tile == A.tiles - 1);
+        if (A.tiles > 1) e = pass_state(A, tile, ct, all.root(), ah, R && R->start[0] != -1, tile == A.tiles - 1);
 #pragma unroll 8
         for (int i = 0; i < Lay::kGroups; ++i) {
-            const float next = step_of(sa[i][SH ? c / V : c], e, sh[i][c]);
+            const float next = step_of(sr[i][SH ? c / V : c], e, sh[i][c]);
             sh[i][c] = e;  // state entering group i
             e = next;
         }
@@ -84,7 +84,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = sh[th.group][th.lane * V + v];
     if (care == kCareNone) write_rows<kCareNone, Th, T>(A, R, th, h);
-    else if (care == kCareZero) write_rows<kCareZero, Th, T>(A, R, th, h);
+    else if (care == kCareRoot) write_rows<kCareRoot, Th, T>(A, R, th, h);
     else if (care == kCareRows) write_rows<kCareRows, Th, T>(A, R, th, h);
 }
 
@@ -167,10 +167,7 @@ __global__ __launch_bounds__(256) void lx_recur_step(RecurStepArgs A)
             for (int v = 0; v < V; ++v) a[v] = one;
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float d = decay_of(a[v]);
-            h[v] = d == 0.f ? x[v] : fmaf(d, h[v], x[v]);
-        }
+        for (int v = 0; v < V; ++v) h[v] = step_of(root_of(a[v]), h[v], x[v]);
         store_vec<V>(st, h);
     }
     store_vec<V>((T*)A.y + b * A.ldy + col, h);

@@ -40,15 +40,15 @@ __device__ __forceinline__ void row_dy(const RecurArgs& A, const RecurRows* R, c
     }
 }
 
-// Both maps of the thread's rows: the state after them, h -> m h + H, and the
-// gradient before them, w -> m w + W.  In row order W is the sum of dy_j
-// times the product of the decays up to row j, so one sweep gives both.
+// Both maps of the thread's rows: the state after them, h -> r (r h) + H, and
+// the gradient before them, w -> r (r w) + W.  In row order W is the sum of
+// dy_j times the product of the decays up to row j, so one sweep gives both.
+// False if the wave has to take care and did not.
 template <int CARE, class Th, class T, int V>
-__device__ __forceinline__ void compose_both(const RecurArgs& A, const RecurRows* R, const Th& th,
-                                             const RowPack<T, V, Th::L>& dy, float (&m)[Th::D], float (&H)[V], float (&W)[V])
+__device__ __forceinline__ bool compose_both(const RecurArgs& A, const RecurRows* R, const Th& th,
+                                             const RowPack<T, V, Th::L>& dy, float (&r)[Th::D], float (&H)[V], float (&W)[V])
 {
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) m[d] = 1.f;
+    RecurProducts<CARE, Th::D, Th::L> m;
 #pragma unroll
     for (int v = 0; v < V; ++v) H[v] = W[v] = 0.f;
 #pragma unroll
@@ -57,16 +57,12 @@ __device__ __forceinline__ void compose_both(const RecurArgs& A, const RecurRows
         th.template decays<CARE>(R, j, a);
         th.template step<CARE>(A, R, j, a, H);
         row_dy<CARE, Th, T, V>(A, R, th, dy, j, d);
+        m.row(a);
 #pragma unroll
-        for (int i = 0; i < Th::D; ++i) m[i] = CARE ? both_of(m[i], a[i]) : m[i] * a[i];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float mv = m[Th::D == 1 ? 0 : v];
-            W[v] = CARE && mv == 0.f ? W[v] : fmaf(mv, d[v], W[v]);
-        }
-        settle(m);
+        for (int v = 0; v < V; ++v) W[v] = m.add(Th::D == 1 ? 0 : v, d[v], W[v]);
         settle(W);
     }
+    return m.roots(r);
 }
 
 // dg of one row from a product per channel, one channel per lane: the lanes
@@ -126,9 +122,9 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             if (A.h0 && th.in) load_vec<V>(A.h0 + (int64_t)q * A.width + th.col(), h0);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float av = decay_of(g[SH ? 0 : v]);
+                const float av = root_of(g[SH ? 0 : v]);
                 u[v] += w[v];
-                out[v] = av == 0.f ? 0.f : av * u[v];
+                out[v] = decayed(av, u[v]);
                 p[v] = av == 0.f ? 0.f : out[v] * h0[v];
                 w[v] = 0.f;
             }
@@ -138,7 +134,7 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             for (int v = 0; v < V; ++v) {
                 const float av = a[SH ? 0 : v];
                 u[v] += w[v];
-                w[v] = CARE && av == 0.f ? 0.f : av * u[v];
+                w[v] = CARE ? decayed(av, u[v]) : av * u[v];
                 p[v] = CARE && av == 0.f ? 0.f : w[v] * before[j][v];
             }
         }
@@ -199,7 +195,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     using Th = RecurThread<T, TG, V, L, SH>;
     using Lay = RecurLayout<V, L>;
     __shared__ RecurRows rows;
-    __shared__ float sa[Lay::kGroups][Lay::kLanes * Th::D];
+    __shared__ float sr[Lay::kGroups][Lay::kLanes * Th::D];
     __shared__ float sh[Lay::kGroups][kRecurCols];
     __shared__ float sw[Lay::kGroups][kRecurCols];
     constexpr bool kSums = SH && V > 1;
@@ -215,20 +211,19 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     if (th.gone(A)) dy.clear();
     else dy.load(th.template at<T, V>(A.dy, A.lddy), th.whole, th.last, A.stream);
     const RecurRows* R = uniform(recur_rows<Lay::kThreads>(A, tile * kRecurTile, mark, rows)) ? &rows : nullptr;
-    float m[Th::D], h[V], w[V];
+    float r[Th::D], h[V], w[V];
     int care = th.find_odd(A, R);
 #pragma unroll
-    for (int d = 0; d < Th::D; ++d) m[d] = 0.f;
+    for (int d = 0; d < Th::D; ++d) r[d] = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = w[v] = 0.f;
     if (care == kCareNone) {
-        compose_both<kCareNone, Th, T, V>(A, R, th, dy, m, h, w);
-        if (any_zero(m)) care = kCareZero;
+        if (!compose_both<kCareNone, Th, T, V>(A, R, th, dy, r, h, w)) care = kCareRoot;
     }
-    if (care == kCareZero) compose_both<kCareZero, Th, T, V>(A, R, th, dy, m, h, w);
-    if (care == kCareRows) compose_both<kCareRows, Th, T, V>(A, R, th, dy, m, h, w);
+    if (care == kCareRoot) compose_both<kCareRoot, Th, T, V>(A, R, th, dy, r, h, w);
+    if (care == kCareRows) compose_both<kCareRows, Th, T, V>(A, R, th, dy, r, h, w);
 #pragma unroll
-    for (int d = 0; d < Th::D; ++d) sa[th.group][th.lane * Th::D + d] = m[d];
+    for (int d = 0; d < Th::D; ++d) sr[th.group][th.lane * Th::D + d] = r[d];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         sh[th.group][th.lane * V + v] = h[v];
@@ -238,20 +233,21 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     // one wave carries the gradient, another the state
     const int c = lane_id();
     if (threadIdx.x < kWave) {
-        float am = 1.f, aw = 0.f;
+        GroupsProduct all;
+        float aw = 0.f;
 #pragma unroll 8
         for (int i = Lay::kGroups - 1; i >= 0; --i) {
-            const float a = sa[i][SH ? c / V : c];
+            const float a = sr[i][SH ? c / V : c];
             aw = step_of(a, aw, sw[i][c]);
-            am = both_of(am, a);
+            all.times(a);
         }
         // nothing comes back into a tile whose last row ends a sequence or has none
         const bool fresh = R && (R->last[kRecurTile - 1] != -1 || R->start[kRecurTile - 1] == -2);
         float b = 0.f;
-        if (A.tiles > 1) b = pass_state(A, back, ct, am, aw, fresh, back == A.tiles - 1);
+        if (A.tiles > 1) b = pass_state(A, back, ct, all.root(), aw, fresh, back == A.tiles - 1);
 #pragma unroll 8
         for (int i = Lay::kGroups - 1; i >= 0; --i) {
-            const float next = step_of(sa[i][SH ? c / V : c], b, sw[i][c]);
+            const float next = step_of(sr[i][SH ? c / V : c], b, sw[i][c]);
             sw[i][c] = b;  // gradient entering group i from the rows after it
             b = next;
         }
@@ -259,7 +255,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
         float e = tile > 0 ? A.states_in[((tile - 1) * A.cols + ct) * kRecurCols + c] : 0.f;
 #pragma unroll 8
         for (int i = 0; i < Lay::kGroups; ++i) {
-            const float next = step_of(sa[i][SH ? c / V : c], e, sh[i][c]);
+            const float next = step_of(sr[i][SH ? c / V : c], e, sh[i][c]);
             sh[i][c] = e;  // state entering group i
             e = next;
         }
@@ -271,7 +267,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
         w[v] = sw[th.group][th.lane * V + v];
     }
     if (care == kCareNone) write_grads<kCareNone>(A, R, th, dy, ct, h, w, s_sum);
-    else if (care == kCareZero) write_grads<kCareZero>(A, R, th, dy, ct, h, w, s_sum);
+    else if (care == kCareRoot) write_grads<kCareRoot>(A, R, th, dy, ct, h, w, s_sum);
     else if (care == kCareRows) write_grads<kCareRows>(A, R, th, dy, ct, h, w, s_sum);
     if (kSums && A.dg) {
         __syncthreads();
