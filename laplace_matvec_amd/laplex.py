@@ -378,15 +378,19 @@ def _flat(t, name, dtype, shape, device):
 _HERE = contextlib.nullcontext()
 
 
-def _launch(stream, device):
+def _launch(stream, device, *inputs):
     """(stream handle, context in which outputs and scratch are allocated):
-    with a stream other than the current one they come from its own pool."""
+    with a stream other than the current one they come from its own pool, and
+    the inputs' memory is not given out again before that stream is done."""
     if stream is None:
         # the handle alone: a Stream object would cost as much as the launch
         s = torch._C._cuda_getCurrentRawStream(device.index)
         return s, _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
@@ -431,7 +435,7 @@ def laplex_route(experts, n_experts: int, stream=None) -> Route:
     tokens, slots = experts.shape[0], 1 if experts.dim() == 1 else experts.shape[1]
     lib, dev = load(), experts.device
     need = _size(lib.laplex_route_workspace(tokens, slots, n_experts), "laplex_route")
-    s, ctx = _launch(stream, dev)
+    s, ctx = _launch(stream, dev, experts)
     with ctx:
         order = torch.empty(tokens * slots, dtype=torch.int32, device=dev)
         place = torch.empty((tokens, slots), dtype=torch.int32, device=dev)
@@ -450,7 +454,7 @@ def laplex_dispatch(route: Route, x, stream=None):
     place, offsets, tokens, slots, experts = _route_parts(route, x.device)
     if x.dim() != 2 or rows != tokens:
         raise ValueError(f"x must have shape [{tokens}][width]")
-    s, ctx = _launch(stream, x.device)
+    s, ctx = _launch(stream, x.device, place, offsets, x)
     with ctx:
         xs = x.new_empty((tokens * slots, width))
         _check(load().laplex_dispatch(tokens, slots, experts, _at(place), _at(offsets), _DTYPES[x.dtype], width,
@@ -466,7 +470,7 @@ def laplex_combine(route: Route, ys, weights=None, stream=None):
     if ys.dim() != 2 or rows != tokens * slots:
         raise ValueError(f"ys must have shape [{tokens * slots}][width]")
     weights = _flat(weights, "weights", torch.float32, (tokens, slots), ys.device)
-    s, ctx = _launch(stream, ys.device)
+    s, ctx = _launch(stream, ys.device, place, ys, weights)
     with ctx:
         y = ys.new_empty((tokens, width))
         _check(load().laplex_combine(tokens, slots, _at(place), _DTYPES[ys.dtype], width, _at(ys), ld,
@@ -486,7 +490,7 @@ def laplex_combine_backward(route: Route, dy, ys, weights, stream=None):
     if weights is None:
         raise TypeError("weights must be given")
     weights = _flat(weights, "weights", torch.float32, (tokens, slots), dy.device)
-    s, ctx = _launch(stream, dy.device)
+    s, ctx = _launch(stream, dy.device, place, offsets, dy, ys, weights)
     with ctx:
         dys = dy.new_empty((tokens * slots, width))
         dw = weights.new_empty((tokens, slots))
@@ -533,7 +537,7 @@ def laplex_recur(x, g, offsets=None, h0=None, final: bool = False, keep: bool = 
     n, seqs, width, heads, ldx, ldg = _recur_parts(x, g, offsets, h0)
     lib, dev = load(), x.device
     need = _size(lib.laplex_recur_workspace(n, width, heads, 0), "laplex_recur")
-    s, ctx = _launch(stream, dev)
+    s, ctx = _launch(stream, dev, x, g, offsets, h0)
     with ctx:
         y = _new_like(x)
         hf = torch.empty((seqs, width), dtype=torch.float32, device=dev) if final else None
@@ -562,7 +566,7 @@ def laplex_recur_backward(x, g, dy, states, offsets=None, h0=None, dfinal=None, 
         raise TypeError("states must be those of laplex_recur(keep=True)")
     _flat(states, "states", torch.float32, (lib.laplex_recur_states(n, width),), dev)
     _flat(dfinal, "dfinal", torch.float32, (seqs, width), dev)
-    s, ctx = _launch(stream, dev)
+    s, ctx = _launch(stream, dev, x, g, dy, states, offsets, h0, dfinal)
     out = {}
     with ctx:
         if "dx" in want:
@@ -599,7 +603,7 @@ def laplex_recur_step(x, g, state, slots=None, stream=None):
     _flat(slots, "slots", torch.int32, (n,), dev)
     if g.device != dev:
         raise ValueError(f"g must be on {dev}")
-    s, ctx = _launch(stream, dev)
+    s, ctx = _launch(stream, dev, x, g, state, slots)
     with ctx:
         y = _new_like(x)
         _check(load().laplex_recur_step(n, state.shape[0], _at(slots), width, heads, _DTYPES[x.dtype],
