@@ -378,7 +378,11 @@ hipError_t gram_launch(const GramArgs& a, hipStream_t s);
 
 // ---- token routing (route.hip) ----
 constexpr int kRouteTile = 2048;        // slots per workgroup
-constexpr int kRouteSingle = 4096;      // slots up to which one workgroup does everything
+// Slots up to which one workgroup does everything.  Calls in a graph, 64
+// experts: one launch 9.3 us for 1500 to 4096 slots, three 12.1; with 8192 in
+// one workgroup 16, three launches 12.2.  (Up to 1024 slots a workgroup of
+// that tile took 4.3, against 9.1.)
+constexpr int kRouteSingle = 4096;
 constexpr int kRouteMaxExperts = 4096;  // 80 KB of counters in LDS
 struct RouteArgs {
     const void* ids = nullptr;  // [n] int32, or int64 if wide

@@ -552,10 +552,15 @@ __device__ __forceinline__ bool past_tiles(const RecurArgs& A, int64_t tile) { r
 inline bool recur_wide(const RecurArgs& a) { return a.width >= 4 && (a.per == 1 || a.per % 4 == 0); }
 
 // With no more than a workgroup per CU the pass is bound by one tile's
-// latency: 1024 threads of 4 rows instead of 256 of 16, whose straight code
-// is four times as long to fetch.  777 x 512 bf16 forward 17.4 -> 10.5 us,
-// 2048 x 2048 16.8 -> 14.1; at 512 workgroups it is slower (float32
-// 2048 x 4096 24.7 -> 29.8).
+// latency: 1024 threads of 4 rows instead of 256 of 16 (or 512 of 8, see
+// kGradRows), whose straight code is two to four times as long to fetch.
+// Calls in a graph, us, 1024 threads against the others, forward and backward:
+//                         128 workgroups    256               512               1024
+//   bf16, own decays      14.8/17.1 17.7/18.7   16.0/18.3 19.1/20.3   19.4/21.8 29.9/24.3   32.4/28.4 49.8/44.8
+//   bf16, shared          13.3/14.4 15.9/21.4   14.4/15.5 17.2/22.8   17.1/18.5 25.8/26.4   28.0/23.2 43.2/40.0
+//   float32, own decays   15.7/17.7 18.9/20.4   19.1/21.0 22.8/23.9   31.5/26.5 37.8/39.2   52.9/45.4 68.2/67.7
+//   float32, shared       14.2/14.9 17.0/18.0   16.1/16.7 19.2/20.1   20.3/20.6 31.2/24.6   34.9/29.9 53.0/40.6
+// Up to 256 it is faster in all of them, at 512 in some, at 1024 in none.
 inline bool recur_few(const RecurArgs& a) { return a.tiles * a.cols <= 256; }
 
 // Clears what a pass publishes and marks the tiles (with more than one tile),

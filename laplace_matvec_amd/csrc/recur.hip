@@ -2,9 +2,9 @@
 // the mathematics, the tile layout and how tiles hand their states on.
 //
 // One pass: x and g are read once and y is written once, bound by memory.
-// 65536 x 2048 bf16 with a decay per channel: 148 us, 5.4 TB/s (three passes,
-// tile maps, carries, rows: 284); packed 32768 x 4096 bf16 with a decay per 64
-// channels: 112 us, 4.8 TB/s.  Few tiles are bound by a tile's latency, some
+// 65536 x 2048 bf16 with a decay per channel: 149 us, 5.4 TB/s (three passes,
+// tile maps, carries, rows: 289 the call); packed 32768 x 4096 bf16 with a decay
+// per 64 channels: 115 us, 4.7 TB/s.  Few tiles are bound by a tile's latency, some
 // 10 us: load, compose, hand over, write.
 #include "lx_recur.h"
 
@@ -137,7 +137,7 @@ hipError_t recur_type(const RecurArgs& a, hipStream_t s)
     return recur_go<T, TG, 1, 16, true>(a, s);
 }
 
-// Bound by its launch: 256 requests of 4096 channels move 13 MB in 4.7 us.
+// Bound by its launch: 256 requests of 4096 channels move 13 MB in 4.6 us.
 // One token for each request: state[slot] = e^g state[slot] + x, y = the new state.
 template <class T, class TG, int V>
 __global__ __launch_bounds__(256) void lx_recur_step(RecurStepArgs A)

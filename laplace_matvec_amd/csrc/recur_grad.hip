@@ -8,10 +8,11 @@
 // serves several channels is the sum over them.  The states h_{t-1} are made
 // again in float32 from x and the saved states between row tiles (1/256 of
 // x's values), which reads no more than a saved y would and loses nothing to
-// y's rounding.  Packed 32768 x 4096 bf16 with a decay per 64 channels: 213
-// to 222 us, 3.7 TB/s of x, dy and dx, bound by what a tile waits for (loads
-// 3 us, hand-over 3, writing 4 of 12, three workgroups per CU); a decay per
-// channel: 5.7 TB/s.  Where a_t is 0 the state was forgotten and w_t and dg_t are 0.
+// y's rounding.  Packed 32768 x 4096 bf16 with a decay per 64 channels: 222
+// us (212 to 233 between launches), 3.7 TB/s of x, dy and dx, bound by what a
+// tile waits for (loads 3 us, hand-over 3, writing 4 of 12, three workgroups
+// per CU) and by dg, whose 4-byte values 256 bytes apart cost 18 % more bytes
+// than they are; a decay per channel: 289 us, 4.6 TB/s.  Where a_t is 0 the state was forgotten and w_t and dg_t are 0.
 #include "lx_recur.h"
 
 namespace lx {
@@ -178,11 +179,11 @@ __device__ __forceinline__ void tile_sums(const RecurArgs& A, int64_t tile, int 
 
 // Rows of a thread and waves per SIMD to compile for.  What counts is bytes
 // in flight per CU: half rows with shared decays take 16 rows per thread,
-// three workgroups of 256 threads (225 -> 205 us packed 32768 x 4096); the
-// others 8 rows, two workgroups of 512, also where that spills a few
-// registers (bf16 rows with float32 decays of their own 380 -> 308 us at
-// 4 x 8192 x 4096, shared float32 330 -> 277).  float32 rows with decays of
-// their own would spill too many (461 -> 549).
+// three workgroups of 256 threads (calls of 4 x 8192 x 4096: 191 us, 8 rows
+// 210); the others 8 rows, two workgroups of 512, also where that spills a
+// few registers (bf16 rows with float32 decays of their own 326 us, without
+// 406; shared float32 301, 374).  float32 rows with decays of their own would
+// spill too many (579 us, without 541).
 template <class T, bool SH>
 constexpr int kGradRows = sizeof(T) == 2 && SH ? 16 : 8;
 template <class T, bool SH>

@@ -13,7 +13,7 @@
 // of them in order, 64 at a time; lanes of one id find each other by ballots
 // over the id's bits and count the lanes below, a counter per wave and id in
 // LDS carries the rest.  Up to kRouteSingle slots one launch does everything
-// (bound by its latency, 4 us, 10 with the host's part); above, tiles of
+// (bound by its latency, 4 us, 11 with the host's part); above, tiles of
 // kRouteTile slots are counted, their counts scanned along the tiles (E
 // columns of `tiles` counts) and the slots placed, three launches.  A wave's
 // rounds wait for each other's counters, so shorter tiles, more of them at a
@@ -32,7 +32,7 @@
 // and is bound by memory.  Rows by expert are moved past the caches: an array
 // of them is read or written once here, in scattered pieces, and filling the
 // caches with it makes the next kernel wait for their write-back (dispatch
-// and combine of 65536 rows of 4 KB: 61 + 92 us through the caches, 57 + 54
+// and combine of 65536 rows of 4 KB: 61 + 92 us through the caches, 58 + 55
 // past them; 8192 rows followed by a product that reads them all: 30.6 us,
 // 23.2).  Sums are float32 in ascending k; a dropped slot's
 // weight and row are never used, whatever they hold.
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(256) void lx_combine(MoveArgs A)
 
 // G threads of a 256-thread workgroup per token; the dot products of KC
 // slots are carried along one pass over the row.  16384 tokens x 4 rows of
-// 2048 bf16: 105 us, 5.8 TB/s (a wave per token there: 135).
+// 2048 bf16: 107 us, 5.7 TB/s.
 template <int V, class T, int KC, int G>
 __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
 {
@@ -453,8 +453,11 @@ hipError_t move_launch(MoveKind kind, MoveArgs a, hipStream_t s)
             LX_LAUNCH("combine", s, (lx_combine<V, T, KC><<<grid_of<256>(blocks), 256, 0, s>>>(a)));
             return hipSuccess;
         case kMoveCombineGrad:
-            // a wave per token while a row is at most two loads per lane, a
-            // workgroup above: see the kernel
+            // A wave per token while a row is at most two loads per lane, a
+            // workgroup above.  bf16, wave against workgroup, us by groups of
+            // a row (64, 128, 192, 256): 16384 tokens x 4 rows 28/56, 51/64,
+            // 80/81, 115/100; 2048 x 2 5.1/7.1, 6.6/8.5, 8.3/9.5, 10.1/10.3;
+            // 64 x 8 5.8/5.5, 7.5/5.7, 9.1/5.9, 10.6/6.2.
             if (a.groups <= 2 * kWave)
                 LX_LAUNCH("combine_grad", s,
                           (lx_combine_grad<V, T, KC, 64><<<grid_of<256>((a.tokens + 3) / 4), 256, 0, s>>>(a)));
