@@ -2,9 +2,9 @@
 // the mathematics, the tile layout and how tiles hand their states on.
 //
 // One pass: x and g are read once and y is written once, bound by memory.
-// 65536 x 2048 bf16 with a decay per channel: 149 us, 5.4 TB/s (three passes,
+// 65536 x 2048 bf16 with a decay per channel: 148 us, 5.4 TB/s (three passes,
 // tile maps, carries, rows: 289 the call); packed 32768 x 4096 bf16 with a decay
-// per 64 channels: 115 us, 4.7 TB/s.  Few tiles are bound by a tile's latency, some
+// per 64 channels: 119 us, 4.6 TB/s.  Few tiles are bound by a tile's latency, some
 // 10 us: load, compose, hand over, write.
 #include "lx_recur.h"
 
@@ -20,9 +20,9 @@ __device__ __forceinline__ void write_rows(const RecurArgs& A, const RecurRows* 
 #pragma unroll
     for (int j = 0; j < Th::L; ++j) {
         float a[Th::D];
-        th.template decays<CARE>(R, j, a);
-        th.template step<CARE>(A, R, j, a, h);
-        if (CARE == kCareRows ? j < th.rows : th.in) store_vec_as<V>(y.row(j), h, A.stream);
+        const bool cut = th.template decays<CARE>(R, j, a);
+        th.template step<CARE>(A, R, j, a, cut, h);
+        if (care_rows(CARE) ? j < th.rows : th.in) store_vec_as<V>(y.row(j), h, A.stream);
         if (th.template special<CARE>(j) && A.final && th.in) {
             const int q = R->last[th.r0 + j];
             if (q >= 0) store_vec<V>(A.final + (int64_t)q * A.width + th.col(), h);
@@ -36,7 +36,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     using Th = RecurThread<T, TG, V, L, SH>;
     using Lay = RecurLayout<V, L>;
     __shared__ RecurRows rows;
-    __shared__ float sr[Lay::kGroups][Lay::kLanes * Th::D];
+    __shared__ RecurGroups<V, L, SH> groups;
     __shared__ float sh[Lay::kGroups][kRecurCols];
     const int ct = channel_tile(A, (uint32_t)group_id<Lay::kThreads>());
     const int64_t tile = next_tile(A, ct);
@@ -51,34 +51,27 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     for (int d = 0; d < Th::D; ++d) r[d] = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = 0.f;
+    // kCareBoth is rare: its code lies behind the others'
     if (care == kCareNone) {
         if (!th.template compose<kCareNone>(A, R, r, h)) care = kCareRoot;
+    } else if (care == kCareRows) {
+        if (!th.template compose<kCareRows>(A, R, r, h)) care = kCareBoth;
     }
     if (care == kCareRoot) th.template compose<kCareRoot>(A, R, r, h);
-    if (care == kCareRows) th.template compose<kCareRows>(A, R, r, h);
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) sr[th.group][th.lane * Th::D + d] = r[d];
+    if (__builtin_expect(care == kCareBoth, 0)) th.template compose<kCareBoth>(A, R, r, h);
+    groups.put(th.group, th.lane, care, r);
 #pragma unroll
     for (int v = 0; v < V; ++v) sh[th.group][th.lane * V + v] = h[v];
     __syncthreads();
     if (threadIdx.x < kRecurCols) {
-        const int c = threadIdx.x;
-        GroupsProduct all;
-        float ah = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < Lay::kGroups; ++i) {
-            const float a = sr[i][SH ? c / V : c];
-            ah = step_of(a, ah, sh[i][c]);
-            all.times(a);
-        }
+        const uint32_t waves = groups.rooted();
         float e = 0.f;
-        if (A.tiles > 1) e = pass_state(A, tile, ct, all.root(), ah, R && R->start[0] != -1, tile == A.tiles - 1);
-#pragma unroll 8
-        for (int i = 0; i < Lay::kGroups; ++i) {
-            const float next = step_of(sr[i][SH ? c / V : c], e, sh[i][c]);
-            sh[i][c] = e;  // state entering group i
-            e = next;
+        if (A.tiles > 1) {
+            float ah;
+            const float ar = groups.template compose<false>(waves, sh, ah);
+            e = pass_state(A, tile, ct, ar, ah, R && R->start[0] != -1, tile == A.tiles - 1);
         }
+        groups.template enter<false>(waves, sh, e);
     }
     __syncthreads();
 #pragma unroll
@@ -86,6 +79,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) void lx_recur_pass(R
     if (care == kCareNone) write_rows<kCareNone, Th, T>(A, R, th, h);
     else if (care == kCareRoot) write_rows<kCareRoot, Th, T>(A, R, th, h);
     else if (care == kCareRows) write_rows<kCareRows, Th, T>(A, R, th, h);
+    else if (__builtin_expect(care == kCareBoth, 0)) write_rows<kCareBoth, Th, T>(A, R, th, h);
 }
 
 // Blocks [0, fill): 16 bytes of all ones per thread over the published
@@ -137,7 +131,7 @@ hipError_t recur_type(const RecurArgs& a, hipStream_t s)
     return recur_go<T, TG, 1, 16, true>(a, s);
 }
 
-// Bound by its launch: 256 requests of 4096 channels move 13 MB in 4.6 us.
+// Bound by its launch: 256 requests of 4096 channels move 13 MB in 4.2 us.
 // One token for each request: state[slot] = e^g state[slot] + x, y = the new state.
 template <class T, class TG, int V>
 __global__ __launch_bounds__(256) void lx_recur_step(RecurStepArgs A)

@@ -8,11 +8,11 @@
 // serves several channels is the sum over them.  The states h_{t-1} are made
 // again in float32 from x and the saved states between row tiles (1/256 of
 // x's values), which reads no more than a saved y would and loses nothing to
-// y's rounding.  Packed 32768 x 4096 bf16 with a decay per 64 channels: 222
-// us (212 to 233 between launches), 3.7 TB/s of x, dy and dx, bound by what a
+// y's rounding.  Packed 32768 x 4096 bf16 with a decay per 64 channels: 230
+// us (214 to 247 between launches), 3.6 TB/s of x, dy and dx, bound by what a
 // tile waits for (loads 3 us, hand-over 3, writing 4 of 12, three workgroups
 // per CU) and by dg, whose 4-byte values 256 bytes apart cost 18 % more bytes
-// than they are; a decay per channel: 289 us, 4.6 TB/s.  Where a_t is 0 the state was forgotten and w_t and dg_t are 0.
+// than they are; a decay per channel: 281 us, 4.8 TB/s.  Where a_t is 0 the state was forgotten and w_t and dg_t are 0.
 #include "lx_recur.h"
 
 namespace lx {
@@ -49,21 +49,21 @@ template <int CARE, class Th, class T, int V>
 __device__ __forceinline__ bool compose_both(const RecurArgs& A, const RecurRows* R, const Th& th,
                                              const RowPack<T, V, Th::L>& dy, float (&r)[Th::D], float (&H)[V], float (&W)[V])
 {
-    RecurProducts<CARE, Th::D, Th::L> m;
+    RecurProducts<care_root(CARE), Th::D, Th::L> m;
 #pragma unroll
     for (int v = 0; v < V; ++v) H[v] = W[v] = 0.f;
 #pragma unroll
     for (int j = 0; j < Th::L; ++j) {
         float a[Th::D], d[V];
-        th.template decays<CARE>(R, j, a);
-        th.template step<CARE>(A, R, j, a, H);
+        const bool cut = th.template decays<CARE>(R, j, a);
+        th.template step<CARE>(A, R, j, a, cut, H);
         row_dy<CARE, Th, T, V>(A, R, th, dy, j, d);
-        m.row(a);
+        m.row(a, cut);
 #pragma unroll
         for (int v = 0; v < V; ++v) W[v] = m.add(Th::D == 1 ? 0 : v, d[v], W[v]);
         settle(W);
     }
-    return m.roots(r);
+    return m.whole(r);
 }
 
 // dg of one row from a product per channel, one channel per lane: the lanes
@@ -98,20 +98,20 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
     for (int j = 0; j < L; ++j) {
         float a[D];
         __builtin_amdgcn_sched_barrier(0);
-        th.template decays<CARE>(R, j, a);
+        const bool cut = th.template decays<CARE>(R, j, a);
 #pragma unroll
         for (int v = 0; v < V; ++v) before[j][v] = h[v];
-        th.template step<CARE>(A, R, j, a, h);
+        th.template step<CARE>(A, R, j, a, cut, h);
     }
     const bool own = V == 1 ? A.per == 1 : !SH;  // a decay for each channel
     const RowAt<T, V> dx = th.template at<T, V>(A.dx, A.lddx);
     const RowAt<TG, V> dg = th.template at<TG, V>(A.dg, A.lddg);
 #pragma unroll
     for (int j = L - 1; j >= 0; --j) {
-        const bool here = CARE == kCareRows ? j < th.rows : th.in;
+        const bool here = care_rows(CARE) ? j < th.rows : th.in;
         float a[D], u[V], p[V];
         __builtin_amdgcn_sched_barrier(0);
-        th.template decays<CARE>(R, j, a);
+        const bool cut = th.template decays<CARE>(R, j, a);
         row_dy<CARE, Th, T, V>(A, R, th, dy, j, u);
         const int q = th.template special<CARE>(j) ? R->start[th.r0 + j] : -1;
         if (q >= 0) {
@@ -135,8 +135,8 @@ __device__ __forceinline__ void write_grads(const RecurArgs& A, const RecurRows*
             for (int v = 0; v < V; ++v) {
                 const float av = a[SH ? 0 : v];
                 u[v] += w[v];
-                w[v] = CARE ? decayed(av, u[v]) : av * u[v];
-                p[v] = CARE && av == 0.f ? 0.f : w[v] * before[j][v];
+                w[v] = care_root(CARE) ? decayed(av, u[v]) : cut ? 0.f : av * u[v];
+                p[v] = cut || (care_root(CARE) && av == 0.f) ? 0.f : w[v] * before[j][v];
             }
         }
         if (CARE) settle(w);
@@ -179,11 +179,11 @@ __device__ __forceinline__ void tile_sums(const RecurArgs& A, int64_t tile, int 
 
 // Rows of a thread and waves per SIMD to compile for.  What counts is bytes
 // in flight per CU: half rows with shared decays take 16 rows per thread,
-// three workgroups of 256 threads (calls of 4 x 8192 x 4096: 191 us, 8 rows
-// 210); the others 8 rows, two workgroups of 512, also where that spills a
+// three workgroups of 256 threads (calls of 4 x 8192 x 4096: 189 us, 8 rows
+// 209); the others 8 rows, two workgroups of 512, also where that spills a
 // few registers (bf16 rows with float32 decays of their own 326 us, without
-// 406; shared float32 301, 374).  float32 rows with decays of their own would
-// spill too many (579 us, without 541).
+// 411; shared float32 297, 368).  float32 rows with decays of their own would
+// spill too many (560 us, without 540).
 template <class T, bool SH>
 constexpr int kGradRows = sizeof(T) == 2 && SH ? 16 : 8;
 template <class T, bool SH>
@@ -196,7 +196,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     using Th = RecurThread<T, TG, V, L, SH>;
     using Lay = RecurLayout<V, L>;
     __shared__ RecurRows rows;
-    __shared__ float sr[Lay::kGroups][Lay::kLanes * Th::D];
+    __shared__ RecurGroups<V, L, SH> groups;
     __shared__ float sh[Lay::kGroups][kRecurCols];
     __shared__ float sw[Lay::kGroups][kRecurCols];
     constexpr bool kSums = SH && V > 1;
@@ -218,13 +218,16 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     for (int d = 0; d < Th::D; ++d) r[d] = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = w[v] = 0.f;
+    // kCareBoth is rare: its code lies behind the others' (float32, shared
+    // decays, 8192 x 4096, both directions 169 -> 163 us)
     if (care == kCareNone) {
         if (!compose_both<kCareNone, Th, T, V>(A, R, th, dy, r, h, w)) care = kCareRoot;
+    } else if (care == kCareRows) {
+        if (!compose_both<kCareRows, Th, T, V>(A, R, th, dy, r, h, w)) care = kCareBoth;
     }
     if (care == kCareRoot) compose_both<kCareRoot, Th, T, V>(A, R, th, dy, r, h, w);
-    if (care == kCareRows) compose_both<kCareRows, Th, T, V>(A, R, th, dy, r, h, w);
-#pragma unroll
-    for (int d = 0; d < Th::D; ++d) sr[th.group][th.lane * Th::D + d] = r[d];
+    if (__builtin_expect(care == kCareBoth, 0)) compose_both<kCareBoth, Th, T, V>(A, R, th, dy, r, h, w);
+    groups.put(th.group, th.lane, care, r);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         sh[th.group][th.lane * V + v] = h[v];
@@ -232,34 +235,20 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     }
     __syncthreads();
     // one wave carries the gradient, another the state
-    const int c = lane_id();
     if (threadIdx.x < kWave) {
-        GroupsProduct all;
-        float aw = 0.f;
-#pragma unroll 8
-        for (int i = Lay::kGroups - 1; i >= 0; --i) {
-            const float a = sr[i][SH ? c / V : c];
-            aw = step_of(a, aw, sw[i][c]);
-            all.times(a);
-        }
+        const uint32_t waves = groups.rooted();
         // nothing comes back into a tile whose last row ends a sequence or has none
         const bool fresh = R && (R->last[kRecurTile - 1] != -1 || R->start[kRecurTile - 1] == -2);
         float b = 0.f;
-        if (A.tiles > 1) b = pass_state(A, back, ct, all.root(), aw, fresh, back == A.tiles - 1);
-#pragma unroll 8
-        for (int i = Lay::kGroups - 1; i >= 0; --i) {
-            const float next = step_of(sr[i][SH ? c / V : c], b, sw[i][c]);
-            sw[i][c] = b;  // gradient entering group i from the rows after it
-            b = next;
+        if (A.tiles > 1) {
+            float aw;
+            const float ar = groups.template compose<true>(waves, sw, aw);
+            b = pass_state(A, back, ct, ar, aw, fresh, back == A.tiles - 1);
         }
+        groups.template enter<true>(waves, sw, b);
     } else if (threadIdx.x < 2 * kWave) {
-        float e = tile > 0 ? A.states_in[((tile - 1) * A.cols + ct) * kRecurCols + c] : 0.f;
-#pragma unroll 8
-        for (int i = 0; i < Lay::kGroups; ++i) {
-            const float next = step_of(sr[i][SH ? c / V : c], e, sh[i][c]);
-            sh[i][c] = e;  // state entering group i
-            e = next;
-        }
+        const float e = tile > 0 ? A.states_in[((tile - 1) * A.cols + ct) * kRecurCols + lane_id()] : 0.f;
+        groups.template enter<false>(groups.rooted(), sh, e);
     }
     __syncthreads();
 #pragma unroll
@@ -270,6 +259,7 @@ __global__ __launch_bounds__((RecurLayout<V, L>::kThreads)) __attribute__((
     if (care == kCareNone) write_grads<kCareNone>(A, R, th, dy, ct, h, w, s_sum);
     else if (care == kCareRoot) write_grads<kCareRoot>(A, R, th, dy, ct, h, w, s_sum);
     else if (care == kCareRows) write_grads<kCareRows>(A, R, th, dy, ct, h, w, s_sum);
+    else if (__builtin_expect(care == kCareBoth, 0)) write_grads<kCareBoth>(A, R, th, dy, ct, h, w, s_sum);
     if (kSums && A.dg) {
         __syncthreads();
         tile_sums<TG, V, Lay::kThreads, kSumPitch>(A, tile, ct, s_sum);
