@@ -1724,12 +1724,12 @@ const char* recur_common(lx::RecurArgs& A, int64_t n, int64_t seqs, const int32_
     // before anyone else reads it.  Past the caches against through them, us:
     //   forward, then an operator that reads y, and backward, 4096 channels
     //              bf16 own decays      bf16 shared          float32 own          float32 shared
-    //    64 MiB     76/ 73   85/ 90      65/ 59   68/ 67      73/ 68   82/ 87      58/ 51   54/ 53
-    //   128 MiB    126/140  143/153     108/115  109/123     124/140  143/149      99/110   94/102
-    //   256 MiB    237/250  258/280     198/207  187/204     237/253  277/266     190/202  160/178
-    //   512 MiB    450/471  484/528     377/390  349/375     456/472  551/514     368/382  293/327
+    //    64 MiB     74/ 70   84/ 91      64/ 59   68/ 68      72/ 67   81/ 87      58/ 52   55/ 53
+    //   128 MiB    125/140  145/155     108/112  110/123     123/139  143/149     100/109   92/100
+    //   256 MiB    234/247  262/284     201/207  190/209     234/251  277/276     189/200  162/173
+    //   512 MiB    447/469  490/532     379/393  359/379     452/474  550/515     370/382  300/323
     // It would gain from 128 MiB on (with nothing else in the cache), and
-    // loses 4 to 8 % of one form, the float32 backward with own decays.
+    // loses up to 7 % of one form, the float32 backward with own decays.
     A.stream = (double)n * (double)width * (double)dtype_size(type) >= 268435456.0;
     A.tiles = tiles;
     A.cols = (int)cols;

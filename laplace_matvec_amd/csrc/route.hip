@@ -32,7 +32,7 @@
 // and is bound by memory.  Rows by expert are moved past the caches: an array
 // of them is read or written once here, in scattered pieces, and filling the
 // caches with it makes the next kernel wait for their write-back (dispatch
-// and combine of 65536 rows of 4 KB: 61 + 92 us through the caches, 58 + 55
+// and combine of 65536 rows of 4 KB: 61 + 92 us through the caches, 58 + 54
 // past them; 8192 rows followed by a product that reads them all: 30.6 us,
 // 23.2).  Sums are float32 in ascending k; a dropped slot's
 // weight and row are never used, whatever they hold.
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(256) void lx_combine(MoveArgs A)
 
 // G threads of a 256-thread workgroup per token; the dot products of KC
 // slots are carried along one pass over the row.  16384 tokens x 4 rows of
-// 2048 bf16: 107 us, 5.7 TB/s.
+// 2048 bf16: 105 us, 5.7 TB/s.
 template <int V, class T, int KC, int G>
 __global__ __launch_bounds__(256) void lx_combine_grad(MoveArgs A)
 {
