@@ -377,6 +377,113 @@ laplex_status laplex_recur_step(int64_t n, int64_t pool, const int32_t* slots, i
                                 laplex_dtype type, laplex_dtype gate_type, const void* x, int64_t ldx,
                                 const void* g, int64_t ldg, float* state, void* y, int64_t ldy, void* stream);
 
+/*
+ * ---- Experts' products and the gated matrix memory ----
+ *
+ * What stands between dispatch and combine, and the recurrence with a matrix
+ * for a state.  As above: nothing is allocated or waited for, work is ordered
+ * on `stream`, sums and states are float32, a result is rounded once when it
+ * is stored, index arrays are not checked on the host (offsets are cut to
+ * [0, n]), outputs may not overlap each other or an input, and results repeat
+ * bit for bit.
+ */
+
+/*
+ * laplex_experts -- y_r = w[e] x_r for the rows r of expert e.
+ *
+ *   n, n_experts  rows (less than 2^31) and experts (1 .. 4096); expert e has
+ *                 rows offsets[e] .. offsets[e + 1] - 1 (none if equal);
+ *                 offsets device int32[n_experts + 1], ascending, as
+ *                 laplex_route gives them.
+ *   in, out       values of a row of x and of y, 1 .. 2^24.
+ *   x             [n][in] of `type`, rows ldx apart.
+ *   w             [n_experts][out][in] of `type`, or [n_experts][in][out]
+ *                 with transpose = 1 (y_r = w[e]^T x_r); rows ldw values
+ *                 apart, experts `pitch`.
+ *   y             [n][out] of `type`; rows of no expert are set to 0.
+ *
+ * laplex_experts_backward -- gradients, dy [n][out] of `type` in:
+ *   dx            [n][in] of `type` or NULL (0 for rows of no expert).
+ *   dw            like w, of `type`, with its own pitches, or NULL: summed over
+ *                 the expert's rows; 0 for an expert without rows.
+ *   x may be NULL without dw, w without dx.
+ * A row reaches its own results alone, and its expert's dw: whatever rows of
+ * no expert hold is not used.
+ */
+laplex_status laplex_experts(int64_t n, int64_t n_experts, const int32_t* offsets, int64_t in, int64_t out,
+                             laplex_dtype type, int transpose, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                             int64_t pitch, void* y, int64_t ldy, void* stream);
+laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_t* offsets, int64_t in, int64_t out,
+                                      laplex_dtype type, int transpose, const void* x, int64_t ldx, const void* w,
+                                      int64_t ldw, int64_t pitch, const void* dy, int64_t lddy, void* dx,
+                                      int64_t lddx, void* dw, int64_t lddw, int64_t pitch_dw, void* stream);
+
+/*
+ * laplex_attend -- linear attention with decays: for each head
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,    y_t = scale S_t^T q_t
+ * along each sequence, S a matrix of dk x dv.
+ *
+ *   n, seqs, offsets  as for laplex_recur (seqs at most 2^24); rows outside
+ *             all sequences get y = 0.
+ *   heads     of g, y and the states, 1 .. 4096; q, k and v have query_heads,
+ *             key_heads and value_heads, each dividing heads: head h uses
+ *             h / (heads / query_heads) of q, and so on.
+ *   dk, dv    1 .. 1024.
+ *   q, k, v, y  of `type`, rows of [query_heads][dk], [key_heads][dk],
+ *             [value_heads][dv] and [heads][dv], ld values apart.
+ *   g         [n][heads] of `gate_type` (`type` or LAPLEX_F32), logarithms of
+ *             the decays.  Where exp(g) is 0 in float32 the state is
+ *             forgotten, whatever it held.  Decays may be above 1 as long as
+ *             their products along any stretch of a sequence stay in
+ *             float32's range.
+ *   h0, final float32 [seqs][heads][dk][dv], states before the first and after
+ *             the last rows, or NULL (h0: 0).
+ *   states    float32[laplex_attend_states(n, heads, dk, dv)] or NULL: what
+ *             laplex_attend_backward needs of this pass (16-byte aligned).
+ *   ws        device scratch of laplex_attend_workspace(..., 0) bytes, 16-byte
+ *             aligned.
+ * Float32 and float16 rows are multiplied in float32.  With bfloat16 rows,
+ * scores and states are rounded to bfloat16 (states: to two of them) where
+ * they enter a product; the states themselves stay float32.
+ * A row that holds inf or NaN reaches its own and later rows of its heads and
+ * sequence, up to a decay of 0; they may get NaN where inf is due.  In the
+ * backward pass it may reach every gradient of its heads and sequence.
+ *
+ * laplex_attend_backward -- gradients: dy (y's layout) and dfinal (or NULL)
+ *   in; dq, dk_out, dv_out (q's, k's and v's layout, summed over the heads
+ *   that share one), dg (g's, 0 where the decay is 0) and dh0 out, each or
+ *   NULL.  q, k, v, g, h0 as in the forward pass, states from it (NULL if it
+ *   has no values).  Scratch: laplex_attend_workspace(..., 1).
+ *
+ * laplex_attend_step -- one token for each of n requests, states updated in
+ *   place: state float32 [pool][heads][dk][dv]; slots as for
+ *   laplex_recur_step (a slot outside [0, pool) has no state: y = 0).
+ *
+ * The two size functions return -1 for sizes out of range.
+ */
+int64_t laplex_attend_states(int64_t n, int64_t heads, int64_t dk, int64_t dv);
+int64_t laplex_attend_workspace(int64_t n, int64_t heads, int64_t query_heads, int64_t key_heads,
+                                int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type, int backward);
+laplex_status laplex_attend(int64_t n, int64_t seqs, const int32_t* offsets, int64_t heads, int64_t query_heads,
+                            int64_t key_heads, int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type,
+                            laplex_dtype gate_type, float scale, const void* q, int64_t ldq, const void* k,
+                            int64_t ldk, const void* v, int64_t ldv, const void* g, int64_t ldg, const float* h0,
+                            void* y, int64_t ldy, float* final, float* states, void* ws, int64_t ws_bytes,
+                            void* stream);
+laplex_status laplex_attend_backward(int64_t n, int64_t seqs, const int32_t* offsets, int64_t heads,
+                                     int64_t query_heads, int64_t key_heads, int64_t value_heads, int64_t dk,
+                                     int64_t dv, laplex_dtype type, laplex_dtype gate_type, float scale,
+                                     const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                     int64_t ldv, const void* g, int64_t ldg, const float* h0, const float* states,
+                                     const void* dy, int64_t lddy, const float* dfinal, void* dq, int64_t lddq,
+                                     void* dk_out, int64_t lddk, void* dv_out, int64_t lddv, void* dg, int64_t lddg,
+                                     float* dh0, void* ws, int64_t ws_bytes, void* stream);
+laplex_status laplex_attend_step(int64_t n, int64_t pool, const int32_t* slots, int64_t heads, int64_t query_heads,
+                                 int64_t key_heads, int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type,
+                                 laplex_dtype gate_type, float scale, const void* q, int64_t ldq, const void* k,
+                                 int64_t ldk, const void* v, int64_t ldv, const void* g, int64_t ldg, float* state,
+                                 void* y, int64_t ldy, void* stream);
+
 /* Kernel timing: while enabled, every kernel the library launches is
  * bracketed by HIP events on its stream (timing-only events, recorded
  * without a system-scope fence, so they order no memory for the host).

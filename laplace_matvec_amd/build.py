@@ -25,7 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 ARCH = os.environ.get("LAPLEX_ARCH", "gfx950")
 
 LIB_SOURCES = ["api.hip", "sort.hip", "small.hip", "scan.hip", "general.hip", "gram.hip", "grad.hip", "merge.hip",
-               "route.hip", "recur.hip", "recur_grad.hip"]
+               "route.hip", "recur.hip", "recur_grad.hip", "experts.hip", "attend.hip", "attend_grad.hip"]
 INPUT_SOURCES = ["inputs_philox.hip", "calib_copy.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

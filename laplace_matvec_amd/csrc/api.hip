@@ -2048,3 +2048,387 @@ laplex_status laplex_recur_step(int64_t n, int64_t pool, const int32_t* slots, i
 }
 
 }  // extern "C"
+
+// ---- experts' products and the gated matrix memory ----
+
+namespace {
+
+// Experts' matrices [experts][rows][cols]: everything between the first and
+// the last value.
+Rows matrices(const void* p, int64_t experts, int64_t rows, int64_t cols, int64_t ld, int64_t pitch, size_t size)
+{
+    const int64_t span = (experts - 1) * pitch + (rows - 1) * ld + cols;
+    return Rows{p, 1, span, span, size};
+}
+
+bool matrices_ok(const void* p, int64_t experts, int64_t rows, int64_t cols, int64_t ld, int64_t pitch, size_t size)
+{
+    return ld >= cols && ld <= (int64_t)1 << 40 && pitch >= 0 && pitch <= (int64_t)1 << 46 &&
+           (double)experts * (double)pitch + (double)rows * (double)ld < 7.0e13 && (uintptr_t)p % size == 0;
+}
+
+bool experts_sizes_ok(int64_t n, int64_t n_experts, int64_t in, int64_t out, laplex_dtype type, int transpose)
+{
+    return n >= 0 && n <= 0x7FFFFFFF && n_experts >= 1 && n_experts <= lx::kRouteMaxExperts && in >= 1 &&
+           in <= (int64_t)1 << 24 && out >= 1 && out <= (int64_t)1 << 24 && dtype_ok(type) &&
+           (transpose == 0 || transpose == 1);
+}
+
+constexpr const char* kBadExperts =
+    "bad sizes, type or transpose: 0 <= n < 2^31, n_experts in [1, 4096], in and out in [1, 2^24]";
+
+// Sizes of a pass of the matrix memory, the same for both directions.
+constexpr int kAttendMaxHeads = 4096, kAttendMaxDim = 1024;
+bool attend_sizes(lx::AttendArgs& A, int64_t n, int64_t heads, int64_t hq, int64_t hk, int64_t hv, int64_t dk,
+                  int64_t dv, laplex_dtype type)
+{
+    if (n < 0 || n > 0x7FFFFFFF || heads < 1 || heads > kAttendMaxHeads || dk < 1 || dk > kAttendMaxDim || dv < 1 ||
+        dv > kAttendMaxDim || !dtype_ok(type))
+        return false;
+    for (int64_t h : {hq, hk, hv})
+        if (h < 1 || h > heads || heads % h) return false;
+    A.n = n;
+    A.heads = (int)heads;
+    A.hq = (int)hq;
+    A.hk = (int)hk;
+    A.hv = (int)hv;
+    A.dk = (int)dk;
+    A.dv = (int)dv;
+    A.block_k = dk <= 64 ? 64 : 128;
+    A.nkb = (int)((dk + A.block_k - 1) / A.block_k);
+    A.nvb = (int)((dv + 63) / 64);
+    A.dkp = A.nkb * A.block_k;
+    A.dvp = A.nvb * 64;
+    A.grad_block_k = type == LAPLEX_BF16 ? A.block_k : 64;
+    A.loop = hq == hk ? (int)(heads / hq) : 1;
+    A.segment = lx::attend_segment(n, heads * A.nkb * A.nvb);
+    // states of all slots between chunks stay below 2^46 bytes
+    return (double)(n / lx::kAttendChunk + 1) * (double)heads * A.dkp * A.dvp < 1.7e13;
+}
+
+int64_t attend_slots(const lx::AttendArgs& A) { return A.n > A.segment ? A.n / A.segment : 0; }
+size_t attend_slot_values(const lx::AttendArgs& A) { return (size_t)A.heads * A.dkp * A.dvp; }
+
+// Lays out the scratch from `base` on; its size.
+size_t attend_carve(lx::AttendArgs& A, char* base, bool backward, bool own_states)
+{
+    size_t off = 0;
+    auto take = [&](size_t values) {
+        float* p = values ? (float*)(base + off) : nullptr;
+        off += align256(values * 4);
+        return p;
+    };
+    const size_t slots = (size_t)attend_slots(A), one = attend_slot_values(A), n = (size_t)A.n;
+    A.seg_decays = take(slots * A.heads);
+    if (!backward) {
+        if (own_states) A.seg_states = take(slots * one);
+        A.part = take(A.nkb > 1 ? (size_t)A.nkb * n * A.heads * A.dv : 0);
+        return off;
+    }
+    A.seg_grads = take(slots * one);
+    A.chunk_states = take(n / lx::kAttendChunk * one);
+    A.chunk_grads = take(n / lx::kAttendChunk * one);
+    const size_t nkb = (size_t)(A.dkp / A.grad_block_k);
+    const size_t rq = A.heads / A.hq / A.loop, rk = A.heads / A.hk / A.loop, rv = A.heads / A.hv * nkb;
+    A.part_q = take(rq > 1 ? rq * n * A.hq * A.dk : 0);
+    A.part_k = take(rk > 1 ? rk * n * A.hk * A.dk : 0);
+    A.part_v = take(rv > 1 ? rv * n * A.hv * A.dv : 0);
+    A.part_g = take(nkb > 1 ? nkb * n * A.heads : 0);
+    return off;
+}
+
+constexpr const char* kBadAttend =
+    "bad sizes or type: 0 <= n < 2^31, heads in [1, 4096] and a multiple of each array's, dk and dv in [1, 1024]";
+
+const char* attend_common(lx::AttendArgs& A, int64_t n, int64_t seqs, const int32_t* offsets, int64_t heads,
+                          int64_t hq, int64_t hk, int64_t hv, int64_t dk, int64_t dv, laplex_dtype type,
+                          laplex_dtype gate_type, float scale, const void* q, int64_t ldq, const void* k, int64_t ldk,
+                          const void* v, int64_t ldv, const void* g, int64_t ldg, const float* h0)
+{
+    if (!attend_sizes(A, n, heads, hq, hk, hv, dk, dv, type)) return kBadAttend;
+    if (seqs < 1 || seqs > (int64_t)1 << 24) return "seqs must be in [1, 2^24]";
+    if (!offsets && n % seqs) return "without offsets n must be a multiple of seqs";
+    if (gate_type != type && gate_type != LAPLEX_F32) return "bad gate_type";
+    if (n > 0 && (!q || !k || !v || !g)) return "q, k, v or g is NULL";
+    if ((double)(n / lx::kAttendChunk + seqs + 2) * (double)heads * A.nkb * 2 * A.nvb > 1.3e11)
+        return "too many sequences for so many heads";
+    A.seqs = seqs;
+    A.seq_len = offsets ? 0 : n / seqs;
+    A.offsets = offsets;
+    A.scale = scale;
+    A.q = q;
+    A.k = k;
+    A.v = v;
+    A.g = g;
+    A.ldq = ldq;
+    A.ldk = ldk;
+    A.ldv = ldv;
+    A.ldg = ldg;
+    A.h0 = h0;
+    return nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+laplex_status laplex_experts(int64_t n, int64_t n_experts, const int32_t* offsets, int64_t in, int64_t out,
+                             laplex_dtype type, int transpose, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                             int64_t pitch, void* y, int64_t ldy, void* stream)
+{
+    if (!experts_sizes_ok(n, n_experts, in, out, type, transpose)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, kBadExperts);
+    if (n == 0) return LAPLEX_OK;
+    if (!offsets || !x || !w || !y) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "offsets, x, w or y is NULL");
+    const size_t e = dtype_size(type);
+    const int64_t rw = transpose ? in : out, cw = transpose ? out : in;
+    if (!matrices_ok(w, n_experts, rw, cw, ldw, pitch, e))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad pitch or alignment of w");
+    const Rows o = {y, n, ldy, out, e};
+    const Rows ins[3] = {{x, n, ldx, in, e}, matrices(w, n_experts, rw, cw, ldw, pitch, e),
+                         {offsets, 1, n_experts + 1, n_experts + 1, 4}};
+    if (!rows_ok(o) || !rows_ok(ins[0]) || !rows_ok(ins[2]))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(&o, 1, ins, 3)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::ExpertsArgs A;
+    A.n = n;
+    A.experts = n_experts;
+    A.offsets = offsets;
+    A.in = in;
+    A.out = out;
+    A.transpose = transpose;
+    A.x = x;
+    A.ldx = ldx;
+    A.w = w;
+    A.ldw = ldw;
+    A.pitch_w = pitch;
+    A.y = y;
+    A.ldy = ldy;
+    LX_TRY(lx::experts_launch(A, (int)type, (hipStream_t)stream), "experts");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_t* offsets, int64_t in, int64_t out,
+                                      laplex_dtype type, int transpose, const void* x, int64_t ldx, const void* w,
+                                      int64_t ldw, int64_t pitch, const void* dy, int64_t lddy, void* dx,
+                                      int64_t lddx, void* dw, int64_t lddw, int64_t pitch_dw, void* stream)
+{
+    if (!experts_sizes_ok(n, n_experts, in, out, type, transpose)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, kBadExperts);
+    if (!dx && !dw) return LAPLEX_OK;
+    if (!offsets || (n > 0 && (!dy || (dw && !x) || (dx && !w))))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "offsets, dy, or what dx or dw needs is NULL");
+    const size_t e = dtype_size(type);
+    const int64_t rw = transpose ? in : out, cw = transpose ? out : in;
+    if ((dx && n > 0 && !matrices_ok(w, n_experts, rw, cw, ldw, pitch, e)) ||
+        (dw && (!matrices_ok(dw, n_experts, rw, cw, lddw, pitch_dw, e) ||
+                (n_experts > 1 && pitch_dw < (rw - 1) * lddw + cw))))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad pitch or alignment of w or dw");
+    const Rows none = {nullptr, 0, 0, 0, 1};
+    const Rows outs[2] = {n > 0 ? Rows{dx, n, lddx, in, e} : none,
+                          dw ? matrices(dw, n_experts, rw, cw, lddw, pitch_dw, e) : none};
+    const Rows ins[4] = {n > 0 ? Rows{dy, n, lddy, out, e} : none, dw && n > 0 ? Rows{x, n, ldx, in, e} : none,
+                         dx && n > 0 ? matrices(w, n_experts, rw, cw, ldw, pitch, e) : none,
+                         {offsets, 1, n_experts + 1, n_experts + 1, 4}};
+    if (!rows_ok(outs[0]) || !rows_ok(ins[0]) || !rows_ok(ins[1]) || !rows_ok(ins[3]))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 2, ins, 4)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::ExpertsArgs A;
+    A.n = n;
+    A.experts = n_experts;
+    A.offsets = offsets;
+    if (dx && n > 0) {  // the product with the other side's matrix
+        A.in = out;
+        A.out = in;
+        A.transpose = !transpose;
+        A.x = dy;
+        A.ldx = lddy;
+        A.w = w;
+        A.ldw = ldw;
+        A.pitch_w = pitch;
+        A.y = dx;
+        A.ldy = lddx;
+        LX_TRY(lx::experts_launch(A, (int)type, (hipStream_t)stream), "experts backward");
+    }
+    if (dw) {  // its rows from dy, its columns from x; the other way round for transposed ones
+        A.in = transpose ? out : in;
+        A.out = transpose ? in : out;
+        A.x = transpose ? dy : x;
+        A.ldx = transpose ? lddy : ldx;
+        A.y = const_cast<void*>(transpose ? x : dy);
+        A.ldy = transpose ? ldx : lddy;
+        A.dw = dw;
+        A.ldw = lddw;
+        A.pitch_w = pitch_dw;
+        LX_TRY(lx::experts_grad_launch(A, (int)type, (hipStream_t)stream), "experts backward");
+    }
+    return LAPLEX_OK;
+}
+
+int64_t laplex_attend_states(int64_t n, int64_t heads, int64_t dk, int64_t dv)
+{
+    lx::AttendArgs A;
+    if (!attend_sizes(A, n, heads, heads, heads, heads, dk, dv, LAPLEX_F32)) return -1;
+    return attend_slots(A) * (int64_t)attend_slot_values(A);
+}
+
+int64_t laplex_attend_workspace(int64_t n, int64_t heads, int64_t query_heads, int64_t key_heads,
+                                int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type, int backward)
+{
+    lx::AttendArgs A;
+    if ((backward != 0 && backward != 1) ||
+        !attend_sizes(A, n, heads, query_heads, key_heads, value_heads, dk, dv, type))
+        return -1;
+    return (int64_t)attend_carve(A, nullptr, backward, true);
+}
+
+laplex_status laplex_attend(int64_t n, int64_t seqs, const int32_t* offsets, int64_t heads, int64_t query_heads,
+                            int64_t key_heads, int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type,
+                            laplex_dtype gate_type, float scale, const void* q, int64_t ldq, const void* k,
+                            int64_t ldk, const void* v, int64_t ldv, const void* g, int64_t ldg, const float* h0,
+                            void* y, int64_t ldy, float* final, float* states, void* ws, int64_t ws_bytes,
+                            void* stream)
+{
+    lx::AttendArgs A;
+    if (const char* m = attend_common(A, n, seqs, offsets, heads, query_heads, key_heads, value_heads, dk, dv, type,
+                                      gate_type, scale, q, ldq, k, ldk, v, ldv, g, ldg, h0))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    if (n > 0 && !y) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "y is NULL");
+    const int64_t need =
+        laplex_attend_workspace(n, heads, query_heads, key_heads, value_heads, dk, dv, type, 0);
+    if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < need))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_attend_workspace");
+    const size_t e = dtype_size(type), eg = dtype_size(gate_type);
+    const int64_t ns = laplex_attend_states(n, heads, dk, dv), one = heads * dk * dv;
+    if (ns > 0 && (uintptr_t)states % 16) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "states must be 16-byte aligned");
+    const Rows outs[4] = {{y, n, ldy, heads * dv, e}, {final, seqs, one, one, 4},
+                          {ns > 0 ? states : nullptr, 1, ns, ns, 4}, {need > 0 ? ws : nullptr, 1, need, need, 1}};
+    const Rows ins[6] = {{q, n, ldq, query_heads * dk, e}, {k, n, ldk, key_heads * dk, e},
+                         {v, n, ldv, value_heads * dv, e}, {g, n, ldg, heads, eg}, {h0, seqs, one, one, 4},
+                         {offsets, 1, seqs + 1, seqs + 1, 4}};
+    for (const Rows& r : {outs[0], outs[1], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]})
+        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 4, ins, 6)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    attend_carve(A, (char*)ws, false, true);
+    if (states) A.seg_states = states;
+    A.y = y;
+    A.ldy = ldy;
+    A.final = final;
+    LX_TRY(lx::attend_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, (hipStream_t)stream), "attend");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_attend_backward(int64_t n, int64_t seqs, const int32_t* offsets, int64_t heads,
+                                     int64_t query_heads, int64_t key_heads, int64_t value_heads, int64_t dk,
+                                     int64_t dv, laplex_dtype type, laplex_dtype gate_type, float scale,
+                                     const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                     int64_t ldv, const void* g, int64_t ldg, const float* h0, const float* states,
+                                     const void* dy, int64_t lddy, const float* dfinal, void* dq, int64_t lddq,
+                                     void* dk_out, int64_t lddk, void* dv_out, int64_t lddv, void* dg, int64_t lddg,
+                                     float* dh0, void* ws, int64_t ws_bytes, void* stream)
+{
+    lx::AttendArgs A;
+    if (const char* m = attend_common(A, n, seqs, offsets, heads, query_heads, key_heads, value_heads, dk, dv, type,
+                                      gate_type, scale, q, ldq, k, ldk, v, ldv, g, ldg, h0))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    if (!dq && !dk_out && !dv_out && !dg && !dh0) return LAPLEX_OK;
+    if (n > 0 && !dy) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "dy is NULL");
+    const int64_t ns = laplex_attend_states(n, heads, dk, dv), one = heads * dk * dv;
+    if (ns > 0 && (!states || (uintptr_t)states % 16))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "states is NULL or misaligned");
+    const int64_t need =
+        laplex_attend_workspace(n, heads, query_heads, key_heads, value_heads, dk, dv, type, 1);
+    if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < need))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_attend_workspace");
+    const size_t e = dtype_size(type), eg = dtype_size(gate_type);
+    const Rows outs[6] = {{dq, n, lddq, query_heads * dk, e}, {dk_out, n, lddk, key_heads * dk, e},
+                          {dv_out, n, lddv, value_heads * dv, e}, {dg, n, lddg, heads, eg}, {dh0, seqs, one, one, 4},
+                          {need > 0 ? ws : nullptr, 1, need, need, 1}};
+    const Rows ins[9] = {{q, n, ldq, query_heads * dk, e}, {k, n, ldk, key_heads * dk, e},
+                         {v, n, ldv, value_heads * dv, e}, {g, n, ldg, heads, eg}, {dy, n, lddy, heads * dv, e},
+                         {h0, seqs, one, one, 4}, {dfinal, seqs, one, one, 4},
+                         {ns > 0 ? states : nullptr, 1, ns, ns, 4}, {offsets, 1, seqs + 1, seqs + 1, 4}};
+    for (int i = 0; i < 5; ++i)
+        if (!rows_ok(outs[i])) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    for (const Rows& r : ins)
+        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 6, ins, 9)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    attend_carve(A, (char*)ws, true, false);
+    A.seg_states = const_cast<float*>(states);  // read only
+    A.dy = dy;
+    A.lddy = lddy;
+    A.dfinal = dfinal;
+    A.dq = dq;
+    A.dkey = dk_out;
+    A.dval = dv_out;
+    A.dg = dg;
+    A.lddq = lddq;
+    A.lddk = lddk;
+    A.lddv = lddv;
+    A.lddg = lddg;
+    A.dh0 = dh0;
+    LX_TRY(lx::attend_grad_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, (hipStream_t)stream),
+           "attend backward");
+    return LAPLEX_OK;
+}
+
+laplex_status laplex_attend_step(int64_t n, int64_t pool, const int32_t* slots, int64_t heads, int64_t query_heads,
+                                 int64_t key_heads, int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type,
+                                 laplex_dtype gate_type, float scale, const void* q, int64_t ldq, const void* k,
+                                 int64_t ldk, const void* v, int64_t ldv, const void* g, int64_t ldg, float* state,
+                                 void* y, int64_t ldy, void* stream)
+{
+    lx::AttendArgs sizes;  // a step's own limits: those of a pass of no rows
+    if (!attend_sizes(sizes, 0, heads, query_heads, key_heads, value_heads, dk, dv, type) || n < 0 ||
+        n > 0x7FFFFFFF || pool < 0 || pool > 0x7FFFFFFF)
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, kBadAttend);
+    if (gate_type != type && gate_type != LAPLEX_F32) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "bad gate_type");
+    if (!slots && n > pool) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "without slots n must be at most pool");
+    if (n * heads > (int64_t)1 << 37) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "n * heads must be at most 2^37");
+    if (n == 0) return LAPLEX_OK;
+    if (!q || !k || !v || !g || !y || (pool > 0 && !state))
+        return fail(LAPLEX_ERR_INVALID_ARGUMENT, "q, k, v, g, state or y is NULL");
+    const size_t e = dtype_size(type), eg = dtype_size(gate_type);
+    const int64_t one = heads * dk * dv;
+    const Rows outs[2] = {{y, n, ldy, heads * dv, e}, {state, pool, one, one, 4}};
+    const Rows ins[5] = {{q, n, ldq, query_heads * dk, e}, {k, n, ldk, key_heads * dk, e},
+                         {v, n, ldv, value_heads * dv, e}, {g, n, ldg, heads, eg}, {slots, 1, n, n, 4}};
+    for (const Rows& r : {outs[0], outs[1], ins[0], ins[1], ins[2], ins[3], ins[4]})
+        if (!rows_ok(r)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "a bad row pitch or alignment");
+    if (const char* m = check_outputs(outs, 2, ins, 5)) return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
+    const laplex_status st = check_device();
+    if (st != LAPLEX_OK) return st;
+    lx::AttendStepArgs A;
+    A.n = n;
+    A.pool = pool;
+    A.heads = (int)heads;
+    A.hq = (int)query_heads;
+    A.hk = (int)key_heads;
+    A.hv = (int)value_heads;
+    A.dk = (int)dk;
+    A.dv = (int)dv;
+    A.scale = scale;
+    A.q = q;
+    A.k = k;
+    A.v = v;
+    A.g = g;
+    A.ldq = ldq;
+    A.ldk = ldk;
+    A.ldv = ldv;
+    A.ldg = ldg;
+    A.slots = slots;
+    A.state = state;
+    A.y = y;
+    A.ldy = ldy;
+    LX_TRY(lx::attend_step_launch(A, (int)type, gate_type == LAPLEX_F32 ? 0 : (int)type, (hipStream_t)stream),
+           "attend step");
+    return LAPLEX_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,528 @@
+// Gated matrix memory: linear attention with a decay per head and row (gfx950).
+//
+//     S_t = e^{g_t} S_{t-1} + k_t v_t^T      (dk x dv, float32)
+//     y_t = scale S_t^T q_t
+//
+// In chunks of 64 rows, with G_i the sum of g over the chunk's rows up to i,
+//     y_i   = scale (e^{G_i} S^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j)
+//     S'    = e^{G_63} S + sum_j e^{G_63 - G_j} k_j v_j^T
+// so all but the decays is products of matrices.  A workgroup takes one head's
+// block of up to 128 x 64 of the state along a segment of a sequence, the
+// state in registers in float32.  Segments of one sequence are independent
+// but for their first states:
+//     sweep kEnd    each segment's last state from a first one of 0
+//     scan          the segments' first states, one after the other
+//     sweep kOut    the outputs
+// A segment is as short as it takes to fill the card (attend_segment); with
+// one segment per sequence the first two are left out.
+#include "lx_attend.h"
+
+namespace lx {
+
+namespace {
+
+enum SweepMode { kEnd, kOut, kStore };
+
+// REV runs the segments backwards with queries and output gradients in place
+// of keys and values: the gradient of the states.
+template <class T, class TG, int DK, int MODE, bool REV>
+__global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
+{
+    typedef typename Compute<T>::E E;
+    constexpr int N = MODE == kOut ? Compute<T>::kTerms : 1;
+    constexpr int NU = Compute<T>::kTerms;  // terms of a row times its decay
+    constexpr int PK = DK + kPad<E>, PV = kDV + kPad<E>;
+    constexpr int TA = DK / 64;  // 16-row tiles of the state per wave
+    __shared__ alignas(16) E s_k[kC * PK];
+    __shared__ alignas(16) E s_v[kC * PV];
+    __shared__ alignas(16) E s_s[MODE == kOut ? N * kDV * PK : 1];
+    __shared__ alignas(16) Decays s_d;
+    __shared__ alignas(16) float s_f[kC];
+    __shared__ int s_odd[4];
+    __shared__ unsigned long long s_rows[kDV];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g4 = 4 * (lane >> 4), l16 = lane & 15;
+    const int64_t id = group_id<kAttendThreads>();
+    const int parts = A.heads * A.nkb * A.nvb;
+    const int64_t unit = id / parts;
+    const int part = (int)(id - unit * parts);
+    const int h = part / (A.nkb * A.nvb), kb = part / A.nvb % A.nkb, vb = part % A.nvb;
+    const Ragged R{A.offsets, A.seqs, A.n, A.seq_len};
+    if (unit >= R.units(A.segment)) return;
+    const RaggedTile t = R.find(unit, A.segment);
+    if (t.rows <= 0) return;
+    const int k0 = kb * DK, v0 = vb * kDV;
+    const int kcols = A.dk - k0, vcols = A.dv - v0;  // how many are there
+    if (t.group < 0) {
+        if (MODE != kOut) return;
+        for (int i = threadIdx.x; i < t.rows * kDV; i += kAttendThreads) {
+            const int64_t row = t.row + i / kDV;
+            const int c = i % kDV;
+            if (c >= vcols) continue;
+            if (A.part)
+                A.part[(kb * A.n + row) * ((int64_t)A.heads * A.dv) + h * A.dv + v0 + c] = 0.f;
+            else
+                ((T*)A.y)[row * A.ldy + h * A.dv + v0 + c] = (T)0.f;
+        }
+        return;
+    }
+    const bool is_first = t.index == 0, is_last = t.row + t.rows == t.end;
+    if (MODE == kEnd && (REV ? is_first : is_last)) return;
+
+    // the state: rows dk 16 (wave TA + a) + g4 + r, columns 16 b + l16
+    f32x4 acc[TA][4];
+    // slot i of a sequence: the state between its segments i and i + 1 (the
+    // gradient there); before and past the sequence they are the edges
+    const int64_t slot = t.first / A.segment + t.index + (MODE == kEnd ? 0 : -1) + (REV ? (MODE == kEnd ? -1 : 1) : 0);
+    float* seg_state = A.seg_states + ((slot * A.heads + h) * A.dkp + k0) * A.dvp + v0;
+    const float* edge = REV ? A.dfinal : A.h0;  // [seqs][heads][dk][dv]
+    const bool at_edge = REV ? is_last : is_first;
+    const int64_t edge_at = ((t.group * A.heads + h) * A.dk + k0) * (int64_t)A.dv + v0;
+#pragma unroll
+    for (int a = 0; a < TA; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * (wave * TA + a) + g4 + r, col = 16 * b + l16;
+                float x = 0.f;
+                if (MODE != kEnd) {
+                    if (!at_edge)
+                        x = seg_state[(int64_t)row * A.dvp + col];
+                    else if (edge && row < kcols && col < vcols)
+                        x = edge[edge_at + (int64_t)row * A.dv + col];
+                }
+                acc[a][b][r] = x;
+            }
+
+    const int64_t ldk = REV ? A.ldq : A.ldk, ldv = REV ? A.lddy : A.ldv;
+    const T* kp = (const T*)(REV ? A.q : A.k) + h / (A.heads / (REV ? A.hq : A.hk)) * A.dk + k0;
+    const T* vp = (const T*)(REV ? A.dy : A.v) + (REV ? h : h / (A.heads / A.hv)) * A.dv + v0;
+    const T* qp = (const T*)A.q + h / (A.heads / A.hq) * A.dk + k0;
+    const TG* gp = (const TG*)A.g + h;
+
+    const int chunks = (t.rows + kC - 1) / kC;
+    RowTile<T, DK> tk;
+    RowTile<T, kDV> tv;
+    Pack<T, 8> tq[DK / 32];
+    float tg = 0.f;
+    auto fetch = [&](int ci) {
+        const int c = REV ? chunks - 1 - ci : ci;
+        const int64_t row = t.row + (int64_t)c * kC;
+        const int rows = t.rows - c * kC < kC ? t.rows - c * kC : kC;
+        tk.load(kp + row * ldk, ldk, rows, kcols);
+        tv.load(vp + row * ldv, ldv, rows, vcols);
+        if (MODE == kOut) {
+            const int i = 16 * wave + l16;
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk)
+                tq[kk] = load8(qp + (row + i) * A.ldq + 32 * kk + 2 * g4, i < rows ? kcols - 32 * kk - 2 * g4 : 0);
+        }
+        if (wave == 0) tg = lane < rows ? (float)gp[(row + lane) * A.ldg] : 0.f;
+    };
+    fetch(0);
+    float decay = 1.f;  // of the segment
+    for (int ci = 0; ci < chunks; ++ci) {
+        const int c = REV ? chunks - 1 - ci : ci;
+        const int64_t row = t.row + (int64_t)c * kC;
+        const int rows = t.rows - c * kC < kC ? t.rows - c * kC : kC;
+        if (wave == 0) {
+            s_d.make(tg);
+            s_f[lane] = REV ? s_d.into[lane] * A.scale : s_d.out[lane];
+        }
+        tk.put(s_k);
+        tv.put(s_v);
+        {
+            const bool odd = __any(tv.template odd<E>());
+            if (lane == 0) s_odd[wave] = odd;
+        }
+        Frag<E> fq[DK / 32];
+        if (MODE == kOut) {
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk) fq[kk] = to_frag<E>(tq[kk]);
+            typedef E V4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int a = 0; a < TA; ++a)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    V4 w[N];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        E e[N];
+                        split<E, N>(acc[a][b][r], e);
+#pragma unroll
+                        for (int m = 0; m < N; ++m) w[m][r] = e[m];
+                    }
+#pragma unroll
+                    for (int m = 0; m < N; ++m)
+                        *reinterpret_cast<V4*>(&s_s[(m * kDV + 16 * b + l16) * PK + 16 * (wave * TA + a) + g4]) = w[m];
+                }
+        }
+        __syncthreads();
+        // 0 times inf or NaN is not 0: rows that do not see such a value of v
+        // must not multiply it.  It becomes 0 and a bit of its column, and what
+        // does see it gets NaN.
+        const bool odd = (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0;
+        if (odd) {
+            if (threadIdx.x < kDV) s_rows[threadIdx.x] = 0;
+            __syncthreads();
+            for (int i = threadIdx.x; i < kC * kDV; i += kAttendThreads) {
+                E* p = s_v + i / kDV * PV + i % kDV;
+                if (!finite(*p)) {
+                    atomicOr(&s_rows[i % kDV], 1ull << (i / kDV));
+                    *p = (E)0.f;
+                }
+            }
+            __syncthreads();
+        }
+        if (ci + 1 < chunks) fetch(ci + 1);
+        const float whole = s_d.into[kC - 1];
+        if (MODE == kEnd) decay *= whole;
+        if (MODE == kStore) {
+            // slots between chunks, likewise
+            const int64_t between = t.first / kC + (row - t.first) / kC - (REV ? 0 : 1);
+            float* to = (REV ? A.chunk_grads : A.chunk_states) + ((between * A.heads + h) * A.dkp + k0) * A.dvp + v0;
+            if (REV ? row + kC < t.end : row > t.first) {
+#pragma unroll
+                for (int a = 0; a < TA; ++a)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            to[(int64_t)(16 * (wave * TA + a) + g4 + r) * A.dvp + 16 * b + l16] = acc[a][b][r];
+            }
+        }
+        if (MODE == kOut) {
+            const int i = 16 * wave + l16;
+            const float hi_i = s_d.hi[i], lo_i = s_d.lo[i];
+            const int last_i = s_d.last[i];
+            Frag<E> fp[2];
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) {
+                f32x4 p = {};
+                if (jt <= wave) {
+#pragma unroll
+                    for (int kk = 0; kk < DK / 32; ++kk)
+                        p = mma(frag_along(s_k + (16 * jt + l16) * PK + 32 * kk + 2 * g4), fq[kk], p);
+                    const f32x4 hi = *reinterpret_cast<const f32x4*>(&s_d.hi[16 * jt + g4]);
+                    const f32x4 lo = *reinterpret_cast<const f32x4*>(&s_d.lo[16 * jt + g4]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = 16 * jt + g4 + r;
+                        const float x = p[r] * A.scale * s_d.between(hi_i, lo_i, hi[r], lo[r]);
+                        p[r] = j <= i && j >= last_i ? x : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) fp[jt >> 1].v[4 * (jt & 1) + r] = (E)p[r];
+            }
+            const f32x4 into = *reinterpret_cast<const f32x4*>(&s_d.into[16 * wave + g4]);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                f32x4 o = {};
+#pragma unroll
+                for (int kk = 0; kk < DK / 32; ++kk)
+#pragma unroll
+                    for (int m = 0; m < N; ++m)
+                        o = mma(fq[kk], frag_along(s_s + (m * kDV + 16 * b + l16) * PK + 32 * kk + 2 * g4), o);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] = into[r] == 0.f ? 0.f : o[r] * (into[r] * A.scale);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (2 * s <= wave) o = mma(fp[s], frag_across(s_v + 32 * s * PV + 16 * b, PV), o);
+                const int col = 16 * b + l16;
+                if (odd) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int at = 16 * wave + g4 + r, from = s_d.last[at];
+                        const unsigned long long seen = (2ull << at) - (1ull << (from < 0 ? 0 : from));
+                        if (s_rows[col] & seen) o[r] = __builtin_nanf("");
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = 16 * wave + g4 + r;
+                    if (at < rows && col < vcols) {
+                        if (A.part)
+                            A.part[(kb * A.n + row + at) * ((int64_t)A.heads * A.dv) + h * A.dv + v0 + col] = o[r];
+                        else
+                            ((T*)A.y)[(row + at) * A.ldy + h * A.dv + v0 + col] = (T)o[r];
+                    }
+                }
+            }
+        }
+        // S' = whole S + sum_j f_j k_j v_j^T
+#pragma unroll
+        for (int a = 0; a < TA; ++a)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[a][b][r] = whole == 0.f ? 0.f : whole * acc[a][b][r];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            Frag<E> fv[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) fv[b] = frag_across(s_v + 32 * s * PV + 16 * b, PV);
+            const f32x4 f0 = *reinterpret_cast<const f32x4*>(&s_f[32 * s + g4]);
+            const f32x4 f1 = *reinterpret_cast<const f32x4*>(&s_f[32 * s + 16 + g4]);
+#pragma unroll
+            for (int a = 0; a < TA; ++a) {
+                const Frag<E> fk = frag_across(s_k + 32 * s * PK + 16 * (wave * TA + a), PK);
+                Frag<E> fs[NU];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = i < 4 ? f0[i] : f1[i - 4];
+                    E e[NU];
+                    split<E, NU>(f == 0.f ? 0.f : f * (float)fk.v[i], e);
+#pragma unroll
+                    for (int m = 0; m < NU; ++m) fs[m].v[i] = e[m];
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int m = 0; m < NU; ++m) acc[a][b] = mma(fs[m], fv[b], acc[a][b]);
+            }
+        }
+        if (odd) {
+            const int from = s_d.last[kC - 1];
+            const unsigned long long seen = REV ? s_d.sees_before() : 0ull - (1ull << (from < 0 ? 0 : from));
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (s_rows[16 * b + l16] & seen)
+#pragma unroll
+                    for (int a = 0; a < TA; ++a) acc[a][b] = f32x4{} + __builtin_nanf("");
+        }
+        __syncthreads();
+    }
+    if (MODE == kEnd && threadIdx.x == 0 && kb == 0 && vb == 0) A.seg_decays[slot * A.heads + h] = decay;
+    float* end = MODE == kOut ? A.final : A.dh0;
+    const bool write_edge = MODE != kEnd && end && (REV ? is_first : MODE == kOut && is_last);
+    if (MODE == kEnd || write_edge) {
+#pragma unroll
+        for (int a = 0; a < TA; ++a)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int rr = 16 * (wave * TA + a) + g4 + r, col = 16 * b + l16;
+                    if (MODE == kEnd)
+                        seg_state[(int64_t)rr * A.dvp + col] = acc[a][b][r];
+                    else if (rr < kcols && col < vcols)
+                        end[edge_at + (int64_t)rr * A.dv + col] = acc[a][b][r];
+                }
+    }
+}
+
+// States between the segments of a sequence (their gradients if REV), in
+// place of what each segment alone makes of a state of 0.
+template <bool REV>
+__global__ __launch_bounds__(256) void lx_attend_scan(AttendArgs A)
+{
+    const int64_t block = (int64_t)A.dkp * A.dvp;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // of [heads][dkp][dvp]
+    if (i >= A.heads * block) return;
+    const int h = (int)(i / block), row = (int)(i % block / A.dvp), col = (int)(i % A.dvp);
+    const Ragged R{A.offsets, A.seqs, A.n, A.seq_len};
+    const float* edge = REV ? A.dfinal : A.h0;
+    for (int64_t q = blockIdx.y; q < A.seqs; q += gridDim.y) {
+        const int64_t first = R.bound(q + 1), end = R.bound(q + 2);
+        if (end - first <= A.segment) continue;
+        const int64_t count = (end - first + A.segment - 1) / A.segment - 1;
+        float s = 0.f;
+        if (edge && row < A.dk && col < A.dv) s = edge[((q * A.heads + h) * A.dk + row) * (int64_t)A.dv + col];
+        for (int64_t c = 0; c < count; ++c) {
+            const int64_t slot = first / A.segment + (REV ? count - 1 - c : c);
+            float* p = A.seg_states + slot * A.heads * block + i;
+            const float decay = A.seg_decays[slot * A.heads + h];
+            s = decay == 0.f ? *p : decay * s + *p;
+            *p = s;
+        }
+    }
+}
+
+// States of sequences without rows stay.
+__global__ __launch_bounds__(256) void lx_attend_empty(AttendArgs A, const float* from, float* to)
+{
+    const Ragged R{A.offsets, A.seqs, A.n, A.seq_len};
+    const int64_t size = (int64_t)A.heads * A.dk * A.dv;
+    for (int64_t q = blockIdx.x; q < A.seqs; q += gridDim.x) {
+        if (R.bound(q + 2) > R.bound(q + 1)) continue;
+        for (int64_t i = threadIdx.x; i < size; i += 256) to[q * size + i] = from ? from[q * size + i] : 0.f;
+    }
+}
+
+// to[n][hx * d] = sum over `planes` of part[plane][n][hx * d], in their order.
+template <class T>
+__global__ __launch_bounds__(256) void lx_attend_sum(const float* part, int planes, int64_t n, int64_t width, T* to,
+                                                     int64_t ld)
+{
+    const int64_t size = n * width;
+    for (int64_t i = group_id<256>() * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * gridDim.y * 256) {
+        float s = part[i];
+        for (int p = 1; p < planes; ++p) s += part[p * size + i];
+        to[i / width * ld + i % width] = (T)s;
+    }
+}
+
+// One token for each request.  A thread has V neighbouring columns of every
+// 256 / (columns / V) -th row of a head's state.
+template <class T, class TG, int V>
+__global__ __launch_bounds__(256) void lx_attend_step(AttendStepArgs A)
+{
+    __shared__ float s_sum[256 * V];
+    const int64_t id = group_id<256>();
+    const int64_t b = id / A.heads;
+    if (b >= A.n) return;
+    const int h = (int)(id - b * A.heads);
+    const int64_t slot = A.slots ? (int64_t)A.slots[b] : b;
+    T* y = (T*)A.y + b * A.ldy + (int64_t)h * A.dv;
+    const T* v = (const T*)A.v + b * A.ldv + h / (A.heads / A.hv) * A.dv;
+    const bool has = slot >= 0 && slot < A.pool;
+    const T* q = (const T*)A.q + b * A.ldq + h / (A.heads / A.hq) * A.dk;
+    const T* k = (const T*)A.k + b * A.ldk + h / (A.heads / A.hk) * A.dk;
+    const float g = has ? (float)((const TG*)A.g)[b * A.ldg + h] : 0.f;
+    const float a = g < -103.972f ? 0.f : expf(g);
+    float* state = A.state + (has ? slot * A.heads + h : 0) * (int64_t)A.dk * A.dv;
+    // column groups of the row, at most 64 at a time
+    const int groups = (A.dv + V - 1) / V;
+    const int wide = groups < 64 ? groups : 64;
+    const int lines = 256 / wide;
+    const int line = threadIdx.x / wide, at = threadIdx.x % wide;
+    for (int c0 = 0; c0 < groups; c0 += wide) {
+        const int col = (c0 + at) * V;
+        const bool here = line < lines && col < A.dv;
+        float sum[V] = {};
+        if (here && has) {
+            float vv[V];
+            load_vec<V>(v + col, vv);
+            for (int r = line; r < A.dk; r += lines) {
+                float* p = state + (int64_t)r * A.dv + col;
+                float s[V];
+                load_vec<V>(p, s);
+                const float kr = (float)k[r], qr = (float)q[r];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[i] = (a == 0.f ? 0.f : a * s[i]) + kr * vv[i];
+                    sum[i] += qr * s[i];
+                }
+                store_vec<V>(p, s);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_sum[threadIdx.x * V + i] = sum[i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < wide * V; c += 256) {
+            float s = 0.f;
+            for (int l = 0; l < lines; ++l) s += s_sum[l * wide * V + c];
+            if (c0 * V + c < A.dv) y[c0 * V + c] = (T)(s * A.scale);
+        }
+    }
+}
+
+template <class T, class TG, int DK, int MODE, bool REV>
+hipError_t sweep_go(const AttendArgs& a, const char* label, hipStream_t s)
+{
+    const int64_t groups = Ragged{a.offsets, a.seqs, a.n, a.seq_len}.units(a.segment) * a.heads * a.nkb * a.nvb;
+    LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, MODE, REV><<<grid_of<kAttendThreads>(groups), kAttendThreads, 0, s>>>(a)));
+    return hipSuccess;
+}
+
+template <bool REV>
+hipError_t scan_go(const AttendArgs& a, hipStream_t s)
+{
+    const int64_t groups = ((int64_t)a.heads * a.dkp * a.dvp + 255) / 256;
+    const unsigned seqs = (unsigned)(a.seqs < 1024 ? a.seqs : 1024);
+    LX_LAUNCH("attend_scan", s, (lx_attend_scan<REV><<<dim3((unsigned)groups, seqs), 256, 0, s>>>(a)));
+    return hipSuccess;
+}
+
+hipError_t empty_go(const AttendArgs& a, const float* from, float* to, hipStream_t s)
+{
+    if (!to || (!a.offsets && a.n > 0)) return hipSuccess;
+    const unsigned seqs = (unsigned)(a.seqs < 4096 ? a.seqs : 4096);
+    LX_LAUNCH("attend_empty", s, (lx_attend_empty<<<seqs, 256, 0, s>>>(a, from, to)));
+    return hipSuccess;
+}
+
+template <class T, class TG, int DK>
+hipError_t forward_dk(const AttendArgs& a, hipStream_t s)
+{
+    hipError_t e = empty_go(a, a.h0, a.final, s);
+    if (e != hipSuccess || a.n == 0) return e;
+    if (attend_may_split(a)) {
+        if ((e = sweep_go<T, TG, DK, kEnd, false>(a, "attend_end", s)) != hipSuccess) return e;
+        if ((e = scan_go<false>(a, s)) != hipSuccess) return e;
+    }
+    if ((e = sweep_go<T, TG, DK, kOut, false>(a, "attend_out", s)) != hipSuccess) return e;
+    if (a.part) return attend_sum_launch(a.part, a.nkb, a.n, (int64_t)a.heads * a.dv, a.y, a.ldy, (int)(sizeof(T) == 4 ? 0 : __is_same(T, bf16_t) ? 1 : 2), s);
+    return hipSuccess;
+}
+
+template <class T, class TG, int DK>
+hipError_t states_dk(const AttendArgs& a, hipStream_t s)
+{
+    hipError_t e = empty_go(a, a.dfinal, a.dh0, s);
+    if (e != hipSuccess || a.n == 0) return e;
+    if ((e = sweep_go<T, TG, DK, kStore, false>(a, "attend_states", s)) != hipSuccess) return e;
+    AttendArgs b = a;
+    b.seg_states = a.seg_grads;
+    if (attend_may_split(a)) {
+        if ((e = sweep_go<T, TG, DK, kEnd, true>(b, "attend_end_back", s)) != hipSuccess) return e;
+        if ((e = scan_go<true>(b, s)) != hipSuccess) return e;
+    }
+    return sweep_go<T, TG, DK, kStore, true>(b, "attend_states_back", s);
+}
+
+template <class T, class TG>
+hipError_t step_go(const AttendStepArgs& a, hipStream_t s)
+{
+    const int64_t groups = a.n * a.heads;
+    if (a.dv % 4 == 0)
+        LX_LAUNCH("attend_step", s, (lx_attend_step<T, TG, 4><<<grid_of<256>(groups), 256, 0, s>>>(a)));
+    else
+        LX_LAUNCH("attend_step", s, (lx_attend_step<T, TG, 1><<<grid_of<256>(groups), 256, 0, s>>>(a)));
+    return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t attend_sum_launch(const float* part, int planes, int64_t n, int64_t width, void* to, int64_t ld, int dtype,
+                             hipStream_t s)
+{
+    const int64_t want = (n * width + 255) / 256;
+    const dim3 grid((unsigned)(want < 65536 ? want : 65536));
+    switch (dtype) {
+        case 0: LX_LAUNCH("attend_sum", s, (lx_attend_sum<float><<<grid, 256, 0, s>>>(part, planes, n, width, (float*)to, ld))); break;
+        case 1: LX_LAUNCH("attend_sum", s, (lx_attend_sum<bf16_t><<<grid, 256, 0, s>>>(part, planes, n, width, (bf16_t*)to, ld))); break;
+        case 2: LX_LAUNCH("attend_sum", s, (lx_attend_sum<f16_t><<<grid, 256, 0, s>>>(part, planes, n, width, (f16_t*)to, ld))); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipSuccess;
+}
+
+#define LX_BY_DK(call, a, T, TG) return a.block_k == 64 ? call<T, TG, 64>(a, s) : call<T, TG, 128>(a, s)
+#define LX_BY_TYPE(call, a)                                                                  \
+    switch (dtype) {                                                                         \
+        case 0: LX_BY_DK(call, a, float, float);                                             \
+        case 1: if (gtype) LX_BY_DK(call, a, bf16_t, bf16_t); else LX_BY_DK(call, a, bf16_t, float); \
+        case 2: if (gtype) LX_BY_DK(call, a, f16_t, f16_t); else LX_BY_DK(call, a, f16_t, float);    \
+        default: return hipErrorInvalidValue;                                                \
+    }
+
+hipError_t attend_launch(const AttendArgs& a, int dtype, int gtype, hipStream_t s) { LX_BY_TYPE(forward_dk, a) }
+
+hipError_t attend_states_launch(const AttendArgs& a, int dtype, int gtype, hipStream_t s) { LX_BY_TYPE(states_dk, a) }
+
+hipError_t attend_step_launch(const AttendStepArgs& a, int dtype, int gtype, hipStream_t s)
+{
+    switch (dtype) {
+        case 0: return step_go<float, float>(a, s);
+        case 1: return gtype ? step_go<bf16_t, bf16_t>(a, s) : step_go<bf16_t, float>(a, s);
+        case 2: return gtype ? step_go<f16_t, f16_t>(a, s) : step_go<f16_t, float>(a, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace lx

@@ -1,0 +1,158 @@
+// Shared parts of the gated matrix memory's kernels (gfx950).
+#pragma once
+#include "lx_device.h"
+#include "lx_internal.h"
+#include "lx_mma.h"
+#include "lx_ragged.h"
+
+namespace lx {
+
+constexpr int kAttendThreads = 256;
+constexpr int kC = kAttendChunk;  // rows of a chunk: one per lane
+constexpr int kDV = 64;           // columns of a state block in a sweep
+
+// What products are made in for storage type T: bfloat16 rows as they are,
+// other types as float32 (float16's range is too small for states and
+// scores).  Values that are made here (states, rows times decays) go into
+// bfloat16 products in two terms, the value's rounding and the rounding of
+// what is left: 17 bits, so that float32 results keep 5 digits.
+template <class T>
+struct Compute { typedef float E; static constexpr int kTerms = 1; };
+template <>
+struct Compute<bf16_t> { typedef bf16_t E; static constexpr int kTerms = 2; };
+
+// Values of padding at the end of an LDS row of E: 16 bytes.
+template <class E>
+constexpr int kPad = 16 / (int)sizeof(E);
+
+// 8 neighbours from p on, of which `count` are there (0 past them).
+template <class T>
+__device__ __forceinline__ Pack<T, 8> load8(const T* p, int64_t count)
+{
+    Pack<T, 8> r;
+    if (count >= 8) {
+        if constexpr (sizeof(T) == 2) {
+            r = load_pack<8>(p);
+        } else {
+            const Pack<T, 4> a = load_pack<4>(p), b = load_pack<4>(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r.v[i] = a.v[i];
+                r.v[4 + i] = b.v[i];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.v[i] = i < count ? p[i] : (T)0.f;
+    }
+    return r;
+}
+
+template <class E, class T>
+__device__ __forceinline__ Frag<E> to_frag(const Pack<T, 8>& p)
+{
+    Frag<E> f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] = (E)p.v[i];
+    return f;
+}
+
+template <class E, class T>
+__device__ __forceinline__ void put8(E* s, const Pack<T, 8>& p)
+{
+    *reinterpret_cast<typename Frag<E>::V*>(s) = to_frag<E>(p).v;
+}
+
+__device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u; }
+__device__ __forceinline__ bool finite(bf16_t x) { return (__builtin_bit_cast(uint16_t, x) & 0x7F80u) != 0x7F80u; }
+
+// A tile of kC rows x W columns on its way from memory to LDS.
+template <class T, int W>
+struct RowTile {
+    static constexpr int kVecs = kC * W / 8 / kAttendThreads;
+    Pack<T, 8> r[kVecs];
+
+    // p: first row and column; rows and cols: how many are there
+    __device__ __forceinline__ void load(const T* p, int64_t ld, int rows, int cols)
+    {
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int i = (int)threadIdx.x + j * kAttendThreads;
+            const int row = i / (W / 8), col = i % (W / 8) * 8;
+            r[j] = load8(p + row * ld + col, row < rows ? cols - col : 0);
+        }
+    }
+    // whether any of the values is inf or NaN as an E
+    template <class E>
+    __device__ __forceinline__ bool odd() const
+    {
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) any |= !finite((E)r[j].v[i]);
+        return any;
+    }
+    template <class E>
+    __device__ __forceinline__ void put(E* s) const
+    {
+        constexpr int kPitch = W + kPad<E>;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int i = (int)threadIdx.x + j * kAttendThreads;
+            put8(s + i / (W / 8) * kPitch + i % (W / 8) * 8, r[j]);
+        }
+    }
+};
+
+// Decays of a chunk, worked out by one wave with a row per lane.  Sums of the
+// logarithms are float64, handed on in two floats, so that a difference of two
+// is as good after thousands of strong decays as at the start.  A decay that
+// is 0 in float32 cuts: rows before it are gone for the rows from it on.
+struct Decays {
+    float hi[kC], lo[kC];  // sums of log2 of the decays up to each row, cuts left out
+    float into[kC];        // what a row sees of the state before the chunk
+    float out[kC];         // what the state after the chunk holds of a row
+    int last[kC];          // the last cut up to each row, -1 for none
+
+    __device__ __forceinline__ void make(float g)
+    {
+        const int lane = threadIdx.x & 63;
+        const bool cut = g < -103.972f;  // e^g < 2^-150
+        const uint64_t cuts = __ballot(cut);
+        double sum = cut ? 0.0 : (double)g * 1.4426950408889634074;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const double below = __shfl_up(sum, d);
+            if (lane >= d) sum += below;
+        }
+        const double total = __shfl(sum, 63);
+        const uint64_t mine = cuts & ((2ull << lane) - 1);
+        hi[lane] = (float)sum;
+        lo[lane] = (float)(sum - (double)(float)sum);
+        last[lane] = mine ? 63 - __builtin_clzll(mine) : -1;
+        into[lane] = mine ? 0.f : __builtin_amdgcn_exp2f((float)sum);
+        // a cut after this row takes it away; its own does not
+        out[lane] = (cuts >> lane) > 1 ? 0.f : __builtin_amdgcn_exp2f((float)(total - sum));
+    }
+    // rows that see the state before the chunk, a bit each
+    __device__ __forceinline__ unsigned long long sees_before() const
+    {
+        return __ballot(last[threadIdx.x & 63] < 0);
+    }
+    // exp of the decays after row j up to row i >= j
+    __device__ __forceinline__ float between(float hi_i, float lo_i, float hi_j, float lo_j) const
+    {
+        return __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j));
+    }
+};
+
+// x in terms: term 0 the rounding of x, term 1 of what is left.
+template <class E, int N>
+__device__ __forceinline__ void split(float x, E (&t)[N])
+{
+    t[0] = (E)x;
+    if constexpr (N == 2) t[1] = (E)(x - (float)t[0]);
+}
+
+}  // namespace lx

@@ -473,4 +473,81 @@ struct RecurStepArgs {
 };
 hipError_t recur_step_launch(const RecurStepArgs& a, int dtype, int gtype, hipStream_t s);
 
+// ---- experts' products (experts.hip) ----
+struct ExpertsArgs {
+    int64_t n = 0, experts = 0;
+    const int32_t* offsets = nullptr;  // [experts + 1]
+    int64_t in = 0, out = 0;
+    int transpose = 0;                 // w is [experts][in][out]
+    const void* x = nullptr;           // [n][in]
+    int64_t ldx = 0;
+    const void* w = nullptr;           // [experts][out][in]
+    int64_t ldw = 0, pitch_w = 0;      // values between its rows and between experts
+    void* y = nullptr;                 // [n][out]; the gradient reads it
+    int64_t ldy = 0;
+    void* dw = nullptr;                // [experts][out][in], ldw and pitch_w
+    int64_t row_tiles = 0, col_tiles = 0;  // set at launch
+};
+hipError_t experts_launch(const ExpertsArgs& a, int dtype, hipStream_t s);
+hipError_t experts_grad_launch(const ExpertsArgs& a, int dtype, hipStream_t s);
+
+// ---- gated matrix memory (attend.hip, attend_grad.hip) ----
+constexpr int kAttendChunk = 64;  // rows of a chunk
+struct AttendArgs {
+    int64_t n = 0, seqs = 0, seq_len = 0;
+    const int32_t* offsets = nullptr;   // [seqs + 1], or null: equal sequences
+    int heads = 0, hq = 0, hk = 0, hv = 0, dk = 0, dv = 0;
+    int block_k = 0, nkb = 0, nvb = 0;  // blocks of the state: block_k x 64
+    int dkp = 0, dvp = 0;               // the state's sizes in whole blocks
+    int segment = 0;                    // rows
+    float scale = 1.f;
+    const void *q = nullptr, *k = nullptr, *v = nullptr, *g = nullptr;
+    int64_t ldq = 0, ldk = 0, ldv = 0, ldg = 0;
+    const float* h0 = nullptr;          // [seqs][heads][dk][dv]
+    void* y = nullptr;
+    int64_t ldy = 0;
+    float* part = nullptr;              // [nkb][n][heads * dv], where nkb > 1
+    float* final = nullptr;             // [seqs][heads][dk][dv]
+    float* seg_states = nullptr;        // [n / segment][heads][dkp][dvp]: slot first / segment + i of a sequence
+    float* seg_decays = nullptr;        // [n / segment][heads]
+    // backward
+    const void* dy = nullptr;
+    int64_t lddy = 0;
+    const float* dfinal = nullptr;
+    float* dh0 = nullptr;
+    float* seg_grads = nullptr;
+    float *chunk_states = nullptr, *chunk_grads = nullptr;  // [n / kAttendChunk][heads][dkp][dvp], likewise
+    int grad_block_k = 0, loop = 1;     // heads that share query and key heads
+    void *dq = nullptr, *dkey = nullptr, *dval = nullptr, *dg = nullptr;
+    int64_t lddq = 0, lddk = 0, lddv = 0, lddg = 0;
+    float *part_q = nullptr, *part_k = nullptr, *part_v = nullptr, *part_g = nullptr;
+};
+// Rows of a segment: about 1024 workgroups, `parts` of them beside each other.
+inline int attend_segment(int64_t n, int64_t parts)
+{
+    const double rows = (double)n * (double)parts / 1024.0;
+    const int64_t r = rows < 512.0 ? 512 : rows > 1073741824.0 ? 1073741824 : (int64_t)rows;
+    return (int)((r + kAttendChunk - 1) / kAttendChunk * kAttendChunk);
+}
+// Whether a sequence may have more than one segment.
+inline bool attend_may_split(const AttendArgs& a) { return (a.offsets ? a.n : a.seq_len) > a.segment; }
+hipError_t attend_launch(const AttendArgs& a, int dtype, int gtype, hipStream_t s);
+hipError_t attend_states_launch(const AttendArgs& a, int dtype, int gtype, hipStream_t s);
+hipError_t attend_grad_launch(const AttendArgs& a, int dtype, int gtype, hipStream_t s);
+// to [n][width] = sum over planes of part [planes][n][width]
+hipError_t attend_sum_launch(const float* part, int planes, int64_t n, int64_t width, void* to, int64_t ld, int dtype,
+                             hipStream_t s);
+struct AttendStepArgs {
+    int64_t n = 0, pool = 0;
+    int heads = 0, hq = 0, hk = 0, hv = 0, dk = 0, dv = 0;
+    float scale = 1.f;
+    const void *q = nullptr, *k = nullptr, *v = nullptr, *g = nullptr;
+    int64_t ldq = 0, ldk = 0, ldv = 0, ldg = 0;
+    const int32_t* slots = nullptr;
+    float* state = nullptr;             // [pool][heads][dk][dv]
+    void* y = nullptr;
+    int64_t ldy = 0;
+};
+hipError_t attend_step_launch(const AttendStepArgs& a, int dtype, int gtype, hipStream_t s);
+
 }  // namespace lx

@@ -57,6 +57,17 @@ SIGNATURES = {
     "laplex_recur_backward": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _VP,
                                      _I64, _VP, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP]),
     "laplex_recur_step": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP]),
+    "laplex_experts": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _I64, _VP, _I64, _VP]),
+    "laplex_experts_backward": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _I64, _VP, _I64,
+                                       _VP, _I64, _VP, _I64, _I64, _VP]),
+    "laplex_attend_states": (_I64, [_I64] * 4),
+    "laplex_attend_workspace": (_I64, [_I64] * 7 + [_I32, _I32]),
+    "laplex_attend": (_I32, [_I64, _I64, _VP] + [_I64] * 6 + [_I32, _I32, ctypes.c_float] + [_VP, _I64] * 4
+                      + [_VP, _VP, _I64, _VP, _VP, _VP, _I64, _VP]),
+    "laplex_attend_backward": (_I32, [_I64, _I64, _VP] + [_I64] * 6 + [_I32, _I32, ctypes.c_float] + [_VP, _I64] * 4
+                               + [_VP, _VP, _VP, _I64, _VP] + [_VP, _I64] * 4 + [_VP, _VP, _I64, _VP]),
+    "laplex_attend_step": (_I32, [_I64, _I64, _VP] + [_I64] * 6 + [_I32, _I32, ctypes.c_float] + [_VP, _I64] * 4
+                           + [_VP, _VP, _I64, _VP]),
     "laplex_profile_enable": (_I32, [_I32]),
     "laplex_profile_only": (_I32, [ctypes.c_char_p]),
     "laplex_profile_reset": (_I32, []),
@@ -609,6 +620,204 @@ def laplex_recur_step(x, g, state, slots=None, stream=None):
         _check(load().laplex_recur_step(n, state.shape[0], _at(slots), width, heads, _DTYPES[x.dtype],
                                         _DTYPES[g.dtype], _at(x), ldx, _at(g), ldg, _at(state), _at(y), width, s),
                "laplex_recur_step")
+    return y
+
+
+# ---- experts' products and the gated matrix memory -----------------------
+
+def _device_offsets(offsets, device):
+    """int32 offsets of groups, checked; the number of groups."""
+    if not (isinstance(offsets, torch.Tensor) and offsets.dim() == 1 and offsets.numel() > 1):
+        raise TypeError("offsets must be an int32 tensor [groups + 1]")
+    _flat(offsets, "offsets", torch.int32, offsets.shape, device)
+    return offsets.numel() - 1
+
+
+def _matrices(w, name, dtype, device, experts):
+    """(rows, columns, values between rows, values between experts) of w [experts, rows, columns]."""
+    if not (isinstance(w, torch.Tensor) and w.dtype is dtype and w.device == device):
+        raise TypeError(f"{name} must be a {dtype} tensor on {device}")
+    if w.dim() != 3 or w.shape[0] != experts or 0 in w.shape:
+        raise ValueError(f"{name} must have shape [{experts}][rows][columns]")
+    _, rows, cols = w.shape
+    pitch, ld, one = w.stride()
+    ld = ld if rows > 1 else cols
+    if (one != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have unit stride along its last dimension and rows apart")
+    return rows, cols, ld, pitch if experts > 1 else rows * ld
+
+
+def _experts_parts(x, w, offsets, transpose):
+    n, width, ldx = _rows(x, "x")
+    if x.dim() != 2 or width < 1:
+        raise ValueError("x must have shape [rows][width]")
+    experts = _device_offsets(offsets, x.device)
+    rows, cols, ldw, pitch = _matrices(w, "w", x.dtype, x.device, experts)
+    if (rows if transpose else cols) != width:
+        raise ValueError("w must be [experts][out][in], or [experts][in][out] with transpose, for rows of x of `in`")
+    return n, experts, width, cols if transpose else rows, ldx, ldw, pitch
+
+
+def laplex_experts(x, w, offsets, transpose: bool = False, stream=None):
+    """y_r = w[e] x_r for the rows r of each expert e: x [rows, in] sorted by
+    expert, offsets int32 [experts + 1] (those of a Route), w [experts, out,
+    in], or [experts, in, out] with transpose.  Rows of no expert give 0."""
+    n, experts, width, out, ldx, ldw, pitch = _experts_parts(x, w, offsets, transpose)
+    s, ctx = _launch(stream, x.device, x, w, offsets)
+    with ctx:
+        y = x.new_empty((n, out))
+        _check(load().laplex_experts(n, experts, _at(offsets), width, out, _DTYPES[x.dtype], int(transpose), _at(x),
+                                     ldx, _at(w), ldw, pitch, _at(y), out, s), "laplex_experts")
+    return y
+
+
+def laplex_experts_backward(x, w, dy, offsets, transpose: bool = False, want=("dx", "dw"), stream=None) -> dict:
+    """Gradients of laplex_experts from dy (y's shape and type): the
+    requested tensors among dx and dw (w's shape and type)."""
+    n, experts, width, out, ldx, ldw, pitch = _experts_parts(x, w, offsets, transpose)
+    _, _, lddy = _rows(dy, "dy", x.dtype, (n, out))
+    if dy.device != x.device:
+        raise ValueError(f"dy must be on {x.device}")
+    s, ctx = _launch(stream, x.device, x, w, dy, offsets)
+    grads = {}
+    with ctx:
+        if "dx" in want:
+            grads["dx"] = _new_like(x)
+        if "dw" in want:
+            grads["dw"] = w.new_empty(w.shape)
+        rows, cols = w.shape[1:]
+        _check(load().laplex_experts_backward(n, experts, _at(offsets), width, out, _DTYPES[x.dtype], int(transpose),
+                                              _at(x), ldx, _at(w), ldw, pitch, _at(dy), lddy, _at(grads.get("dx")),
+                                              width, _at(grads.get("dw")), cols, rows * cols, s),
+               "laplex_experts_backward")
+    return grads
+
+
+def _head_rows(t, name, dtype, lead, device):
+    """(heads, width of a head, values between rows) of a tensor [..., heads,
+    width] whose rows are packed and evenly spaced."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype):
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    sizes = t.shape
+    if len(sizes) != len(lead) + 2 or sizes[:-2] != lead or sizes[-1] < 1 or sizes[-2] < 1:
+        raise ValueError(f"{name} must have shape {tuple(lead)} + [heads][width]")
+    heads, width = sizes[-2:]
+    if t.is_contiguous():
+        return heads, width, heads * width
+    if (width > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != width):
+        raise ValueError(f"{name}'s heads must lie next to each other, their values too")
+    rows, _, ld = _rows(t.select(-2, 0), name)
+    if rows > 1 and ld < heads * width:
+        raise ValueError(f"{name} must have rows apart")
+    return heads, width, max(ld, heads * width)
+
+
+def _attend_parts(q, k, v, g, offsets, h0):
+    """Sizes and pitches of a matrix memory's inputs, checked."""
+    n, heads, ldg = _rows(g, "g")
+    lead = g.shape[:-1]
+    if len(lead) not in (1, 2) or (len(lead) == 2 and offsets is not None) or heads < 1:
+        raise ValueError("g must be [rows, heads], or [seqs, rows, heads] without offsets")
+    dev = g.device
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise TypeError("q must be a float32, bfloat16 or float16 CUDA tensor")
+    if g.dtype not in (q.dtype, torch.float32):
+        raise TypeError("g must have q's type or be float32")
+    hq, dk, ldq = _head_rows(q, "q", q.dtype, lead, dev)
+    hk, dk2, ldk = _head_rows(k, "k", q.dtype, lead, dev)
+    hv, dv, ldv = _head_rows(v, "v", q.dtype, lead, dev)
+    if dk2 != dk:
+        raise ValueError("q's and k's heads must have one width")
+    if heads % hq or heads % hk or heads % hv:
+        raise ValueError("the heads of q, k and v must each divide those of g")
+    seqs = _device_offsets(offsets, dev) if offsets is not None else lead[0] if len(lead) == 2 else 1
+    _flat(h0, "h0", torch.float32, (seqs, heads, dk, dv), dev)
+    return n, seqs, (heads, hq, hk, hv, dk, dv), (ldq, ldk, ldv, ldg)
+
+
+def laplex_attend(q, k, v, g, offsets=None, h0=None, scale: float = 1.0, final: bool = False, keep: bool = False,
+                  stream=None) -> Recurrence:
+    """Linear attention with decays: S_t = exp(g_t) S_{t-1} + k_t v_t^T, y_t =
+    scale S_t^T q_t for each head along each sequence.
+
+    g [rows, heads] (one sequence, or those of int32 offsets [seqs + 1]) or
+    [seqs, rows, heads], of q's type or float32; q, k [..., some heads, dk], v
+    [..., some heads, dv], their heads dividing g's; h0 float32 [seqs, heads,
+    dk, dv] or None.  y is [..., heads, dv].  final: also return the last
+    states; keep: also return what laplex_attend_backward needs."""
+    n, seqs, sizes, (ldq, ldk, ldv, ldg) = _attend_parts(q, k, v, g, offsets, h0)
+    heads, dk, dv = sizes[0], sizes[4], sizes[5]
+    lib, dev, kind = load(), q.device, _DTYPES[q.dtype]
+    need = _size(lib.laplex_attend_workspace(n, *sizes, kind, 0), "laplex_attend")
+    s, ctx = _launch(stream, dev, q, k, v, g, offsets, h0)
+    with ctx:
+        y = q.new_empty((*g.shape, dv))
+        hf = torch.empty((seqs, heads, dk, dv), dtype=torch.float32, device=dev) if final else None
+        states = torch.empty(lib.laplex_attend_states(n, heads, dk, dv), dtype=torch.float32, device=dev) if keep else None
+        ws = _scratch(need, dev)
+        _check(lib.laplex_attend(n, seqs, _at(offsets), *sizes, kind, _DTYPES[g.dtype], scale, _at(q), ldq, _at(k),
+                                 ldk, _at(v), ldv, _at(g), ldg, _at(h0), _at(y), heads * dv, _at(hf), _at(states),
+                                 _at(ws), need, s), "laplex_attend")
+    return Recurrence(y, hf, states)
+
+
+def laplex_attend_backward(q, k, v, g, dy, states, offsets=None, h0=None, scale: float = 1.0, dfinal=None,
+                           want=("dq", "dk", "dv", "dg", "dh0"), stream=None) -> dict:
+    """Gradients of laplex_attend from dy (y's shape and type) and dfinal
+    (float32 [seqs, heads, dk, dv] or None); the other inputs as in the
+    forward pass, states from it (keep=True).  Returns the requested tensors
+    among dq, dk, dv, dg and dh0."""
+    n, seqs, sizes, (ldq, ldk, ldv, ldg) = _attend_parts(q, k, v, g, offsets, h0)
+    heads, hq, hk, hv, dk, dv = sizes
+    dev, kind = q.device, _DTYPES[q.dtype]
+    hy, wy, lddy = _head_rows(dy, "dy", q.dtype, g.shape[:-1], dev)
+    if (hy, wy) != (heads, dv):
+        raise ValueError(f"dy must have shape {(*g.shape, dv)}")
+    lib = load()
+    need = _size(lib.laplex_attend_workspace(n, *sizes, kind, 1), "laplex_attend_backward")
+    if not isinstance(states, torch.Tensor):
+        raise TypeError("states must be those of laplex_attend(keep=True)")
+    _flat(states, "states", torch.float32, (lib.laplex_attend_states(n, heads, dk, dv),), dev)
+    _flat(dfinal, "dfinal", torch.float32, (seqs, heads, dk, dv), dev)
+    s, ctx = _launch(stream, dev, q, k, v, g, dy, states, offsets, h0, dfinal)
+    out = {}
+    with ctx:
+        for name, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g)):
+            if name in want:
+                out[name] = _new_like(like)
+        if "dh0" in want:
+            out["dh0"] = torch.empty((seqs, heads, dk, dv), dtype=torch.float32, device=dev)
+        ws = _scratch(need, dev)
+        _check(lib.laplex_attend_backward(n, seqs, _at(offsets), *sizes, kind, _DTYPES[g.dtype], scale, _at(q), ldq,
+                                          _at(k), ldk, _at(v), ldv, _at(g), ldg, _at(h0), _at(states), _at(dy), lddy,
+                                          _at(dfinal), _at(out.get("dq")), hq * dk, _at(out.get("dk")), hk * dk,
+                                          _at(out.get("dv")), hv * dv, _at(out.get("dg")), heads,
+                                          _at(out.get("dh0")), _at(ws), need, s), "laplex_attend_backward")
+    return out
+
+
+def laplex_attend_step(q, k, v, g, state, slots=None, scale: float = 1.0, stream=None):
+    """One token for each request, in place on state float32 [pool, heads, dk,
+    dv]: S = exp(g_i) S + k_i v_i^T for S = state[slots[i]]; returns y [n,
+    heads, dv] = scale S^T q_i.  slots int32 [n] (None: request i has state i);
+    a slot outside the pool has no state and gives 0."""
+    if not isinstance(g, torch.Tensor) or g.dim() != 2:
+        raise TypeError("g must be a CUDA tensor [n, heads]")
+    n, _, sizes, (ldq, ldk, ldv, ldg) = _attend_parts(q, k, v, g, None, None)
+    heads, dk, dv = sizes[0], sizes[4], sizes[5]
+    dev = q.device
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise TypeError("state must be a float32 tensor [pool][heads][dk][dv]")
+    _flat(state, "state", torch.float32, (state.shape[0], heads, dk, dv), dev)
+    _flat(slots, "slots", torch.int32, (n,), dev)
+    s, ctx = _launch(stream, dev, q, k, v, g, state, slots)
+    with ctx:
+        y = q.new_empty((n, heads, dv))
+        _check(load().laplex_attend_step(n, state.shape[0], _at(slots), *sizes, _DTYPES[q.dtype], _DTYPES[g.dtype],
+                                         scale, _at(q), ldq, _at(k), ldk, _at(v), ldv, _at(g), ldg, _at(state),
+                                         _at(y), heads * dv, s), "laplex_attend_step")
     return y
 
 

@@ -1,0 +1,206 @@
+"""Experts' products against float64, at the sizes and layouts where they can go wrong."""
+import pytest
+import torch
+
+import more_tokens_ref as ref
+from laplace_matvec_amd import laplex as lx
+from tokens_ref import assert_within
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def make(gpu, dtype, counts, inner, outer, transpose, before=0, past=0, seed=0):
+    """x, w, dy and offsets (a list): counts rows for each expert, with rows of no expert around them."""
+    gen = torch.Generator().manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=gen).to(dtype).to(gpu)  # noqa: E731
+    offsets = [before]
+    for c in counts:
+        offsets.append(offsets[-1] + c)
+    n = offsets[-1] + past
+    shape = (len(counts), inner, outer) if transpose else (len(counts), outer, inner)
+    return rand(n, inner), rand(*shape), rand(n, outer), offsets
+
+
+def on(gpu, offsets):
+    return torch.tensor(offsets, dtype=torch.int32, device=gpu)
+
+
+def check(x, w, dy, offsets, transpose, gpu):
+    at = on(gpu, offsets)
+    y, dx, dw = ref.experts(x, w, offsets, transpose, dy)
+    assert_within(lx.laplex_experts(x, w, at, transpose=transpose), *y)
+    got = lx.laplex_experts_backward(x, w, dy, at, transpose=transpose)
+    assert_within(got["dx"], *dx)
+    assert_within(got["dw"], *dw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts", [[1], [0, 1, 0], [5, 0, 64, 65, 1, 0], [200, 3], [1] * 70, [0, 0, 700]])
+def test_counts(gpu, dtype, transpose, counts):
+    check(*make(gpu, dtype, counts, 72, 136, transpose), transpose, gpu)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("inner,outer", [(1, 1), (1, 300), (300, 1), (7, 9), (64, 64), (8, 257), (129, 250), (512, 256),
+                                         (250, 520), (1000, 72)])
+def test_widths(gpu, dtype, transpose, inner, outer):
+    check(*make(gpu, dtype, [3, 40, 0, 90], inner, outer, transpose, seed=inner), transpose, gpu)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("rows", [16, 130, 600])
+def test_rows_of_no_expert(gpu, dtype, transpose, rows):
+    """Rows before the first expert's and past the last give 0 and are not used, whatever they hold."""
+    x, w, dy, offsets = make(gpu, dtype, [rows, 0, 2 * rows], 96, 80, transpose, before=67, past=131)
+    for t in (x, dy):
+        t[:67] = float("nan")
+        t[offsets[-1]:] = float("inf")
+    at = on(gpu, offsets)
+    clean = [t.clone() for t in (x, dy)]
+    for t in clean:
+        t[:67] = 0
+        t[offsets[-1]:] = 0
+    y, dx, dw = ref.experts(clean[0], w, offsets, transpose, clean[1])
+    assert_within(lx.laplex_experts(x, w, at, transpose=transpose), *y)
+    got = lx.laplex_experts_backward(x, w, dy, at, transpose=transpose)
+    assert_within(got["dx"], *dx)
+    assert_within(got["dw"], *dw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts", [[3, 2, 0, 4], [150, 70, 0, 300]])
+def test_a_row_reaches_its_own_results_alone(gpu, dtype, transpose, counts):
+    x, w, dy, offsets = make(gpu, dtype, counts, 128, 192, transpose)
+    at = on(gpu, offsets)
+    y0 = lx.laplex_experts(x, w, at, transpose=transpose)
+    g0 = lx.laplex_experts_backward(x, w, dy, at, transpose=transpose)
+    row = offsets[1]  # the second expert's first
+    x[row, 5], dy[row, 7] = float("inf"), float("nan")
+    y = lx.laplex_experts(x, w, at, transpose=transpose)
+    g = lx.laplex_experts_backward(x, w, dy, at, transpose=transpose)
+    others = torch.arange(x.shape[0], device=gpu) != row
+    assert torch.equal(y[others], y0[others]) and not torch.isfinite(y[row]).any()
+    assert torch.equal(g["dx"][others], g0["dx"][others]) and torch.isnan(g["dx"][row]).all()
+    keep = [0, 2, 3]
+    assert torch.equal(g["dw"][keep], g0["dw"][keep]) and not torch.isfinite(g["dw"][1]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("counts", [[2, 5], [100, 260]])
+def test_strided_and_unaligned(gpu, dtype, transpose, shift, counts):
+    """Rows that are parts of wider ones, from any value on; matrices with pitches of their own."""
+    x, w, dy, offsets = make(gpu, dtype, counts, 136, 72, transpose)
+    y0 = lx.laplex_experts(x, w, on(gpu, offsets), transpose=transpose)
+    g0 = lx.laplex_experts_backward(x, w, dy, on(gpu, offsets), transpose=transpose)
+
+    def inside(t, extra):
+        wide = torch.full((*t.shape[:-1], t.shape[-1] + extra), float("nan"), dtype=t.dtype, device=gpu)
+        view = wide[..., shift:shift + t.shape[-1]]
+        view.copy_(t)
+        return view
+
+    x2, dy2, w2 = inside(x, 11), inside(dy, 24), inside(w, 5)
+    # experts between each other's rows
+    w3 = torch.empty(w.shape[1], w.shape[0], w.shape[2], dtype=dtype, device=gpu).transpose(0, 1).copy_(w)
+    for m in (w2, w3):
+        assert torch.equal(lx.laplex_experts(x2, m, on(gpu, offsets), transpose=transpose), y0)
+        g = lx.laplex_experts_backward(x2, m, dy2, on(gpu, offsets), transpose=transpose)
+        assert torch.equal(g["dx"], g0["dx"]) and torch.equal(g["dw"], g0["dw"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_matrix_for_all(gpu, dtype):
+    x, w, _, offsets = make(gpu, dtype, [30, 0, 70], 64, 48, False)
+    one = w[:1].expand(3, -1, -1)
+    assert torch.equal(lx.laplex_experts(x, one, on(gpu, offsets)), lx.laplex_experts(x, one.contiguous(), on(gpu, offsets)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_no_rows(gpu, dtype):
+    x, w, dy, offsets = make(gpu, dtype, [0, 0], 24, 40, False)
+    assert lx.laplex_experts(x, w, on(gpu, offsets)).shape == (0, 40)
+    g = lx.laplex_experts_backward(x, w, dy, on(gpu, offsets))
+    assert g["dx"].shape == (0, 24) and not g["dw"].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_wanted_gradients_only(gpu, dtype):
+    x, w, dy, offsets = make(gpu, dtype, [30, 70], 64, 48, False)
+    both = lx.laplex_experts_backward(x, w, dy, on(gpu, offsets))
+    for name in ("dx", "dw"):
+        one = lx.laplex_experts_backward(x, w, dy, on(gpu, offsets), want=(name,))
+        assert list(one) == [name] and torch.equal(one[name], both[name])
+
+
+def test_offsets_out_of_range(gpu):
+    """Offsets are cut to the rows there are; nothing else is touched."""
+    x, w, dy, _ = make(gpu, torch.bfloat16, [100, 100], 64, 64, False)
+    wild = on(gpu, [-50, 100, 10 ** 9])
+    want = lx.laplex_experts(x, w, on(gpu, [0, 100, 200]))
+    assert torch.equal(lx.laplex_experts(x, w, wild), want)
+    g, g0 = (lx.laplex_experts_backward(x, w, dy, o) for o in (wild, on(gpu, [0, 100, 200])))
+    assert torch.equal(g["dw"], g0["dw"]) and torch.equal(g["dx"], g0["dx"])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradients_against_differences(gpu, dtype):
+    """<dL/dx, u> for L = <y, c> against (L(x + u) - L(x - u)) / 2: L is linear in x and in w, so the difference is the
+    gradient itself, up to roundings (float64 sums of the kernels' y)."""
+    x, w, c, offsets = make(gpu, dtype, [40, 0, 90], 96, 56, False)
+    at = on(gpu, offsets)
+    _, dx, dw = ref.experts(x, w, offsets, False, c)
+    g = lx.laplex_experts_backward(x, w, c, at)
+    u = torch.randn(x.shape, generator=torch.Generator().manual_seed(9)).to(dtype).to(gpu)
+    m = torch.randn(w.shape, generator=torch.Generator().manual_seed(8)).to(dtype).to(gpu)
+    half = torch.finfo(dtype).eps / 2
+
+    def off(t, bound, by):  # t within its bound and one rounding, summed with `by`
+        return float(((bound + half * (t.abs() + bound) + torch.finfo(dtype).tiny) * by.cpu().double().abs()).sum())
+
+    dot = lambda a, b: float((a.cpu().double() * b.cpu().double()).sum())  # noqa: E731
+    assert abs(dot(g["dx"], u) - dot(lx.laplex_experts(u, w, at), c)) <= off(*dx, u) + off(*ref.experts(u, w, offsets), c)
+    assert abs(dot(g["dw"], m) - dot(lx.laplex_experts(x, m, at), c)) <= off(*dw, m) + off(*ref.experts(x, m, offsets), c)
+
+
+def test_repeats_bit_for_bit_and_in_a_graph(gpu):
+    x, w, dy, offsets = make(gpu, torch.bfloat16, [300, 0, 700, 25], 256, 320, False)
+    at = on(gpu, offsets)
+
+    def both():
+        return lx.laplex_experts(x, w, at), lx.laplex_experts_backward(x, w, dy, at)
+
+    y0, g0 = both()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, g = both()
+    for k in range(3):
+        x.mul_(-1)
+        dy.mul_(2)
+        graph.replay()
+        torch.cuda.synchronize()
+        ye, ge = both()
+        assert torch.equal(y, ye) and torch.equal(g["dx"], ge["dx"]) and torch.equal(g["dw"], ge["dw"])
+    assert torch.equal(ye, -y0)
+
+
+def test_another_stream(gpu):
+    x, w, dy, offsets = make(gpu, torch.float16, [300, 200], 128, 64, True)
+    at = on(gpu, offsets)
+    want, side = lx.laplex_experts(x, w, at, transpose=True), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for s in (side, side.cuda_stream):
+        y = lx.laplex_experts(x, w, at, transpose=True, stream=s)
+        side.synchronize()
+        assert torch.equal(y, want)
