@@ -154,6 +154,323 @@ __global__ __launch_bounds__(kAnyThreads) void lx_experts_any_grad(ExpertsArgs A
                                       A.ldw);
 }
 
+// ---- 16-bit values, tiles by LDS ------------------------------------------
+
+constexpr int kK = 64;  // contraction of a step
+
+// How a product's operands lie in memory and LDS.  ALONG: lines are rows of
+// the operand, kK values of the contraction in 8 vectors of 16 bytes; vector c
+// of line r lies at c ^ (r % 8), so that eight lanes that read one vector of
+// eight lines each use all banks.  Else lines are steps of the contraction
+// with ROWS of the operand's rows next to each other; pairs of vectors are
+// exchanged so that the 16 lines of a transposing read spread over the banks.
+template <int ROWS, bool ALONG>
+struct Lines {
+    static constexpr int kVecs = ALONG ? kK / 8 : ROWS / 8;  // of a line
+    static constexpr int kCount = ALONG ? ROWS : kK;
+    static constexpr int kValues = ROWS * kK;
+    static __device__ __forceinline__ int swap(int line)
+    {
+        return ALONG ? line & 7 : (((line & 3) | ((line >> 1) & 4)) << 1) & (kVecs - 1);
+    }
+    // Zeros from contraction `left` on.
+    template <class T>
+    static __device__ __forceinline__ void blank(T* p, int left, int threads)
+    {
+        for (int i = threadIdx.x; i < kValues / 8; i += threads) {
+            const int line = i / kVecs;
+            if (ALONG ? 8 * ((i % kVecs) ^ swap(line)) >= left : line >= left) *reinterpret_cast<Pack<T, 8>*>(p + 8 * i) = Pack<T, 8>{};
+        }
+    }
+    // 16 rows from row0 on, contraction 32 s .. 32 s + 31 in the order 8 g + i
+    template <class T>
+    static __device__ __forceinline__ Frag<T> read(const T* p, int row0, int s)
+    {
+        const int lane = threadIdx.x & 63;
+        Frag<T> f;
+        if constexpr (ALONG) {
+            const int r = row0 + (lane & 15);
+            f = frag_along(p + r * kK + ((4 * s + (lane >> 4)) ^ swap(r)) * 8);
+        } else {
+            typedef short S4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) S4* At;
+            union { S4 h[2]; typename Frag<T>::V v; } u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int line = 32 * s + 8 * (lane >> 4) + 4 * i + ((lane & 15) >> 2);
+                const int at = row0 + 4 * (lane & 3);
+                u.h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (At)(const_cast<T*>(p) + line * ROWS + (((at >> 3) ^ swap(line)) << 3) + (at & 7)));
+            }
+            f.v = u.v;
+        }
+        return f;
+    }
+};
+
+// 16 bytes a lane from base + off to LDS, lane after lane from s on.  By hand
+// because the compiler, which cannot tell the two tiles apart, would wait for
+// every such load before the next read of LDS; tile_product waits for them
+// itself before it hands a tile over.  No register is written.
+__device__ __forceinline__ void to_lds(const void* base, uint32_t off, void* s)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(at), "v"(off), "s"(base)
+                 : "memory");
+}
+
+// What a thread moves of a tile: kVecs vectors of 16 bytes a step, straight to
+// LDS (DMA: 16-byte aligned lines; lines and vectors that are not there are
+// read from the last ones that are) or by registers (any alignment, 0 for
+// what is not there).
+template <class T, int ROWS, bool ALONG, int THREADS, bool DMA>
+struct Mover {
+    typedef Lines<ROWS, ALONG> L;
+    static constexpr int kAll = ROWS * kK / 8, kVecs = (kAll + THREADS - 1) / THREADS;
+    static_assert(kAll % 64 == 0, "whole waves");
+    // vectors of wave w, j-th: 64 from here on
+    static __device__ __forceinline__ int first(int j)
+    {
+        return (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kVecs + j) * 64;
+    }
+    static __device__ __forceinline__ bool has(int j) { return kAll % THREADS == 0 || first(j) < kAll; }
+    const T* base;    // first row, first step
+    int64_t ld;
+    int rows;         // rows that are there
+    uint32_t line[kVecs], at[kVecs];  // values from base to the line and within it
+    Pack<T, 8> r[DMA ? 1 : kVecs];
+
+    __device__ __forceinline__ void init(const T* p, int64_t pitch, int64_t there)
+    {
+        base = p;
+        ld = pitch;
+        rows = there < ROWS ? (int)there : ROWS;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const int i = first(j) + (threadIdx.x & 63);
+            const int l = i / L::kVecs, v = (i % L::kVecs) ^ L::swap(l);
+            if (DMA) {
+                line[j] = (uint32_t)(ALONG ? (l < rows ? l : rows - 1) : l) * (uint32_t)ld;
+                at[j] = 8 * v;
+                if (!ALONG && (int)at[j] > rows - 8) at[j] = rows - 8;
+            } else {
+                line[j] = l;
+                at[j] = 8 * v;
+            }
+        }
+    }
+    // Vector j of the step whose contraction starts at k0, of k in all.
+    __device__ __forceinline__ void load(int j, int64_t k0, int64_t k, T* s)
+    {
+        if (!has(j)) return;
+        const T* p = base + (ALONG ? k0 : k0 * ld);
+        if constexpr (DMA) {
+            const int64_t left = k - k0;
+            uint32_t off;
+            if (ALONG) {
+                const uint32_t most = left < kK ? (uint32_t)left - 8 : kK;
+                off = line[j] + (at[j] < most ? at[j] : most);
+            } else {
+                const uint32_t most = (uint32_t)(left < kK ? left - 1 : kK) * (uint32_t)ld;
+                off = (line[j] < most ? line[j] : most) + at[j];
+            }
+            to_lds(p, off * (uint32_t)sizeof(T), s + first(j) * 8);
+        } else {
+            const int64_t left = k - k0;
+            const int64_t lines = ALONG ? rows : left, along = (ALONG ? left : rows) - at[j];
+            const T* q = p + line[j] * ld + at[j];
+            if (line[j] < lines && along >= 8) {
+                r[j] = load_pack<8>(q);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 8; ++v) r[j].v[v] = line[j] < lines && v < along ? q[v] : (T)0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void put(T* s) const
+    {
+        if constexpr (!DMA) {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                if (has(j)) *reinterpret_cast<Pack<T, 8>*>(s + (first(j) + (threadIdx.x & 63)) * 8) = r[j];
+        }
+    }
+};
+
+// Shapes of a tile: BM rows by BN columns, WM x WN waves.
+template <int BM_, int BN_, int WM_, int WN_>
+struct Shape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int kThreads = 64 * WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+};
+
+// c [rows][cols] = a b^T.  Two tiles in LDS: while one is multiplied, the
+// next one is on its way; a barrier a step.  The order within a step is fixed
+// by hand: fragments are read two ahead of the products that use them, loads
+// go out among the first products.
+template <class T, class S, bool AALONG, bool BALONG, bool DMA>
+__device__ __forceinline__ void tile_product(const T* a, int64_t lda, int64_t rows, const T* b, int64_t ldb,
+                                             int64_t cols, int64_t k, T* c, int64_t ldc)
+{
+    typedef Lines<S::BM, AALONG> LA;
+    typedef Lines<S::BN, BALONG> LB;
+    constexpr int TM = S::TM, TN = S::TN;
+    constexpr int kTile = LA::kValues + LB::kValues;
+    __shared__ alignas(1024) T s_tiles[2 * kTile];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m0 = wave / S::WN * 16 * TM, n0 = wave % S::WN * 16 * TN;
+    const bool on = m0 < rows && n0 < cols;  // whether any of the wave's results are there
+    f32x4 acc[TM][TN] = {};
+    Mover<T, S::BM, AALONG, S::kThreads, DMA> ma;
+    Mover<T, S::BN, BALONG, S::kThreads, DMA> mb;
+    constexpr int VA = decltype(ma)::kVecs, VB = decltype(mb)::kVecs;
+    ma.init(a, lda, rows);
+    mb.init(b, ldb, cols);
+
+    auto load = [&](int q, int64_t k0, T* to) {
+        if (q < VA) ma.load(q, k0, k, to);
+        else if (q < VA + VB) mb.load(q - VA, k0, k, to + LA::kValues);
+    };
+    auto put = [&](T* to) {
+        ma.put(to);
+        mb.put(to + LA::kValues);
+    };
+    T* now = s_tiles;
+    T* next = s_tiles + kTile;
+    if (k > 0) {
+#pragma unroll
+        for (int q = 0; q < VA + VB; ++q) load(q, 0, now);
+        put(now);
+    }
+    for (int64_t k0 = 0; k0 < k; k0 += kK) {
+        const bool more = k0 + kK < k;
+        // the tile is there and everyone is done with the other one
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        __syncthreads();
+        if (DMA && k - k0 < kK) {  // past the end of the contraction: other rows' values, or whatever else
+            LA::blank(now, (int)(k - k0), S::kThreads);
+            LB::blank(now + LA::kValues, (int)(k - k0), S::kThreads);
+            __syncthreads();
+        }
+        if (on) {
+            const T *sa = now, *sb = now + LA::kValues;
+            Frag<T> fa[2][TM], fb[2][TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb[0][j] = LB::read(sb, n0 + 16 * j, 0);
+            fa[0][0] = LA::read(sa, m0, 0);
+            if (TM > 1) fa[0][1] = LA::read(sa, m0 + 16, 0);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (TM == 1) {
+                        if (s == 0) {
+                            fa[1][0] = LA::read(sa, m0, 1);
+#pragma unroll
+                            for (int j = 0; j < TN; ++j) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
+                        }
+                    } else if (i + 2 < TM) {
+                        fa[s][i + 2] = LA::read(sa, m0 + 16 * (i + 2), s);
+                    } else if (s == 0) {
+                        fa[1][i + 2 - TM] = LA::read(sa, m0 + 16 * (i + 2 - TM), 1);
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+                            if ((j < (TN + 1) / 2) == (i == TM - 2)) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
+                    }
+                    constexpr int kEach = TM >= 8 ? 2 : VA + VB;
+                    if (s == 0 && i * kEach < VA + VB && more) {
+#pragma unroll
+                        for (int q = 0; q < kEach; ++q) load(i * kEach + q, k0 + kK, next);
+                    }
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) acc[i][j] = mma(fb[s][j], fa[s][i], acc[i][j]);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        } else if (more) {
+#pragma unroll
+            for (int q = 0; q < VA + VB; ++q) load(q, k0 + kK, next);
+        }
+        if (more) put(next);
+        T* t = now;
+        now = next;
+        next = t;
+    }
+    if (!on) return;
+    // a lane holds row l % 16 and four neighbouring columns of each tile
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int m = m0 + 16 * i + (lane & 15);
+        if (m >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int n = n0 + 16 * j + 4 * (lane >> 4);
+            T* p = c + m * ldc + n;
+            const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+            if (n + 4 <= cols) {
+                store_vec<4>(p, v);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (n + r < cols) p[r] = (T)v[r];
+            }
+        }
+    }
+}
+
+// Workgroup `id` of `total`, consecutive ones of a die next to each other
+// (workgroups go round the eight dies in turn): each die takes a run of tiles.
+__device__ __forceinline__ int64_t by_die(int64_t id, int64_t total)
+{
+    const int64_t run = (total + 7) / 8;
+    return (id & 7) * run + (id >> 3);
+}
+
+constexpr int kBand = 8;  // row tiles of a band: its tiles go column by column
+
+template <class T, class S, bool BALONG, bool DMA>
+__global__ __launch_bounds__(S::kThreads) void lx_experts_tile(ExpertsArgs A)
+{
+    const Ragged R{A.offsets, A.experts, A.n, 0};
+    const int64_t units = R.units(S::BM), total = units * A.col_tiles;
+    const int64_t id = by_die(group_id<S::kThreads>(), total);
+    if (id >= total) return;
+    const int64_t band = id / (kBand * A.col_tiles), in_band = id - band * kBand * A.col_tiles;
+    const int64_t high = units - band * kBand < kBand ? units - band * kBand : kBand;
+    const int64_t c0 = in_band / high * S::BN;
+    const RaggedTile t = R.find(band * kBand + in_band % high, S::BM);
+    if (t.rows <= 0) return;
+    const int64_t cols = A.out - c0;
+    T* y = (T*)A.y + t.row * A.ldy + c0;
+    if (t.group < 0) {
+        for (int i = threadIdx.x; i < t.rows * S::BN; i += S::kThreads)
+            if (i % S::BN < cols) y[(int64_t)(i / S::BN) * A.ldy + i % S::BN] = (T)0.f;
+        return;
+    }
+    const T* w = (const T*)A.w + t.group * A.pitch_w + (BALONG ? c0 * A.ldw : c0);
+    tile_product<T, S, true, BALONG, DMA>((const T*)A.x + t.row * A.ldx, A.ldx, t.rows, w, A.ldw, cols, A.in, y, A.ldy);
+}
+
+template <class T, class S, bool DMA>
+__global__ __launch_bounds__(S::kThreads) void lx_experts_tile_grad(ExpertsArgs A)
+{
+    const int64_t each = A.row_tiles * A.col_tiles, total = A.experts * each;
+    const int64_t id = by_die(group_id<S::kThreads>(), total);
+    if (id >= total) return;
+    const int64_t e = id / each, rest = id - e * each;
+    const int64_t band = rest / (kBand * A.col_tiles), in_band = rest - band * kBand * A.col_tiles;
+    const int64_t high = A.row_tiles - band * kBand < kBand ? A.row_tiles - band * kBand : kBand;
+    const int64_t m0 = (band * kBand + in_band % high) * S::BM, c0 = in_band / high * S::BN;
+    const Ragged R{A.offsets, A.experts, A.n, 0};
+    const int64_t first = R.bound(e + 1), end = R.bound(e + 2);
+    tile_product<T, S, false, false, DMA>((const T*)A.y + first * A.ldy + m0, A.ldy, A.out - m0,
+                                          (const T*)A.x + first * A.ldx + c0, A.ldx, A.in - c0,
+                                          end > first ? end - first : 0,
+                                          (T*)A.dw + e * A.pitch_w + m0 * A.ldw + c0, A.ldw);
+}
+
 template <class T>
 hipError_t any_go(ExpertsArgs a, hipStream_t s)
 {
@@ -178,14 +495,73 @@ hipError_t any_grad_go(ExpertsArgs a, hipStream_t s)
     return hipSuccess;
 }
 
+bool lines16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && ld <= 1 << 22; }
+
+template <class T, class S>
+hipError_t tile_go(ExpertsArgs a, bool dma, hipStream_t s)
+{
+    a.col_tiles = (a.out + S::BN - 1) / S::BN;
+    const int64_t groups = (Ragged{a.offsets, a.experts, a.n, 0}.units(S::BM) * a.col_tiles + 7) / 8 * 8;
+    const dim3 grid = grid_of<S::kThreads>(groups);
+    if (a.transpose) {
+        if (dma)
+            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, false, true><<<grid, S::kThreads, 0, s>>>(a)));
+        else
+            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, false, false><<<grid, S::kThreads, 0, s>>>(a)));
+    } else {
+        if (dma)
+            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, true, true><<<grid, S::kThreads, 0, s>>>(a)));
+        else
+            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, true, false><<<grid, S::kThreads, 0, s>>>(a)));
+    }
+    return hipSuccess;
+}
+
+template <class T, class S>
+hipError_t tile_grad_go(ExpertsArgs a, bool dma, hipStream_t s)
+{
+    a.row_tiles = (a.out + S::BM - 1) / S::BM;
+    a.col_tiles = (a.in + S::BN - 1) / S::BN;
+    const dim3 grid = grid_of<S::kThreads>((a.experts * a.row_tiles * a.col_tiles + 7) / 8 * 8);
+    if (dma)
+        LX_LAUNCH("experts_grad", s, (lx_experts_tile_grad<T, S, true><<<grid, S::kThreads, 0, s>>>(a)));
+    else
+        LX_LAUNCH("experts_grad", s, (lx_experts_tile_grad<T, S, false><<<grid, S::kThreads, 0, s>>>(a)));
+    return hipSuccess;
+}
+
+typedef Shape<256, 256, 2, 4> Large;
+typedef Shape<128, 128, 2, 2> Middle;
+typedef Shape<16, 128, 1, 4> Small;
+
+template <class T>
+hipError_t tiles_go(const ExpertsArgs& a, hipStream_t s)
+{
+    const bool dma = a.in % 8 == 0 && (!a.transpose || a.out % 8 == 0) && lines16(a.x, a.ldx) && lines16(a.w, a.ldw) &&
+                     a.pitch_w % 8 == 0;
+    const int64_t each = a.n / a.experts;  // rows of an expert
+    if (each > 160) return tile_go<T, Large>(a, dma, s);
+    if (each > 16) return tile_go<T, Middle>(a, dma, s);
+    return tile_go<T, Small>(a, dma, s);
+}
+
+template <class T>
+hipError_t tiles_grad_go(const ExpertsArgs& a, hipStream_t s)
+{
+    const bool dma = a.in % 8 == 0 && a.out % 8 == 0 && lines16(a.x, a.ldx) && lines16(a.y, a.ldy);
+    const double tiles = (double)a.experts * (double)a.out * (double)a.in / 65536.0;
+    if (tiles >= 256.0) return tile_grad_go<T, Large>(a, dma, s);
+    return tile_grad_go<T, Middle>(a, dma, s);
+}
+
 }  // namespace
 
 hipError_t experts_launch(const ExpertsArgs& a, int dtype, hipStream_t s)
 {
     switch (dtype) {
         case 0: return any_go<float>(a, s);
-        case 1: return any_go<bf16_t>(a, s);
-        case 2: return any_go<f16_t>(a, s);
+        case 1: return tiles_go<bf16_t>(a, s);
+        case 2: return tiles_go<f16_t>(a, s);
         default: return hipErrorInvalidValue;
     }
 }
@@ -194,8 +570,8 @@ hipError_t experts_grad_launch(const ExpertsArgs& a, int dtype, hipStream_t s)
 {
     switch (dtype) {
         case 0: return any_grad_go<float>(a, s);
-        case 1: return any_grad_go<bf16_t>(a, s);
-        case 2: return any_grad_go<f16_t>(a, s);
+        case 1: return tiles_grad_go<bf16_t>(a, s);
+        case 2: return tiles_grad_go<f16_t>(a, s);
         default: return hipErrorInvalidValue;
     }
 }
