@@ -244,7 +244,7 @@ struct Mover {
 
     __device__ __forceinline__ void init(const T* p, int64_t pitch, int64_t there)
     {
-        base = p;
+        base = (const T*)(uintptr_t)uniform((int64_t)(uintptr_t)p);
         ld = pitch;
         rows = there < ROWS ? (int)there : ROWS;
 #pragma unroll
@@ -304,6 +304,10 @@ template <int BM_, int BN_, int WM_, int WN_>
 struct Shape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
     static constexpr int kThreads = 64 * WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    // A wave's place.  Waves w and w + 4 share a SIMD: of 2 x 4 waves they get
+    // different halves both ways, so that half a tile keeps all SIMDs at work.
+    static __device__ __forceinline__ int row_of(int w) { return WM == 2 && WN == 4 ? (w ^ (w >> 2)) & 1 : w / WN; }
+    static __device__ __forceinline__ int col_of(int w) { return WM == 2 && WN == 4 ? w >> 1 : w % WN; }
 };
 
 // c [rows][cols] = a b^T.  Two tiles in LDS: while one is multiplied, the
@@ -320,7 +324,7 @@ __device__ __forceinline__ void tile_product(const T* a, int64_t lda, int64_t ro
     constexpr int kTile = LA::kValues + LB::kValues;
     __shared__ alignas(1024) T s_tiles[2 * kTile];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m0 = wave / S::WN * 16 * TM, n0 = wave % S::WN * 16 * TN;
+    const int m0 = S::row_of(wave) * 16 * TM, n0 = S::col_of(wave) * 16 * TN;
     const bool on = m0 < rows && n0 < cols;  // whether any of the wave's results are there
     f32x4 acc[TM][TN] = {};
     Mover<T, S::BM, AALONG, S::kThreads, DMA> ma;
@@ -420,27 +424,32 @@ __device__ __forceinline__ void tile_product(const T* a, int64_t lda, int64_t ro
     }
 }
 
-// Workgroup `id` of `total`, consecutive ones of a die next to each other
-// (workgroups go round the eight dies in turn): each die takes a run of tiles.
-__device__ __forceinline__ int64_t by_die(int64_t id, int64_t total)
-{
-    const int64_t run = (total + 7) / 8;
-    return (id & 7) * run + (id >> 3);
-}
-
 constexpr int kBand = 8;  // row tiles of a band: its tiles go column by column
 
+// Place `at` among rows x cols tiles.
+struct Place {
+    int64_t row, col;
+};
+__device__ __forceinline__ Place in_bands(int64_t at, int64_t rows, int64_t cols)
+{
+    const int64_t band = at / (kBand * cols), in_band = at - band * kBand * cols;
+    const int64_t high = rows - band * kBand < kBand ? rows - band * kBand : kBand;
+    return {band * kBand + in_band % high, in_band / high};
+}
+
+// Workgroups go round the eight dies in turn, so each die takes a run of
+// tiles, which share operands in its cache.
 template <class T, class S, bool BALONG, bool DMA>
 __global__ __launch_bounds__(S::kThreads) void lx_experts_tile(ExpertsArgs A)
 {
     const Ragged R{A.offsets, A.experts, A.n, 0};
-    const int64_t units = R.units(S::BM), total = units * A.col_tiles;
-    const int64_t id = by_die(group_id<S::kThreads>(), total);
-    if (id >= total) return;
-    const int64_t band = id / (kBand * A.col_tiles), in_band = id - band * kBand * A.col_tiles;
-    const int64_t high = units - band * kBand < kBand ? units - band * kBand : kBand;
-    const int64_t c0 = in_band / high * S::BN;
-    const RaggedTile t = R.find(band * kBand + in_band % high, S::BM);
+    const int64_t id = group_id<S::kThreads>();
+    const Ragged::Dense d = R.dense(S::BM);
+    const int64_t rows = d.inside + d.outside, run = (rows * A.col_tiles + 7) / 8, at = (id & 7) * run + (id >> 3);
+    if ((id >> 3) >= run || at >= rows * A.col_tiles) return;
+    const Place p = in_bands(at, rows, A.col_tiles);
+    const RaggedTile t = p.row < d.inside ? R.dense_tile(d, (int)p.row, S::BM) : R.outside_tile((int)p.row - d.inside, S::BM);
+    const int64_t c0 = p.col * S::BN;
     if (t.rows <= 0) return;
     const int64_t cols = A.out - c0;
     T* y = (T*)A.y + t.row * A.ldy + c0;
@@ -456,15 +465,25 @@ __global__ __launch_bounds__(S::kThreads) void lx_experts_tile(ExpertsArgs A)
 template <class T, class S, bool DMA>
 __global__ __launch_bounds__(S::kThreads) void lx_experts_tile_grad(ExpertsArgs A)
 {
-    const int64_t each = A.row_tiles * A.col_tiles, total = A.experts * each;
-    const int64_t id = by_die(group_id<S::kThreads>(), total);
-    if (id >= total) return;
-    const int64_t e = id / each, rest = id - e * each;
-    const int64_t band = rest / (kBand * A.col_tiles), in_band = rest - band * kBand * A.col_tiles;
-    const int64_t high = A.row_tiles - band * kBand < kBand ? A.row_tiles - band * kBand : kBand;
-    const int64_t m0 = (band * kBand + in_band % high) * S::BM, c0 = in_band / high * S::BN;
+    // Experts go round the dies, so that a die's are long and short ones;
+    // fewer than eight of them are cut into runs.
+    const int64_t each = A.row_tiles * A.col_tiles, id = group_id<S::kThreads>(), die = id & 7;
+    const int64_t whole = A.experts / 8 * 8 * each;
+    int64_t at;
+    if (id < whole) {
+        at = id >> 3;
+        at = (at / each * 8 + die) * each + at % each;
+    } else {
+        const int64_t left = A.experts * each - whole;
+        at = (id - whole) / 8 + die * ((left + 7) / 8);
+        if (at >= left || (id - whole) / 8 >= (left + 7) / 8) return;
+        at += whole;
+    }
+    const int64_t e = at / each;
+    const Place p = in_bands(at - e * each, A.row_tiles, A.col_tiles);
+    const int64_t m0 = p.row * S::BM, c0 = p.col * S::BN;
     const Ragged R{A.offsets, A.experts, A.n, 0};
-    const int64_t first = R.bound(e + 1), end = R.bound(e + 2);
+    const int64_t first = uniform(R.bound(e + 1)), end = uniform(R.bound(e + 2));
     tile_product<T, S, false, false, DMA>((const T*)A.y + first * A.ldy + m0, A.ldy, A.out - m0,
                                           (const T*)A.x + first * A.ldx + c0, A.ldx, A.in - c0,
                                           end > first ? end - first : 0,
