@@ -242,11 +242,11 @@ struct Mover {
     uint32_t line[kVecs], at[kVecs];  // values from base to the line and within it
     Pack<T, 8> r[DMA ? 1 : kVecs];
 
-    __device__ __forceinline__ void init(const T* p, int64_t pitch, int64_t there)
+    __device__ __forceinline__ void init(const T* p, int64_t pitch, int there)
     {
         base = (const T*)(uintptr_t)uniform((int64_t)(uintptr_t)p);
         ld = pitch;
-        rows = there < ROWS ? (int)there : ROWS;
+        rows = there;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             const int i = first(j) + (threadIdx.x & 63);
@@ -304,19 +304,36 @@ template <int BM_, int BN_, int WM_, int WN_>
 struct Shape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
     static constexpr int kThreads = 64 * WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    // Workgroups that stay for several tiles: one on each of the 256 CUs,
+    // which saves the wait for a tile's first values.  Where the contraction k
+    // is short the results' way to memory is the bound, and tiles that end at
+    // any time do better (gradient of 128 matrices of 1536 x 2048: 30 rows each
+    // 289 us against 267, 200 rows 210 against 213).  Smaller shapes overlap
+    // by themselves, and what staying costs in registers costs more.
+    static constexpr bool kStays = BM >= 256;
+    static int64_t groups(int64_t tiles, int64_t k) { return kStays && tiles > 256 && k >= 192 ? 256 : tiles; }
     // A wave's place.  Waves w and w + 4 share a SIMD: of 2 x 4 waves they get
     // different halves both ways, so that half a tile keeps all SIMDs at work.
     static __device__ __forceinline__ int row_of(int w) { return WM == 2 && WN == 4 ? (w ^ (w >> 2)) & 1 : w / WN; }
     static __device__ __forceinline__ int col_of(int w) { return WM == 2 && WN == 4 ? w >> 1 : w % WN; }
 };
 
-// c [rows][cols] = a b^T.  Two tiles in LDS: while one is multiplied, the
-// next one is on its way; a barrier a step.  The order within a step is fixed
-// by hand: fragments are read two ahead of the products that use them, loads
-// go out among the first products.
-template <class T, class S, bool AALONG, bool BALONG, bool DMA>
-__device__ __forceinline__ void tile_product(const T* a, int64_t lda, int64_t rows, const T* b, int64_t ldb,
-                                             int64_t cols, int64_t k, T* c, int64_t ldc)
+// One tile c [rows][cols] = a b^T of a launch's work.
+template <class T>
+struct Work {
+    const T *a, *b;
+    T* c;
+    int rows, cols;
+    int64_t k;
+};
+
+// The tiles that `next` gives, one after the other.  Two steps in LDS: while
+// one is multiplied, the next one is on its way, across the end of a tile
+// too; a barrier a step.  The order within a step is fixed by hand: fragments
+// are read two ahead of the products that use them, loads go out among the
+// first products.
+template <class T, class S, bool AALONG, bool BALONG, bool DMA, class Next>
+__device__ __forceinline__ void tile_products(int64_t lda, int64_t ldb, int64_t ldc, Next next_work)
 {
     typedef Lines<S::BM, AALONG> LA;
     typedef Lines<S::BN, BALONG> LB;
@@ -325,15 +342,10 @@ __device__ __forceinline__ void tile_product(const T* a, int64_t lda, int64_t ro
     __shared__ alignas(1024) T s_tiles[2 * kTile];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m0 = S::row_of(wave) * 16 * TM, n0 = S::col_of(wave) * 16 * TN;
-    const bool on = m0 < rows && n0 < cols;  // whether any of the wave's results are there
-    f32x4 acc[TM][TN] = {};
     Mover<T, S::BM, AALONG, S::kThreads, DMA> ma;
     Mover<T, S::BN, BALONG, S::kThreads, DMA> mb;
     constexpr int VA = decltype(ma)::kVecs, VB = decltype(mb)::kVecs;
-    ma.init(a, lda, rows);
-    mb.init(b, ldb, cols);
-
-    auto load = [&](int q, int64_t k0, T* to) {
+    auto load = [&](int q, int64_t k0, int64_t k, T* to) {
         if (q < VA) ma.load(q, k0, k, to);
         else if (q < VA + VB) mb.load(q - VA, k0, k, to + LA::kValues);
     };
@@ -341,87 +353,117 @@ __device__ __forceinline__ void tile_product(const T* a, int64_t lda, int64_t ro
         ma.put(to);
         mb.put(to + LA::kValues);
     };
+
+    Work<T> w;
+    if (!next_work(w)) return;
     T* now = s_tiles;
     T* next = s_tiles + kTile;
-    if (k > 0) {
+    ma.init(w.a, lda, w.rows);
+    mb.init(w.b, ldb, w.cols);
 #pragma unroll
-        for (int q = 0; q < VA + VB; ++q) load(q, 0, now);
-        put(now);
-    }
-    for (int64_t k0 = 0; k0 < k; k0 += kK) {
-        const bool more = k0 + kK < k;
-        // the tile is there and everyone is done with the other one
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-        __syncthreads();
-        if (DMA && k - k0 < kK) {  // past the end of the contraction: other rows' values, or whatever else
-            LA::blank(now, (int)(k - k0), S::kThreads);
-            LB::blank(now + LA::kValues, (int)(k - k0), S::kThreads);
+    for (int q = 0; q < VA + VB; ++q) load(q, 0, w.k, now);
+    put(now);
+    for (;;) {
+        const bool on = m0 < w.rows && n0 < w.cols;  // whether any of the wave's results are there
+        f32x4 acc[TM][TN] = {};
+        Work<T> then;
+        const bool goes_on = S::kStays && next_work(then);
+        bool more = true;  // whether anything is loaded during a step
+        for (int64_t k0 = 0; k0 < w.k; k0 += kK) {
+            int64_t k1 = k0 + kK, k = w.k;  // the next step
+            if (k1 >= w.k) {
+                more = goes_on;
+                if (more) {
+                    ma.init(then.a, lda, then.rows);
+                    mb.init(then.b, ldb, then.cols);
+                    k1 = 0;
+                    k = then.k;
+                }
+            }
+            // this step's values are there and everyone is done with the other ones
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
             __syncthreads();
+            if (DMA && w.k - k0 < kK) {  // past the end of the contraction: other rows' values, or whatever else
+                LA::blank(now, (int)(w.k - k0), S::kThreads);
+                LB::blank(now + LA::kValues, (int)(w.k - k0), S::kThreads);
+                __syncthreads();
+            }
+            if (on) {
+                const T *sa = now, *sb = now + LA::kValues;
+                Frag<T> fa[2][TM], fb[2][TN];
+#pragma unroll
+                for (int j = 0; j < TN; ++j) fb[0][j] = LB::read(sb, n0 + 16 * j, 0);
+                fa[0][0] = LA::read(sa, m0, 0);
+                if (TM > 1) fa[0][1] = LA::read(sa, m0 + 16, 0);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (TM == 1) {
+                            if (s == 0) {
+                                fa[1][0] = LA::read(sa, m0, 1);
+#pragma unroll
+                                for (int j = 0; j < TN; ++j) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
+                            }
+                        } else if (i + 2 < TM) {
+                            fa[s][i + 2] = LA::read(sa, m0 + 16 * (i + 2), s);
+                        } else if (s == 0) {
+                            fa[1][i + 2 - TM] = LA::read(sa, m0 + 16 * (i + 2 - TM), 1);
+#pragma unroll
+                            for (int j = 0; j < TN; ++j)
+                                if ((j < (TN + 1) / 2) == (i == TM - 2)) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
+                        }
+                        constexpr int kEach = TM >= 8 ? 2 : VA + VB;
+                        if (s == 0 && i * kEach < VA + VB && more) {
+#pragma unroll
+                            for (int q = 0; q < kEach; ++q) load(i * kEach + q, k1, k, next);
+                        }
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) acc[i][j] = mma(fb[s][j], fa[s][i], acc[i][j]);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+            } else if (more) {
+#pragma unroll
+                for (int q = 0; q < VA + VB; ++q) load(q, k1, k, next);
+            }
+            if (more) put(next);
+            T* t = now;
+            now = next;
+            next = t;
         }
         if (on) {
-            const T *sa = now, *sb = now + LA::kValues;
-            Frag<T> fa[2][TM], fb[2][TN];
+            // a lane holds row l % 16 and four neighbouring columns of each tile
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[0][j] = LB::read(sb, n0 + 16 * j, 0);
-            fa[0][0] = LA::read(sa, m0, 0);
-            if (TM > 1) fa[0][1] = LA::read(sa, m0 + 16, 0);
+            for (int i = 0; i < TM; ++i) {
+                const int m = m0 + 16 * i + (lane & 15);
+                if (m >= w.rows) continue;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+                for (int j = 0; j < TN; ++j) {
+                    const int n = n0 + 16 * j + 4 * (lane >> 4);
+                    T* p = w.c + m * ldc + n;
+                    const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    if (n + 4 <= w.cols) {
+                        store_vec<4>(p, v);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (TM == 1) {
-                        if (s == 0) {
-                            fa[1][0] = LA::read(sa, m0, 1);
-#pragma unroll
-                            for (int j = 0; j < TN; ++j) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
-                        }
-                    } else if (i + 2 < TM) {
-                        fa[s][i + 2] = LA::read(sa, m0 + 16 * (i + 2), s);
-                    } else if (s == 0) {
-                        fa[1][i + 2 - TM] = LA::read(sa, m0 + 16 * (i + 2 - TM), 1);
-#pragma unroll
-                        for (int j = 0; j < TN; ++j)
-                            if ((j < (TN + 1) / 2) == (i == TM - 2)) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
+                        for (int r = 0; r < 4; ++r)
+                            if (n + r < w.cols) p[r] = (T)v[r];
                     }
-                    constexpr int kEach = TM >= 8 ? 2 : VA + VB;
-                    if (s == 0 && i * kEach < VA + VB && more) {
-#pragma unroll
-                        for (int q = 0; q < kEach; ++q) load(i * kEach + q, k0 + kK, next);
-                    }
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) acc[i][j] = mma(fb[s][j], fa[s][i], acc[i][j]);
                 }
-            __builtin_amdgcn_sched_barrier(0);
-        } else if (more) {
-#pragma unroll
-            for (int q = 0; q < VA + VB; ++q) load(q, k0 + kK, next);
-        }
-        if (more) put(next);
-        T* t = now;
-        now = next;
-        next = t;
-    }
-    if (!on) return;
-    // a lane holds row l % 16 and four neighbouring columns of each tile
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int m = m0 + 16 * i + (lane & 15);
-        if (m >= rows) continue;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int n = n0 + 16 * j + 4 * (lane >> 4);
-            T* p = c + m * ldc + n;
-            const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-            if (n + 4 <= cols) {
-                store_vec<4>(p, v);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n + r < cols) p[r] = (T)v[r];
             }
         }
+        if (!more) return;
+        w = then;
     }
+}
+
+// Zeros for rows x (at most W) cols.
+template <int W, int THREADS, class T>
+__device__ __forceinline__ void zero_tile(T* p, int64_t ld, int64_t rows, int64_t cols)
+{
+    for (int64_t i = threadIdx.x; i < rows * W; i += THREADS)
+        if (i % W < cols) p[i / W * ld + i % W] = (T)0.f;
 }
 
 constexpr int kBand = 8;  // row tiles of a band: its tiles go column by column
@@ -438,56 +480,139 @@ __device__ __forceinline__ Place in_bands(int64_t at, int64_t rows, int64_t cols
 }
 
 // Workgroups go round the eight dies in turn, so each die takes a run of
-// tiles, which share operands in its cache.
+// tiles, which share operands in its cache.  Where there are more tiles than
+// workgroups, a workgroup takes every gridDim-th.
 template <class T, class S, bool BALONG, bool DMA>
-__global__ __launch_bounds__(S::kThreads) void lx_experts_tile(ExpertsArgs A)
+__global__ __launch_bounds__(S::kThreads, 2) void lx_experts_tile(ExpertsArgs A)
 {
     const Ragged R{A.offsets, A.experts, A.n, 0};
-    const int64_t id = group_id<S::kThreads>();
+    const int64_t id = group_id<S::kThreads>(), die = id & 7;
+    int64_t turn = id >> 3;
     const Ragged::Dense d = R.dense(S::BM);
-    const int64_t rows = d.inside + d.outside, run = (rows * A.col_tiles + 7) / 8, at = (id & 7) * run + (id >> 3);
-    if ((id >> 3) >= run || at >= rows * A.col_tiles) return;
-    const Place p = in_bands(at, rows, A.col_tiles);
-    const RaggedTile t = p.row < d.inside ? R.dense_tile(d, (int)p.row, S::BM) : R.outside_tile((int)p.row - d.inside, S::BM);
-    const int64_t c0 = p.col * S::BN;
-    if (t.rows <= 0) return;
-    const int64_t cols = A.out - c0;
-    T* y = (T*)A.y + t.row * A.ldy + c0;
-    if (t.group < 0) {
-        for (int i = threadIdx.x; i < t.rows * S::BN; i += S::kThreads)
-            if (i % S::BN < cols) y[(int64_t)(i / S::BN) * A.ldy + i % S::BN] = (T)0.f;
-        return;
-    }
-    const T* w = (const T*)A.w + t.group * A.pitch_w + (BALONG ? c0 * A.ldw : c0);
-    tile_product<T, S, true, BALONG, DMA>((const T*)A.x + t.row * A.ldx, A.ldx, t.rows, w, A.ldw, cols, A.in, y, A.ldy);
+    const int64_t rows = d.inside + d.outside, run = (rows * A.col_tiles + 7) / 8;
+    tile_products<T, S, true, BALONG, DMA>(A.ldx, A.ldw, A.ldy, [&](Work<T>& w) {
+        for (;; turn += A.groups >> 3) {
+            const int64_t at = die * run + turn;
+            if (turn >= run || at >= rows * A.col_tiles) return false;
+            const Place p = in_bands(at, rows, A.col_tiles);
+            const RaggedTile t = p.row < d.inside ? R.dense_tile(d, (int)p.row, S::BM)
+                                                  : R.outside_tile((int)p.row - d.inside, S::BM);
+            if (t.rows <= 0) continue;
+            const int64_t c0 = p.col * S::BN;
+            w.rows = t.rows;
+            w.cols = A.out - c0 < S::BN ? (int)(A.out - c0) : S::BN;
+            w.c = (T*)A.y + t.row * A.ldy + c0;
+            if (t.group < 0) {
+                zero_tile<S::BN, S::kThreads>(w.c, A.ldy, w.rows, w.cols);
+                continue;
+            }
+            w.a = (const T*)A.x + t.row * A.ldx;
+            w.b = (const T*)A.w + t.group * A.pitch_w + (BALONG ? c0 * A.ldw : c0);
+            w.k = A.in;
+            turn += A.groups >> 3;
+            return true;
+        }
+    });
 }
 
 template <class T, class S, bool DMA>
-__global__ __launch_bounds__(S::kThreads) void lx_experts_tile_grad(ExpertsArgs A)
+__global__ __launch_bounds__(S::kThreads, 2) void lx_experts_tile_grad(ExpertsArgs A)
 {
-    // Experts go round the dies, so that a die's are long and short ones;
-    // fewer than eight of them are cut into runs.
-    const int64_t each = A.row_tiles * A.col_tiles, id = group_id<S::kThreads>(), die = id & 7;
-    const int64_t whole = A.experts / 8 * 8 * each;
-    int64_t at;
-    if (id < whole) {
-        at = id >> 3;
-        at = (at / each * 8 + die) * each + at % each;
-    } else {
-        const int64_t left = A.experts * each - whole;
-        at = (id - whole) / 8 + die * ((left + 7) / 8);
-        if (at >= left || (id - whole) / 8 >= (left + 7) / 8) return;
-        at += whole;
-    }
-    const int64_t e = at / each;
-    const Place p = in_bands(at - e * each, A.row_tiles, A.col_tiles);
-    const int64_t m0 = p.row * S::BM, c0 = p.col * S::BN;
+    const int64_t each = A.row_tiles * A.col_tiles, run = (A.experts * each + 7) / 8;
+    const int64_t id = group_id<S::kThreads>(), die = id & 7;
+    int64_t turn = id >> 3;
     const Ragged R{A.offsets, A.experts, A.n, 0};
-    const int64_t first = uniform(R.bound(e + 1)), end = uniform(R.bound(e + 2));
-    tile_product<T, S, false, false, DMA>((const T*)A.y + first * A.ldy + m0, A.ldy, A.out - m0,
-                                          (const T*)A.x + first * A.ldx + c0, A.ldx, A.in - c0,
-                                          end > first ? end - first : 0,
-                                          (T*)A.dw + e * A.pitch_w + m0 * A.ldw + c0, A.ldw);
+    tile_products<T, S, false, false, DMA>(A.ldy, A.ldx, A.ldw, [&](Work<T>& w) {
+        for (;; turn += A.groups >> 3) {
+            const int64_t at = die * run + turn;
+            if (turn >= run || at >= A.experts * each) return false;
+            const int64_t e = at / each;
+            const Place p = in_bands(at - e * each, A.row_tiles, A.col_tiles);
+            const int64_t r0 = p.row * S::BM, c0 = p.col * S::BN;
+            const int64_t first = uniform(R.bound(e + 1)), end = uniform(R.bound(e + 2));
+            w.rows = A.out - r0 < S::BM ? (int)(A.out - r0) : S::BM;
+            w.cols = A.in - c0 < S::BN ? (int)(A.in - c0) : S::BN;
+            w.c = (T*)A.dw + e * A.pitch_w + r0 * A.ldw + c0;
+            if (end <= first) {  // no rows
+                zero_tile<S::BN, S::kThreads>(w.c, A.ldw, w.rows, w.cols);
+                continue;
+            }
+            w.a = (const T*)A.y + first * A.ldy + r0;
+            w.b = (const T*)A.x + first * A.ldx + c0;
+            w.k = end - first;
+            turn += A.groups >> 3;
+            return true;
+        }
+    });
+}
+
+// 8 neighbours from p on, of which `left` are there (0 past them).
+template <class T>
+__device__ __forceinline__ Pack<T, 8> load_some(const T* p, int64_t left)
+{
+    Pack<T, 8> r;
+    if (left >= 8) return load_pack<8>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = i < left ? p[i] : (T)0.f;
+    return r;
+}
+
+// ---- a few rows: the contraction in eight parts ----------------------------
+
+// 16 rows by 16 columns, each wave an eighth of the contraction, four steps of
+// it in flight, so that a call is little more than one way to memory.
+constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
+template <class T>
+__global__ __launch_bounds__(kFewThreads) void lx_experts_few(ExpertsArgs A)
+{
+    __shared__ f32x4 s_part[kFewWaves][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = group_id<kFewThreads>();
+    const int64_t unit = id / A.col_tiles, c0 = (id - unit * A.col_tiles) * 16;
+    const Ragged R{A.offsets, A.experts, A.n, 0};
+    if (unit >= R.units(16)) return;
+    const RaggedTile t = R.find(unit, 16);
+    if (t.rows <= 0) return;
+    const int64_t cols = A.out - c0 < 16 ? A.out - c0 : 16;
+    T* y = (T*)A.y + t.row * A.ldy + c0;
+    f32x4 sum = {};
+    if (t.group >= 0) {
+        const int l = lane & 15;
+        // rows and columns that are not there: the last ones' values, not stored
+        const T* x = (const T*)A.x + (t.row + (l < t.rows ? l : t.rows - 1)) * A.ldx;
+        const T* w = (const T*)A.w + t.group * A.pitch_w + (c0 + (l < cols ? l : cols - 1)) * A.ldw;
+        const int64_t steps = (A.in + 31) / 32, each = (steps + kFewWaves - 1) / kFewWaves;
+        const int64_t from = wave * each, to = from + each < steps ? from + each : steps;
+        for (int64_t s = from; s < to; s += 4) {
+            Frag<T> fx[4], fw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t k = (s + i) * 32 + 8 * (lane >> 4), left = s + i < to ? A.in - k : 0;
+                fw[i].v = __builtin_bit_cast(typename Frag<T>::V, load_some(w + k, left));
+                fx[i].v = __builtin_bit_cast(typename Frag<T>::V, load_some(x + k, left));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum = mma(fw[i], fx[i], sum);
+        }
+    }
+    s_part[wave][lane] = sum;
+    __syncthreads();
+    if (threadIdx.x < 256) {  // value r of lane l: row l % 16, column 4 (l / 16) + r
+        const int m = threadIdx.x >> 4, n = threadIdx.x & 15, l = m + 16 * (n >> 2);
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFewWaves; ++i) v += s_part[i][l][n & 3];
+        if (m < t.rows && n < cols) y[m * A.ldy + n] = (T)v;
+    }
+}
+
+template <class T>
+hipError_t few_go(ExpertsArgs a, hipStream_t s)
+{
+    a.col_tiles = (a.out + 15) / 16;
+    const int64_t groups = Ragged{a.offsets, a.experts, a.n, 0}.units(16) * a.col_tiles;
+    LX_LAUNCH("experts", s, (lx_experts_few<T><<<grid_of<kFewThreads>(groups), kFewThreads, 0, s>>>(a)));
+    return hipSuccess;
 }
 
 template <class T>
@@ -520,8 +645,8 @@ template <class T, class S>
 hipError_t tile_go(ExpertsArgs a, bool dma, hipStream_t s)
 {
     a.col_tiles = (a.out + S::BN - 1) / S::BN;
-    const int64_t groups = (Ragged{a.offsets, a.experts, a.n, 0}.units(S::BM) * a.col_tiles + 7) / 8 * 8;
-    const dim3 grid = grid_of<S::kThreads>(groups);
+    a.groups = S::groups((Ragged{a.offsets, a.experts, a.n, 0}.units(S::BM) * a.col_tiles + 7) / 8 * 8, a.in);
+    const dim3 grid = grid_of<S::kThreads>(a.groups);
     if (a.transpose) {
         if (dma)
             LX_LAUNCH("experts", s, (lx_experts_tile<T, S, false, true><<<grid, S::kThreads, 0, s>>>(a)));
@@ -541,7 +666,8 @@ hipError_t tile_grad_go(ExpertsArgs a, bool dma, hipStream_t s)
 {
     a.row_tiles = (a.out + S::BM - 1) / S::BM;
     a.col_tiles = (a.in + S::BN - 1) / S::BN;
-    const dim3 grid = grid_of<S::kThreads>((a.experts * a.row_tiles * a.col_tiles + 7) / 8 * 8);
+    a.groups = S::groups((a.experts * a.row_tiles * a.col_tiles + 7) / 8 * 8, a.n / a.experts);
+    const dim3 grid = grid_of<S::kThreads>(a.groups);
     if (dma)
         LX_LAUNCH("experts_grad", s, (lx_experts_tile_grad<T, S, true><<<grid, S::kThreads, 0, s>>>(a)));
     else
@@ -551,7 +677,16 @@ hipError_t tile_grad_go(ExpertsArgs a, bool dma, hipStream_t s)
 
 typedef Shape<256, 256, 2, 4> Large;
 typedef Shape<128, 128, 2, 2> Middle;
+typedef Shape<64, 64, 2, 2> Little;
 typedef Shape<16, 128, 1, 4> Small;
+
+// Tiles that a launch of shape S has work for, at most.
+template <class S>
+int64_t tiles_of(const ExpertsArgs& a)
+{
+    const int64_t rows = a.n / S::BM + (a.n < a.experts ? a.n : a.experts);
+    return rows * ((a.out + S::BN - 1) / S::BN);
+}
 
 template <class T>
 hipError_t tiles_go(const ExpertsArgs& a, hipStream_t s)
@@ -559,8 +694,12 @@ hipError_t tiles_go(const ExpertsArgs& a, hipStream_t s)
     const bool dma = a.in % 8 == 0 && (!a.transpose || a.out % 8 == 0) && lines16(a.x, a.ldx) && lines16(a.w, a.ldw) &&
                      a.pitch_w % 8 == 0;
     const int64_t each = a.n / a.experts;  // rows of an expert
-    if (each > 160) return tile_go<T, Large>(a, dma, s);
-    if (each > 16) return tile_go<T, Middle>(a, dma, s);
+    if (each > 16) {
+        if (each > 160 && tiles_of<Large>(a) >= 224) return tile_go<T, Large>(a, dma, s);
+        if (tiles_of<Middle>(a) >= 384) return tile_go<T, Middle>(a, dma, s);
+        return tile_go<T, Little>(a, dma, s);
+    }
+    if (!a.transpose && tiles_of<Small>(a) < 512) return few_go<T>(a, s);
     return tile_go<T, Small>(a, dma, s);
 }
 

@@ -486,7 +486,7 @@ struct ExpertsArgs {
     void* y = nullptr;                 // [n][out]; the gradient reads it
     int64_t ldy = 0;
     void* dw = nullptr;                // [experts][out][in], ldw and pitch_w
-    int64_t row_tiles = 0, col_tiles = 0;  // set at launch
+    int64_t row_tiles = 0, col_tiles = 0, groups = 0;  // set at launch
 };
 hipError_t experts_launch(const ExpertsArgs& a, int dtype, hipStream_t s);
 hipError_t experts_grad_launch(const ExpertsArgs& a, int dtype, hipStream_t s);
