@@ -310,8 +310,8 @@ struct Shape {
     // any time do better (gradient of 128 matrices of 1536 x 2048: 30 rows each
     // 289 us against 267, 200 rows 210 against 213).  Smaller shapes overlap
     // by themselves, and what staying costs in registers costs more.
-    static constexpr bool kStays = BM >= 256;
-    static int64_t groups(int64_t tiles, int64_t k) { return kStays && tiles > 256 && k >= 192 ? 256 : tiles; }
+    static constexpr bool kMayStay = BM >= 256;
+    static bool stays(int64_t tiles, int64_t k) { return kMayStay && tiles > 256 && k >= 192; }
     // A wave's place.  Waves w and w + 4 share a SIMD: of 2 x 4 waves they get
     // different halves both ways, so that half a tile keeps all SIMDs at work.
     static __device__ __forceinline__ int row_of(int w) { return WM == 2 && WN == 4 ? (w ^ (w >> 2)) & 1 : w / WN; }
@@ -332,7 +332,7 @@ struct Work {
 // too; a barrier a step.  The order within a step is fixed by hand: fragments
 // are read two ahead of the products that use them, loads go out among the
 // first products.
-template <class T, class S, bool AALONG, bool BALONG, bool DMA, class Next>
+template <class T, class S, bool AALONG, bool BALONG, bool DMA, bool STAYS, class Next>
 __device__ __forceinline__ void tile_products(int64_t lda, int64_t ldb, int64_t ldc, Next next_work)
 {
     typedef Lines<S::BM, AALONG> LA;
@@ -367,7 +367,7 @@ __device__ __forceinline__ void tile_products(int64_t lda, int64_t ldb, int64_t 
         const bool on = m0 < w.rows && n0 < w.cols;  // whether any of the wave's results are there
         f32x4 acc[TM][TN] = {};
         Work<T> then;
-        const bool goes_on = S::kStays && next_work(then);
+        const bool goes_on = STAYS && next_work(then);
         bool more = true;  // whether anything is loaded during a step
         for (int64_t k0 = 0; k0 < w.k; k0 += kK) {
             int64_t k1 = k0 + kK, k = w.k;  // the next step
@@ -482,7 +482,7 @@ __device__ __forceinline__ Place in_bands(int64_t at, int64_t rows, int64_t cols
 // Workgroups go round the eight dies in turn, so each die takes a run of
 // tiles, which share operands in its cache.  Where there are more tiles than
 // workgroups, a workgroup takes every gridDim-th.
-template <class T, class S, bool BALONG, bool DMA>
+template <class T, class S, bool BALONG, bool DMA, bool STAYS>
 __global__ __launch_bounds__(S::kThreads, 2) void lx_experts_tile(ExpertsArgs A)
 {
     const Ragged R{A.offsets, A.experts, A.n, 0};
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void lx_experts_tile(ExpertsArgs A)
     int64_t turn = id >> 3;
     const Ragged::Dense d = R.dense(S::BM);
     const int64_t rows = d.inside + d.outside, run = (rows * A.col_tiles + 7) / 8;
-    tile_products<T, S, true, BALONG, DMA>(A.ldx, A.ldw, A.ldy, [&](Work<T>& w) {
+    tile_products<T, S, true, BALONG, DMA, STAYS>(A.ldx, A.ldw, A.ldy, [&](Work<T>& w) {
         for (;; turn += A.groups >> 3) {
             const int64_t at = die * run + turn;
             if (turn >= run || at >= rows * A.col_tiles) return false;
@@ -515,14 +515,14 @@ __global__ __launch_bounds__(S::kThreads, 2) void lx_experts_tile(ExpertsArgs A)
     });
 }
 
-template <class T, class S, bool DMA>
+template <class T, class S, bool DMA, bool STAYS>
 __global__ __launch_bounds__(S::kThreads, 2) void lx_experts_tile_grad(ExpertsArgs A)
 {
     const int64_t each = A.row_tiles * A.col_tiles, run = (A.experts * each + 7) / 8;
     const int64_t id = group_id<S::kThreads>(), die = id & 7;
     int64_t turn = id >> 3;
     const Ragged R{A.offsets, A.experts, A.n, 0};
-    tile_products<T, S, false, false, DMA>(A.ldy, A.ldx, A.ldw, [&](Work<T>& w) {
+    tile_products<T, S, false, false, DMA, STAYS>(A.ldy, A.ldx, A.ldw, [&](Work<T>& w) {
         for (;; turn += A.groups >> 3) {
             const int64_t at = die * run + turn;
             if (turn >= run || at >= A.experts * each) return false;
@@ -641,38 +641,52 @@ hipError_t any_grad_go(ExpertsArgs a, hipStream_t s)
 
 bool lines16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0 && ld <= 1 << 22; }
 
-template <class T, class S>
-hipError_t tile_go(ExpertsArgs a, bool dma, hipStream_t s)
+template <class T, class S, bool BALONG, bool DMA>
+hipError_t tile_layout_go(ExpertsArgs a, hipStream_t s)
 {
     a.col_tiles = (a.out + S::BN - 1) / S::BN;
-    a.groups = S::groups((Ragged{a.offsets, a.experts, a.n, 0}.units(S::BM) * a.col_tiles + 7) / 8 * 8, a.in);
-    const dim3 grid = grid_of<S::kThreads>(a.groups);
-    if (a.transpose) {
-        if (dma)
-            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, false, true><<<grid, S::kThreads, 0, s>>>(a)));
-        else
-            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, false, false><<<grid, S::kThreads, 0, s>>>(a)));
-    } else {
-        if (dma)
-            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, true, true><<<grid, S::kThreads, 0, s>>>(a)));
-        else
-            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, true, false><<<grid, S::kThreads, 0, s>>>(a)));
+    a.groups = (Ragged{a.offsets, a.experts, a.n, 0}.units(S::BM) * a.col_tiles + 7) / 8 * 8;
+    if constexpr (S::kMayStay && DMA) {
+        if (S::stays(a.groups, a.in)) {
+            a.groups = 256;
+            LX_LAUNCH("experts", s, (lx_experts_tile<T, S, BALONG, DMA, true><<<256, S::kThreads, 0, s>>>(a)));
+            return hipSuccess;
+        }
     }
+    LX_LAUNCH("experts", s,
+              (lx_experts_tile<T, S, BALONG, DMA, false><<<grid_of<S::kThreads>(a.groups), S::kThreads, 0, s>>>(a)));
     return hipSuccess;
 }
 
 template <class T, class S>
-hipError_t tile_grad_go(ExpertsArgs a, bool dma, hipStream_t s)
+hipError_t tile_go(const ExpertsArgs& a, bool dma, hipStream_t s)
+{
+    if (a.transpose) return dma ? tile_layout_go<T, S, false, true>(a, s) : tile_layout_go<T, S, false, false>(a, s);
+    return dma ? tile_layout_go<T, S, true, true>(a, s) : tile_layout_go<T, S, true, false>(a, s);
+}
+
+template <class T, class S, bool DMA>
+hipError_t tile_grad_layout_go(ExpertsArgs a, hipStream_t s)
 {
     a.row_tiles = (a.out + S::BM - 1) / S::BM;
     a.col_tiles = (a.in + S::BN - 1) / S::BN;
-    a.groups = S::groups((a.experts * a.row_tiles * a.col_tiles + 7) / 8 * 8, a.n / a.experts);
-    const dim3 grid = grid_of<S::kThreads>(a.groups);
-    if (dma)
-        LX_LAUNCH("experts_grad", s, (lx_experts_tile_grad<T, S, true><<<grid, S::kThreads, 0, s>>>(a)));
-    else
-        LX_LAUNCH("experts_grad", s, (lx_experts_tile_grad<T, S, false><<<grid, S::kThreads, 0, s>>>(a)));
+    a.groups = (a.experts * a.row_tiles * a.col_tiles + 7) / 8 * 8;
+    if constexpr (S::kMayStay && DMA) {
+        if (S::stays(a.groups, a.n / a.experts)) {
+            a.groups = 256;
+            LX_LAUNCH("experts_grad", s, (lx_experts_tile_grad<T, S, DMA, true><<<256, S::kThreads, 0, s>>>(a)));
+            return hipSuccess;
+        }
+    }
+    LX_LAUNCH("experts_grad", s,
+              (lx_experts_tile_grad<T, S, DMA, false><<<grid_of<S::kThreads>(a.groups), S::kThreads, 0, s>>>(a)));
     return hipSuccess;
+}
+
+template <class T, class S>
+hipError_t tile_grad_go(const ExpertsArgs& a, bool dma, hipStream_t s)
+{
+    return dma ? tile_grad_layout_go<T, S, true>(a, s) : tile_grad_layout_go<T, S, false>(a, s);
 }
 
 typedef Shape<256, 256, 2, 4> Large;
