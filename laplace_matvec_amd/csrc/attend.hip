@@ -25,21 +25,21 @@ enum SweepMode { kEnd, kOut, kStore };
 
 // REV runs the segments backwards with queries and output gradients in place
 // of keys and values: the gradient of the states.
-template <class T, class TG, int DK, int MODE, bool REV>
-__global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
+template <class T, class TG, int DK, int DV, int MODE, bool REV>
+__global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof(typename Compute<T>::E) == 4 ? 1 : 2) void lx_attend_sweep(AttendArgs A)
 {
     typedef typename Compute<T>::E E;
-    constexpr int N = MODE == kOut ? Compute<T>::kTerms : 1;
     constexpr int NU = Compute<T>::kTerms;  // terms of a row times its decay
-    constexpr int PK = DK + kPad<E>, PV = kDV + kPad<E>;
+    constexpr int TB = DV / 16;
+    constexpr int PK = DK + kPad<E>, PV = DV + kPad<E>;
     constexpr int TA = DK / 64;  // 16-row tiles of the state per wave
     __shared__ alignas(16) E s_k[kC * PK];
     __shared__ alignas(16) E s_v[kC * PV];
-    __shared__ alignas(16) E s_s[MODE == kOut ? N * kDV * PK : 1];
+    __shared__ alignas(16) E s_s[MODE == kOut ? DV * PK : 1];
     __shared__ alignas(16) Decays s_d;
     __shared__ alignas(16) float s_f[kC];
     __shared__ int s_odd[4];
-    __shared__ unsigned long long s_rows[kDV];
+    __shared__ unsigned long long s_rows[DV];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g4 = 4 * (lane >> 4), l16 = lane & 15;
@@ -52,13 +52,13 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
     if (unit >= R.units(A.segment)) return;
     const RaggedTile t = R.find(unit, A.segment);
     if (t.rows <= 0) return;
-    const int k0 = kb * DK, v0 = vb * kDV;
+    const int k0 = kb * DK, v0 = vb * DV;
     const int kcols = A.dk - k0, vcols = A.dv - v0;  // how many are there
     if (t.group < 0) {
         if (MODE != kOut) return;
-        for (int i = threadIdx.x; i < t.rows * kDV; i += kAttendThreads) {
-            const int64_t row = t.row + i / kDV;
-            const int c = i % kDV;
+        for (int i = threadIdx.x; i < t.rows * DV; i += kAttendThreads) {
+            const int64_t row = t.row + i / DV;
+            const int c = i % DV;
             if (c >= vcols) continue;
             if (A.part)
                 A.part[(kb * A.n + row) * ((int64_t)A.heads * A.dv) + h * A.dv + v0 + c] = 0.f;
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
     if (MODE == kEnd && (REV ? is_first : is_last)) return;
 
     // the state: rows dk 16 (wave TA + a) + g4 + r, columns 16 b + l16
-    f32x4 acc[TA][4];
+    f32x4 acc[TA][TB];
     // slot i of a sequence: the state between its segments i and i + 1 (the
     // gradient there); before and past the sequence they are the edges
     const int64_t slot = t.first / A.segment + t.index + (MODE == kEnd ? 0 : -1) + (REV ? (MODE == kEnd ? -1 : 1) : 0);
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
 #pragma unroll
     for (int a = 0; a < TA; ++a)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < TB; ++b)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = 16 * (wave * TA + a) + g4 + r, col = 16 * b + l16;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
 
     const int chunks = (t.rows + kC - 1) / kC;
     RowTile<T, DK> tk;
-    RowTile<T, kDV> tv;
+    RowTile<T, DV> tv;
     Pack<T, 8> tq[DK / 32];
     float tg = 0.f;
     auto fetch = [&](int ci) {
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
         tk.put(s_k);
         tv.put(s_v);
         {
-            const bool odd = __any(tv.template odd<E>());
+            const bool odd = __any(tv.odd());
             if (lane == 0) s_odd[wave] = odd;
         }
         Frag<E> fq[DK / 32];
@@ -145,18 +145,11 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
 #pragma unroll
             for (int a = 0; a < TA; ++a)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    V4 w[N];
+                for (int b = 0; b < TB; ++b) {
+                    V4 w;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        E e[N];
-                        split<E, N>(acc[a][b][r], e);
-#pragma unroll
-                        for (int m = 0; m < N; ++m) w[m][r] = e[m];
-                    }
-#pragma unroll
-                    for (int m = 0; m < N; ++m)
-                        *reinterpret_cast<V4*>(&s_s[(m * kDV + 16 * b + l16) * PK + 16 * (wave * TA + a) + g4]) = w[m];
+                    for (int r = 0; r < 4; ++r) w[r] = (E)acc[a][b][r];
+                    *reinterpret_cast<V4*>(&s_s[(16 * b + l16) * PK + 16 * (wave * TA + a) + g4]) = w;
                 }
         }
         __syncthreads();
@@ -165,12 +158,12 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
         // does see it gets NaN.
         const bool odd = (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0;
         if (odd) {
-            if (threadIdx.x < kDV) s_rows[threadIdx.x] = 0;
+            if (threadIdx.x < DV) s_rows[threadIdx.x] = 0;
             __syncthreads();
-            for (int i = threadIdx.x; i < kC * kDV; i += kAttendThreads) {
-                E* p = s_v + i / kDV * PV + i % kDV;
+            for (int i = threadIdx.x; i < kC * DV; i += kAttendThreads) {
+                E* p = s_v + i / DV * PV + i % DV;
                 if (!finite(*p)) {
-                    atomicOr(&s_rows[i % kDV], 1ull << (i / kDV));
+                    atomicOr(&s_rows[i % DV], 1ull << (i / DV));
                     *p = (E)0.f;
                 }
             }
@@ -187,7 +180,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
 #pragma unroll
                 for (int a = 0; a < TA; ++a)
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
+                    for (int b = 0; b < TB; ++b)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             to[(int64_t)(16 * (wave * TA + a) + g4 + r) * A.dvp + 16 * b + l16] = acc[a][b][r];
@@ -219,13 +212,11 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
             }
             const f32x4 into = *reinterpret_cast<const f32x4*>(&s_d.into[16 * wave + g4]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < TB; ++b) {
                 f32x4 o = {};
 #pragma unroll
                 for (int kk = 0; kk < DK / 32; ++kk)
-#pragma unroll
-                    for (int m = 0; m < N; ++m)
-                        o = mma(fq[kk], frag_along(s_s + (m * kDV + 16 * b + l16) * PK + 32 * kk + 2 * g4), o);
+                    o = mma(fq[kk], frag_along(s_s + (16 * b + l16) * PK + 32 * kk + 2 * g4), o);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[r] = into[r] == 0.f ? 0.f : o[r] * (into[r] * A.scale);
 #pragma unroll
@@ -256,14 +247,14 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
 #pragma unroll
         for (int a = 0; a < TA; ++a)
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < TB; ++b)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[a][b][r] = whole == 0.f ? 0.f : whole * acc[a][b][r];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            Frag<E> fv[4];
+            Frag<E> fv[TB];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) fv[b] = frag_across(s_v + 32 * s * PV + 16 * b, PV);
+            for (int b = 0; b < TB; ++b) fv[b] = frag_across(s_v + 32 * s * PV + 16 * b, PV);
             const f32x4 f0 = *reinterpret_cast<const f32x4*>(&s_f[32 * s + g4]);
             const f32x4 f1 = *reinterpret_cast<const f32x4*>(&s_f[32 * s + 16 + g4]);
 #pragma unroll
@@ -279,7 +270,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
                     for (int m = 0; m < NU; ++m) fs[m].v[i] = e[m];
                 }
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int b = 0; b < TB; ++b)
 #pragma unroll
                     for (int m = 0; m < NU; ++m) acc[a][b] = mma(fs[m], fv[b], acc[a][b]);
             }
@@ -288,7 +279,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
             const int from = s_d.last[kC - 1];
             const unsigned long long seen = REV ? s_d.sees_before() : 0ull - (1ull << (from < 0 ? 0 : from));
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < TB; ++b)
                 if (s_rows[16 * b + l16] & seen)
 #pragma unroll
                     for (int a = 0; a < TA; ++a) acc[a][b] = f32x4{} + __builtin_nanf("");
@@ -302,7 +293,7 @@ __global__ __launch_bounds__(kAttendThreads) void lx_attend_sweep(AttendArgs A)
 #pragma unroll
         for (int a = 0; a < TA; ++a)
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int b = 0; b < TB; ++b)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int rr = 16 * (wave * TA + a) + g4 + r, col = 16 * b + l16;
@@ -346,9 +337,10 @@ __global__ __launch_bounds__(256) void lx_attend_empty(AttendArgs A, const float
 {
     const Ragged R{A.offsets, A.seqs, A.n, A.seq_len};
     const int64_t size = (int64_t)A.heads * A.dk * A.dv;
-    for (int64_t q = blockIdx.x; q < A.seqs; q += gridDim.x) {
+    for (int64_t q = blockIdx.y; q < A.seqs; q += gridDim.y) {
         if (R.bound(q + 2) > R.bound(q + 1)) continue;
-        for (int64_t i = threadIdx.x; i < size; i += 256) to[q * size + i] = from ? from[q * size + i] : 0.f;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256)
+            to[q * size + i] = from ? from[q * size + i] : 0.f;
     }
 }
 
@@ -422,10 +414,18 @@ __global__ __launch_bounds__(256) void lx_attend_step(AttendStepArgs A)
 }
 
 template <class T, class TG, int DK, int MODE, bool REV>
-hipError_t sweep_go(const AttendArgs& a, const char* label, hipStream_t s)
+hipError_t sweep_go(AttendArgs a, const char* label, hipStream_t s)
 {
+    if constexpr (sizeof(typename Compute<T>::E) == 2) {
+        if (a.nvb % 2 == 0) {
+            a.nvb /= 2;
+            const int64_t groups = Ragged{a.offsets, a.seqs, a.n, a.seq_len}.units(a.segment) * a.heads * a.nkb * a.nvb;
+            LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, 128, MODE, REV><<<grid_of<kAttendThreads>(groups), kAttendThreads, 0, s>>>(a)));
+            return hipSuccess;
+        }
+    }
     const int64_t groups = Ragged{a.offsets, a.seqs, a.n, a.seq_len}.units(a.segment) * a.heads * a.nkb * a.nvb;
-    LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, MODE, REV><<<grid_of<kAttendThreads>(groups), kAttendThreads, 0, s>>>(a)));
+    LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, 64, MODE, REV><<<grid_of<kAttendThreads>(groups), kAttendThreads, 0, s>>>(a)));
     return hipSuccess;
 }
 
@@ -441,8 +441,9 @@ hipError_t scan_go(const AttendArgs& a, hipStream_t s)
 hipError_t empty_go(const AttendArgs& a, const float* from, float* to, hipStream_t s)
 {
     if (!to || (!a.offsets && a.n > 0)) return hipSuccess;
-    const unsigned seqs = (unsigned)(a.seqs < 4096 ? a.seqs : 4096);
-    LX_LAUNCH("attend_empty", s, (lx_attend_empty<<<seqs, 256, 0, s>>>(a, from, to)));
+    const int64_t size = ((int64_t)a.heads * a.dk * a.dv + 1023) / 1024;
+    const dim3 grid((unsigned)(size < 256 ? size : 256), (unsigned)(a.seqs < 1024 ? a.seqs : 1024));
+    LX_LAUNCH("attend_empty", s, (lx_attend_empty<<<grid, 256, 0, s>>>(a, from, to)));
     return hipSuccess;
 }
 

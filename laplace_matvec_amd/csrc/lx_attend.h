@@ -9,7 +9,6 @@ namespace lx {
 
 constexpr int kAttendThreads = 256;
 constexpr int kC = kAttendChunk;  // rows of a chunk: one per lane
-constexpr int kDV = 64;           // columns of a state block in a sweep
 
 // What products are made in for storage type T: bfloat16 rows as they are,
 // other types as float32 (float16's range is too small for states and
@@ -82,16 +81,22 @@ struct RowTile {
             r[j] = load8(p + row * ld + col, row < rows ? cols - col : 0);
         }
     }
-    // whether any of the values is inf or NaN as an E
-    template <class E>
+    // Whether any of the values is inf or NaN: its exponent is all ones, and
+    // one more carries into the sign.
     __device__ __forceinline__ bool odd() const
     {
-        bool any = false;
+        constexpr uint32_t kExp = sizeof(T) == 4 ? 0x7F800000u : sizeof(T) == 2 && __is_same(T, f16_t) ? 0x7C007C00u : 0x7F807F80u;
+        constexpr uint32_t kOne = sizeof(T) == 4 ? 0x00800000u : __is_same(T, f16_t) ? 0x04000400u : 0x00800080u;
+        constexpr uint32_t kSign = sizeof(T) == 4 ? 0x80000000u : 0x80008000u;
+        uint32_t any = 0;
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j)
+        for (int j = 0; j < kVecs; ++j) {
+            typedef uint32_t Bits __attribute__((ext_vector_type(2 * sizeof(T))));
+            const Bits w = __builtin_bit_cast(Bits, r[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) any |= !finite((E)r[j].v[i]);
-        return any;
+            for (int i = 0; i < 2 * (int)sizeof(T); ++i) any |= (w[i] & kExp) + kOne;
+        }
+        return any & kSign;
     }
     template <class E>
     __device__ __forceinline__ void put(E* s) const
@@ -121,11 +126,12 @@ struct Decays {
         const bool cut = g < -103.972f;  // e^g < 2^-150
         const uint64_t cuts = __ballot(cut);
         double sum = cut ? 0.0 : (double)g * 1.4426950408889634074;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const double below = __shfl_up(sum, d);
-            if (lane >= d) sum += below;
-        }
+        sum += dpp_move<0x111>(sum, 0.0);
+        sum += dpp_move<0x112>(sum, 0.0);
+        sum += dpp_move<0x114>(sum, 0.0);
+        sum += dpp_move<0x118>(sum, 0.0);
+        sum += dpp_move<0x142, 0xA>(sum, 0.0);
+        sum += dpp_move<0x143, 0xC>(sum, 0.0);
         const double total = __shfl(sum, 63);
         const uint64_t mine = cuts & ((2ull << lane) - 1);
         hi[lane] = (float)sum;
