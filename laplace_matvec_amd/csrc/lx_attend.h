@@ -66,9 +66,9 @@ __device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uin
 __device__ __forceinline__ bool finite(bf16_t x) { return (__builtin_bit_cast(uint16_t, x) & 0x7F80u) != 0x7F80u; }
 
 // A tile of kC rows x W columns on its way from memory to LDS.
-template <class T, int W>
+template <class T, int W, int THREADS = kAttendThreads>
 struct RowTile {
-    static constexpr int kVecs = kC * W / 8 / kAttendThreads;
+    static constexpr int kVecs = kC * W / 8 / THREADS;
     Pack<T, 8> r[kVecs];
 
     // p: first row and column; rows and cols: how many are there
@@ -76,7 +76,7 @@ struct RowTile {
     {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int i = (int)threadIdx.x + j * kAttendThreads;
+            const int i = (int)threadIdx.x + j * THREADS;
             const int row = i / (W / 8), col = i % (W / 8) * 8;
             r[j] = load8(p + row * ld + col, row < rows ? cols - col : 0);
         }
@@ -104,7 +104,7 @@ struct RowTile {
         constexpr int kPitch = W + kPad<E>;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int i = (int)threadIdx.x + j * kAttendThreads;
+            const int i = (int)threadIdx.x + j * THREADS;
             put8(s + i / (W / 8) * kPitch + i % (W / 8) * 8, r[j]);
         }
     }
