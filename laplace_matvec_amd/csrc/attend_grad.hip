@@ -37,6 +37,62 @@ __device__ __forceinline__ float sum16(float x)
     return x;
 }
 
+// Sums up to each lane.
+__device__ __forceinline__ float scan_up(float x)
+{
+#define LX_DPP(ctrl, rows) __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, rows, 0xF, false))
+    x += LX_DPP(0x111, 0xF);
+    x += LX_DPP(0x112, 0xF);
+    x += LX_DPP(0x114, 0xF);
+    x += LX_DPP(0x118, 0xF);
+    x += LX_DPP(0x142, 0xA);
+    x += LX_DPP(0x143, 0xC);
+#undef LX_DPP
+    return x;
+}
+
+// Rows of a result, or of a plane of partial sums (float32) where `sums` is there.
+template <class T>
+struct Out {
+    float* sums;
+    T* to;
+    int64_t ld;
+    __device__ __forceinline__ void put(int row, int col, float x) const
+    {
+        if (sums)
+            sums[row * ld + col] = x;
+        else
+            to[row * ld + col] = (T)x;
+    }
+    // x[c][r]: rows row0 + r, columns 16 c + col0, as far as they are there
+    template <int C>
+    __device__ __forceinline__ void put_tiles(int row0, int col0, int rows, int cols, const f32x4 (&x)[C]) const
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (row0 + r >= rows) continue;
+            if (sums) {
+                float* p = sums + (row0 + r) * ld + col0;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (16 * c + col0 < cols) p[16 * c] = x[c][r];
+            } else {
+                T* p = to + (row0 + r) * ld + col0;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (16 * c + col0 < cols) p[16 * c] = (T)x[c][r];
+            }
+        }
+    }
+};
+template <class T>
+__device__ __forceinline__ Out<T> out_rows(void* to, int64_t ld, float* sums, int64_t plane, int64_t n, int width,
+                                           int64_t row, int col)
+{
+    if (sums) return {sums + (plane * n + row) * width + col, nullptr, width};
+    return {nullptr, (T*)to + row * ld + col, ld};
+}
+
 // Waves 0 to 3 make the rows' side (scores, dq), waves 4 to 7 the columns'
 // (dk, dv), sixteen rows of the chunk each; wave w and w + 4 share a SIMD, so
 // each has one of either.  What the next head needs is on its way meanwhile.
@@ -75,41 +131,23 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     const int k0 = kb * DK, kcols = A.dk - k0;
     const int rq = A.heads / A.hq, rk = A.heads / A.hk, rv = A.heads / A.hv;
     const int nvb = A.dvp / DV;
-    // where results go: the arrays, or planes of partial sums
-    auto put = [](float x, float* p, int64_t ldp, void* to, int64_t at, int64_t ld, int row, int col) {
-        if (p)
-            p[row * ldp + col] = x;
-        else
-            ((T*)to)[at + row * ld + col] = (T)x;
-    };
-    auto put_q = [&](float x, int row, int col) {
-        float* p = A.part_q ? A.part_q + (h0 % rq / A.loop * A.n + t.row) * ((int64_t)A.hq * A.dk) + h0 / rq * A.dk + k0 : nullptr;
-        put(x, p, (int64_t)A.hq * A.dk, A.dq, t.row * A.lddq + h0 / rq * A.dk + k0, A.lddq, row, col);
-    };
-    auto put_k = [&](float x, int row, int col) {
-        float* p = A.part_k ? A.part_k + (h0 % rk / A.loop * A.n + t.row) * ((int64_t)A.hk * A.dk) + h0 / rk * A.dk + k0 : nullptr;
-        put(x, p, (int64_t)A.hk * A.dk, A.dkey, t.row * A.lddk + h0 / rk * A.dk + k0, A.lddk, row, col);
-    };
-    auto put_v = [&](float x, int h, int row, int col) {
-        float* p = A.part_v ? A.part_v + ((int64_t)(h % rv * A.nkb + kb) * A.n + t.row) * ((int64_t)A.hv * A.dv) + h / rv * A.dv : nullptr;
-        put(x, p, (int64_t)A.hv * A.dv, A.dval, t.row * A.lddv + h / rv * A.dv, A.lddv, row, col);
-    };
-    auto put_g = [&](float x, int h, int row) {
-        if (A.part_g)
-            A.part_g[(kb * A.n + t.row + row) * (int64_t)A.heads + h] = x;
-        else
-            ((TG*)A.dg)[(t.row + row) * A.lddg + h] = (TG)x;
-    };
+    // This chunk's rows of the results: of the arrays, or of planes of partial
+    // sums where several workgroups add to one row.
+    const int hq0 = h0 / rq, hk0 = h0 / rk, hv0 = h0 / rv;
+    const Out<T> oq = out_rows<T>(A.dq, A.lddq, A.part_q, h0 % rq / A.loop, A.n, A.hq * A.dk, t.row, hq0 * A.dk + k0);
+    const Out<T> ok = out_rows<T>(A.dkey, A.lddk, A.part_k, h0 % rk / A.loop, A.n, A.hk * A.dk, t.row, hk0 * A.dk + k0);
+    const Out<TG> og = out_rows<TG>(A.dg, A.lddg, A.part_g, kb, A.n, A.heads, t.row, h0);
     if (t.group < 0) {
         for (int i = threadIdx.x; i < rows * DK; i += kGradThreads) {
             if (i % DK >= kcols) continue;
-            if (A.dq) put_q(0.f, i / DK, i % DK);
-            if (A.dkey) put_k(0.f, i / DK, i % DK);
+            if (A.dq) oq.put(i / DK, i % DK, 0.f);
+            if (A.dkey) ok.put(i / DK, i % DK, 0.f);
         }
         for (int h = h0; h < h0 + A.loop; ++h) {
+            const Out<T> ov = out_rows<T>(A.dval, A.lddv, A.part_v, h % rv * A.nkb + kb, A.n, A.hv * A.dv, t.row, h / rv * A.dv);
             if (A.dval)
-                for (int i = threadIdx.x; i < rows * A.dv; i += kGradThreads) put_v(0.f, h, i / A.dv, i % A.dv);
-            if (A.dg && (int)threadIdx.x < rows) put_g(0.f, h, threadIdx.x);
+                for (int i = threadIdx.x; i < rows * A.dv; i += kGradThreads) ov.put(i / A.dv, i % A.dv, 0.f);
+            if (A.dg && (int)threadIdx.x < rows) og.put(threadIdx.x, h - h0, 0.f);
         }
         return;
     }
@@ -118,32 +156,44 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     // of the sequence, or a slot between chunks.
     const bool is_first = t.index == 0, is_last = t.row + t.rows == t.end;
     const int64_t slot = t.first / kC + t.index;
-    auto four = [&](const float* edges, const float* slots, bool edge, int64_t at_slot, int h, int v0, int row, int col) {
-        f32x4 x = {};
+    const int64_t size = (int64_t)A.dkp * A.dvp;
+    const float* slot_s = A.chunk_states + ((slot - 1) * A.heads + h0) * size + (int64_t)k0 * A.dvp;
+    const float* slot_t = A.chunk_grads + (slot * A.heads + h0) * size + (int64_t)k0 * A.dvp;
+    const int64_t edge_at = ((t.group * A.heads + h0) * A.dk + k0) * (int64_t)A.dv;
+    const int at0 = threadIdx.x / (DV / 4), col0 = threadIdx.x % (DV / 4) * 4;  // of a thread's values of a state
+    constexpr int kStep = kGradThreads / (DV / 4);                             // rows to its next ones
+    auto state_in = [&](f32x4 (&x)[NS], bool edge, const float* slots, const float* edges, int hl, int v0) {
         if (!edge) {
-            x = *reinterpret_cast<const f32x4*>(slots + ((at_slot * A.heads + h) * A.dkp + k0 + row) * A.dvp + v0 + col);
-        } else if (edges && row < kcols) {
-            const float* p = edges + ((t.group * A.heads + h) * A.dk + k0 + row) * (int64_t)A.dv + v0 + col;
+            const float* p = slots + hl * size + v0 + (int64_t)at0 * A.dvp + col0;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (v0 + col + r < A.dv) x[r] = p[r];
+            for (int u = 0; u < NS; ++u) x[u] = *reinterpret_cast<const f32x4*>(p + u * kStep * A.dvp);
+        } else {
+            const float* p = edges ? edges + edge_at + hl * ((int64_t)A.dk * A.dv) + v0 + col0 : nullptr;
+            const int cols = A.dv - v0 - col0;
+#pragma unroll
+            for (int u = 0; u < NS; ++u) {
+                x[u] = f32x4{};
+                const int row = at0 + u * kStep;
+                if (p && row < kcols)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (r < cols) x[u][r] = p[(int64_t)row * A.dv + r];
+            }
         }
-        return x;
     };
     RowTile<T, DV, kGradThreads> tv, td;
     f32x4 ts[NS], tt[NS];
     float tg = 0.f;
-    auto fetch = [&](int h, int vb) {
+    const T* vp = (const T*)A.v + t.row * A.ldv;
+    const T* dp = (const T*)A.dy + t.row * A.lddy + (int64_t)h0 * A.dv;
+    const TG* gp = (const TG*)A.g + (t.row + lane) * A.ldg + h0;
+    auto fetch = [&](int hl, int hv, int vb) {
         const int v0 = vb * DV, vcols = A.dv - v0;
-        tv.load((const T*)A.v + t.row * A.ldv + h / rv * A.dv + v0, A.ldv, rows, vcols);
-        td.load((const T*)A.dy + t.row * A.lddy + (int64_t)h * A.dv + v0, A.lddy, rows, vcols);
-#pragma unroll
-        for (int u = 0; u < NS; ++u) {
-            const int at = (int)threadIdx.x + u * kGradThreads, row = at / (DV / 4), col = at % (DV / 4) * 4;
-            ts[u] = four(A.h0, A.chunk_states, is_first, slot - 1, h, v0, row, col);
-            tt[u] = four(A.dfinal, A.chunk_grads, is_last, slot, h, v0, row, col);
-        }
-        if (wave == 0) tg = lane < rows ? (float)((const TG*)A.g)[(t.row + lane) * A.ldg + h] : 0.f;
+        tv.load(vp + hv * A.dv + v0, A.ldv, rows, vcols);
+        td.load(dp + hl * A.dv + v0, A.lddy, rows, vcols);
+        state_in(ts, is_first, slot_s, A.h0, hl, v0);
+        state_in(tt, is_last, slot_t, A.dfinal, hl, v0);
+        if (wave == 0) tg = lane < rows ? (float)gp[hl] : 0.f;
     };
     auto put_state = [&](const f32x4& x, E* s, int row, int col) {
         V4 w[N];
@@ -159,9 +209,9 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     };
     {
         RowTile<T, DK, kGradThreads> a, b;
-        a.load((const T*)A.q + t.row * A.ldq + h0 / rq * A.dk + k0, A.ldq, rows, kcols);
-        b.load((const T*)A.k + t.row * A.ldk + h0 / rk * A.dk + k0, A.ldk, rows, kcols);
-        fetch(h0, 0);
+        a.load((const T*)A.q + t.row * A.ldq + hq0 * A.dk + k0, A.ldq, rows, kcols);
+        b.load((const T*)A.k + t.row * A.ldk + hk0 * A.dk + k0, A.ldk, rows, kcols);
+        fetch(0, hv0, 0);
         a.put(s_q);
         b.put(s_k);
     }
@@ -181,18 +231,20 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     // dq, or dk: rows w16 + g4 + r, columns 16 c + l16
     f32x4 acc[DK / 16] = {};
     float dg = 0.f;  // wave 0: row `lane`
-    int flip = 0;
-    for (int it = 0; it < A.loop * nvb; ++it, flip ^= 1) {
-        const int h = h0 + it / nvb, vb = it % nvb;
+    int flip = 0, vb = 0, hl = 0;  // block of columns; head, from h0 on
+    int hv = hv0, in_hv = h0 - hv0 * rv;  // the value head, and which of those that share it
+    for (;; flip ^= 1) {
         const int v0 = vb * DV, vcols = A.dv - v0;
+        const bool ends_head = vb + 1 == nvb;
+        const bool more = !(ends_head && hl + 1 == A.loop);
+        const int next_hv = ends_head && in_hv + 1 == rv ? hv + 1 : hv;
         tv.put(s_v);
         td.put(s_do);
         float z = 0.f;
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
-            const int at = (int)threadIdx.x + u * kGradThreads, row = at / (DV / 4), col = at % (DV / 4) * 4;
-            put_state(ts[u], s_s, row, col);
-            put_state(tt[u], s_t, row, col);
+            put_state(ts[u], s_s, at0 + u * kStep, col0);
+            put_state(tt[u], s_t, at0 + u * kStep, col0);
 #pragma unroll
             for (int r = 0; r < 4; ++r) z += ts[u][r] * tt[u][r];
         }
@@ -202,7 +254,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         if (lane == 0) s_z[flip][wave] = z;
         if (wave == 0 && vb == 0) s_d.make(tg);
         __syncthreads();
-        if (it + 1 < A.loop * nvb) fetch(h0 + (it + 1) / nvb, (it + 1) % nvb);
+        if (more) fetch(ends_head ? hl + 1 : hl, next_hv, ends_head ? 0 : vb + 1);
 
         Frag<E> fe[2];
         f32x4 dv[DV / 16];
@@ -334,13 +386,9 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
 #pragma unroll
                     for (int b = 0; b < DV / 16; ++b) dv[b] = mma(f, frag_across(s_do + 32 * s * PV + 16 * b, PV), dv[b]);
                 }
-#pragma unroll
-                for (int b = 0; b < DV / 16; ++b) {
-                    const int col = 16 * b + l16;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (w16 + g4 + r < rows && col < vcols) put_v(dv[b][r], h, w16 + g4 + r, v0 + col);
-                }
+                const Out<T> ov = out_rows<T>(A.dval, A.lddv, A.part_v, in_hv * A.nkb + kb, A.n, A.hv * A.dv, t.row,
+                                              hv * A.dv + v0);
+                ov.template put_tiles<DV / 16>(w16 + g4, l16, rows, vcols, dv);
             }
         }
         __syncthreads();
@@ -348,12 +396,8 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
             float from = s_row[lane] - ((s_col[0][lane] + s_col[1][lane]) + (s_col[2][lane] + s_col[3][lane]));
             float to = s_b[lane];
             const float own = to;
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const float above = __shfl_down(from, d), below = __shfl_up(to, d);
-                if (lane + d < 64) from += above;
-                if (lane >= d) to += below;
-            }
+            to = scan_up(to);
+            from = __shfl(scan_up(__shfl(from, 63 - lane)), 63 - lane);  // from each row on
             float z = 0.f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) z += s_z[flip][w];
@@ -361,21 +405,20 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
             const float through = whole == 0.f ? 0.f : whole * z;
             // the last cut up to a row is the row itself: its decay has no gradient
             dg = (vb ? dg : 0.f) + (s_d.last[lane] == lane ? 0.f : from + (to - own) + through);
-            if (A.dg && vb + 1 == nvb && lane < rows) put_g(dg, h, lane);
+            if (A.dg && ends_head && lane < rows) og.put(lane, hl, dg);
+        }
+        if (!more) break;
+        if (ends_head) {
+            vb = 0;
+            ++hl;
+            in_hv = next_hv == hv ? in_hv + 1 : 0;
+            hv = next_hv;
+        } else {
+            ++vb;
         }
     }
-#pragma unroll
-    for (int c = 0; c < DK / 16; ++c) {
-        const int col = 16 * c + l16;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = w16 + g4 + r;
-            if (row < rows && col < kcols) {
-                if (side == 0 && A.dq) put_q(acc[c][r], row, col);
-                if (side == 1 && A.dkey) put_k(acc[c][r], row, col);
-            }
-        }
-    }
+    if (side == 0 ? A.dq != nullptr : A.dkey != nullptr)
+        (side == 0 ? oq : ok).template put_tiles<DK / 16>(w16 + g4, l16, rows, kcols, acc);
 }
 
 template <class T, class TG, int DK, int DV>
