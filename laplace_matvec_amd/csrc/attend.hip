@@ -25,7 +25,7 @@ enum SweepMode { kEnd, kOut, kStore };
 
 // REV runs the segments backwards with queries and output gradients in place
 // of keys and values: the gradient of the states.
-template <class T, class TG, int DK, int DV, int MODE, bool REV>
+template <class T, class TG, int DK, int DV, int MODE, bool REV, bool WHOLE>
 __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof(typename Compute<T>::E) == 4 ? 1 : 2) void lx_attend_sweep(AttendArgs A)
 {
     typedef typename Compute<T>::E E;
@@ -103,10 +103,10 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
     const TG* gp = (const TG*)A.g + h;
 
     const int chunks = (t.rows + kC - 1) / kC;
-    RowTile<T, DK> tk;
-    RowTile<T, DV> tv;
+    RowTile<T, DK, WHOLE> tk;
+    RowTile<T, DV, WHOLE> tv;
     Pack<T, 8> tq[DK / 32];
-    float tg = 0.f;
+    TG tg = (TG)0.f;
     auto fetch = [&](int ci) {
         const int c = REV ? chunks - 1 - ci : ci;
         const int64_t row = t.row + (int64_t)c * kC;
@@ -117,9 +117,14 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
             const int i = 16 * wave + l16;
 #pragma unroll
             for (int kk = 0; kk < DK / 32; ++kk)
-                tq[kk] = load8(qp + (row + i) * A.ldq + 32 * kk + 2 * g4, i < rows ? kcols - 32 * kk - 2 * g4 : 0);
+                if (WHOLE) {
+                    const int at = i < rows ? i : rows - 1, col = 32 * kk + 2 * g4;
+                    tq[kk] = load8_whole(qp + (row + at) * A.ldq + (col < kcols ? col : kcols - 8));
+                } else {
+                    tq[kk] = load8(qp + (row + i) * A.ldq + 32 * kk + 2 * g4, i < rows ? kcols - 32 * kk - 2 * g4 : 0);
+                }
         }
-        if (wave == 0) tg = lane < rows ? (float)gp[(row + lane) * A.ldg] : 0.f;
+        if (wave == 0) tg = gp[(row + (lane < rows ? lane : rows - 1)) * A.ldg];
     };
     fetch(0);
     float decay = 1.f;  // of the segment
@@ -128,11 +133,11 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
         const int64_t row = t.row + (int64_t)c * kC;
         const int rows = t.rows - c * kC < kC ? t.rows - c * kC : kC;
         if (wave == 0) {
-            s_d.make(tg);
+            s_d.make(lane < rows ? (float)tg : 0.f);
             s_f[lane] = REV ? s_d.into[lane] * A.scale : s_d.out[lane];
         }
-        tk.put(s_k);
-        tv.put(s_v);
+        tk.put(s_k, rows, kcols);
+        tv.put(s_v, rows, vcols);
         {
             const bool odd = __any(tv.odd());
             if (lane == 0) s_odd[wave] = odd;
@@ -211,6 +216,7 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
                 for (int r = 0; r < 4; ++r) fp[jt >> 1].v[4 * (jt & 1) + r] = (E)p[r];
             }
             const f32x4 into = *reinterpret_cast<const f32x4*>(&s_d.into[16 * wave + g4]);
+            T* yp = (T*)A.y + (row + 16 * wave + g4) * A.ldy + h * A.dv + v0 + l16;
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
                 f32x4 o = {};
@@ -231,14 +237,19 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
                         if (s_rows[col] & seen) o[r] = __builtin_nanf("");
                     }
                 }
+                if (rows == kC && vcols >= DV && !A.part) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int at = 16 * wave + g4 + r;
-                    if (at < rows && col < vcols) {
-                        if (A.part)
-                            A.part[(kb * A.n + row + at) * ((int64_t)A.heads * A.dv) + h * A.dv + v0 + col] = o[r];
-                        else
-                            ((T*)A.y)[(row + at) * A.ldy + h * A.dv + v0 + col] = (T)o[r];
+                    for (int r = 0; r < 4; ++r) yp[r * A.ldy + 16 * b] = (T)o[r];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int at = 16 * wave + g4 + r;
+                        if (at < rows && col < vcols) {
+                            if (A.part)
+                                A.part[(kb * A.n + row + at) * ((int64_t)A.heads * A.dv) + h * A.dv + v0 + col] = o[r];
+                            else
+                                yp[r * A.ldy + 16 * b] = (T)o[r];
+                        }
                     }
                 }
             }
@@ -413,20 +424,30 @@ __global__ __launch_bounds__(256) void lx_attend_step(AttendStepArgs A)
     }
 }
 
+template <class T, class TG, int DK, int DV, int MODE, bool REV>
+hipError_t sweep_launch(const AttendArgs& a, const char* label, hipStream_t s)
+{
+    const int64_t groups = Ragged{a.offsets, a.seqs, a.n, a.seq_len}.units(a.segment) * a.heads * a.nkb * a.nvb;
+    const dim3 grid = grid_of<kAttendThreads>(groups);
+    if (a.dk % 8 == 0 && a.dv % 8 == 0)
+        LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, DV, MODE, REV, true><<<grid, kAttendThreads, 0, s>>>(a)));
+    else
+        LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, DV, MODE, REV, false><<<grid, kAttendThreads, 0, s>>>(a)));
+    return hipSuccess;
+}
+
+// With 16-bit products two blocks of columns in one workgroup, which share
+// its keys, queries and scores.
 template <class T, class TG, int DK, int MODE, bool REV>
 hipError_t sweep_go(AttendArgs a, const char* label, hipStream_t s)
 {
     if constexpr (sizeof(typename Compute<T>::E) == 2) {
         if (a.nvb % 2 == 0) {
             a.nvb /= 2;
-            const int64_t groups = Ragged{a.offsets, a.seqs, a.n, a.seq_len}.units(a.segment) * a.heads * a.nkb * a.nvb;
-            LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, 128, MODE, REV><<<grid_of<kAttendThreads>(groups), kAttendThreads, 0, s>>>(a)));
-            return hipSuccess;
+            return sweep_launch<T, TG, DK, 128, MODE, REV>(a, label, s);
         }
     }
-    const int64_t groups = Ragged{a.offsets, a.seqs, a.n, a.seq_len}.units(a.segment) * a.heads * a.nkb * a.nvb;
-    LX_LAUNCH(label, s, (lx_attend_sweep<T, TG, DK, 64, MODE, REV><<<grid_of<kAttendThreads>(groups), kAttendThreads, 0, s>>>(a)));
-    return hipSuccess;
+    return sweep_launch<T, TG, DK, 64, MODE, REV>(a, label, s);
 }
 
 template <bool REV>

@@ -96,7 +96,7 @@ __device__ __forceinline__ Out<T> out_rows(void* to, int64_t ld, float* sums, in
 // Waves 0 to 3 make the rows' side (scores, dq), waves 4 to 7 the columns'
 // (dk, dv), sixteen rows of the chunk each; wave w and w + 4 share a SIMD, so
 // each has one of either.  What the next head needs is on its way meanwhile.
-template <class T, class TG, int DK, int DV>
+template <class T, class TG, int DK, int DV, bool WHOLE>
 __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
 {
     typedef typename Compute<T>::E E;
@@ -181,19 +181,19 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
             }
         }
     };
-    RowTile<T, DV, kGradThreads> tv, td;
+    RowTile<T, DV, WHOLE, kGradThreads> tv, td;
     f32x4 ts[NS], tt[NS];
-    float tg = 0.f;
+    TG tg = (TG)0.f;
     const T* vp = (const T*)A.v + t.row * A.ldv;
     const T* dp = (const T*)A.dy + t.row * A.lddy + (int64_t)h0 * A.dv;
-    const TG* gp = (const TG*)A.g + (t.row + lane) * A.ldg + h0;
+    const TG* gp = (const TG*)A.g + (t.row + (lane < rows ? lane : rows - 1)) * A.ldg + h0;
     auto fetch = [&](int hl, int hv, int vb) {
         const int v0 = vb * DV, vcols = A.dv - v0;
         tv.load(vp + hv * A.dv + v0, A.ldv, rows, vcols);
         td.load(dp + hl * A.dv + v0, A.lddy, rows, vcols);
         state_in(ts, is_first, slot_s, A.h0, hl, v0);
         state_in(tt, is_last, slot_t, A.dfinal, hl, v0);
-        if (wave == 0) tg = lane < rows ? (float)gp[hl] : 0.f;
+        if (wave == 0) tg = gp[hl];
     };
     auto put_state = [&](const f32x4& x, E* s, int row, int col) {
         V4 w[N];
@@ -208,12 +208,12 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         for (int m = 0; m < N; ++m) *reinterpret_cast<V4*>(&s[(m * DK + row) * PV + col]) = w[m];
     };
     {
-        RowTile<T, DK, kGradThreads> a, b;
+        RowTile<T, DK, WHOLE, kGradThreads> a, b;
         a.load((const T*)A.q + t.row * A.ldq + hq0 * A.dk + k0, A.ldq, rows, kcols);
         b.load((const T*)A.k + t.row * A.ldk + hk0 * A.dk + k0, A.ldk, rows, kcols);
         fetch(0, hv0, 0);
-        a.put(s_q);
-        b.put(s_k);
+        a.put(s_q, rows, kcols);
+        b.put(s_k, rows, kcols);
     }
     __syncthreads();
     const int i = w16 + l16;
@@ -238,8 +238,8 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         const bool ends_head = vb + 1 == nvb;
         const bool more = !(ends_head && hl + 1 == A.loop);
         const int next_hv = ends_head && in_hv + 1 == rv ? hv + 1 : hv;
-        tv.put(s_v);
-        td.put(s_do);
+        tv.put(s_v, rows, vcols);
+        td.put(s_do, rows, vcols);
         float z = 0.f;
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         z += __shfl_xor(z, 16);
         z += __shfl_xor(z, 32);
         if (lane == 0) s_z[flip][wave] = z;
-        if (wave == 0 && vb == 0) s_d.make(tg);
+        if (wave == 0 && vb == 0) s_d.make(lane < rows ? (float)tg : 0.f);
         __syncthreads();
         if (more) fetch(ends_head ? hl + 1 : hl, next_hv, ends_head ? 0 : vb + 1);
 
@@ -425,7 +425,11 @@ template <class T, class TG, int DK, int DV>
 hipError_t grad_go(const AttendArgs& a, hipStream_t s)
 {
     const int64_t groups = Ragged{a.offsets, a.seqs, a.n, a.seq_len}.units(kC) * (a.heads / a.loop) * a.nkb;
-    LX_LAUNCH("attend_grad", s, (lx_attend_grad<T, TG, DK, DV><<<grid_of<kGradThreads>(groups), kGradThreads, 0, s>>>(a)));
+    const dim3 grid = grid_of<kGradThreads>(groups);
+    if (a.dk % 8 == 0 && a.dv % 8 == 0)
+        LX_LAUNCH("attend_grad", s, (lx_attend_grad<T, TG, DK, DV, true><<<grid, kGradThreads, 0, s>>>(a)));
+    else
+        LX_LAUNCH("attend_grad", s, (lx_attend_grad<T, TG, DK, DV, false><<<grid, kGradThreads, 0, s>>>(a)));
     return hipSuccess;
 }
 

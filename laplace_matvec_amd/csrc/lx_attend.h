@@ -65,20 +65,66 @@ __device__ __forceinline__ void put8(E* s, const Pack<T, 8>& p)
 __device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u; }
 __device__ __forceinline__ bool finite(bf16_t x) { return (__builtin_bit_cast(uint16_t, x) & 0x7F80u) != 0x7F80u; }
 
-// A tile of kC rows x W columns on its way from memory to LDS.
-template <class T, int W, int THREADS = kAttendThreads>
+// 8 neighbours from p on, all there.
+template <class T>
+__device__ __forceinline__ Pack<T, 8> load8_whole(const T* p)
+{
+    if constexpr (sizeof(T) == 2) {
+        return load_pack<8>(p);
+    } else {
+        Pack<T, 8> r;
+        const Pack<T, 4> a = load_pack<4>(p), b = load_pack<4>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r.v[i] = a.v[i];
+            r.v[4 + i] = b.v[i];
+        }
+        return r;
+    }
+}
+
+// A tile of kC rows x W columns on its way from memory to LDS.  WHOLE: rows
+// are whole groups of 8 values.  Then what is not there is read from what is,
+// and cleared on its way to LDS: loads without branches, which would have to
+// wait for their values where the paths meet again.
+template <class T, int W, bool WHOLE, int THREADS = kAttendThreads>
 struct RowTile {
     static constexpr int kVecs = kC * W / 8 / THREADS;
     Pack<T, 8> r[kVecs];
 
-    // p: first row and column; rows and cols: how many are there
+    // p: first row and column; rows and cols: how many are there, at least one
     __device__ __forceinline__ void load(const T* p, int64_t ld, int rows, int cols)
     {
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
             const int i = (int)threadIdx.x + j * THREADS;
-            const int row = i / (W / 8), col = i % (W / 8) * 8;
-            r[j] = load8(p + row * ld + col, row < rows ? cols - col : 0);
+            int row = i / (W / 8), col = i % (W / 8) * 8;
+            if (WHOLE) {
+                row = row < rows ? row : rows - 1;
+                col = col < cols ? col : cols - 8;
+                r[j] = load8_whole(p + row * ld + col);
+            } else {
+                r[j] = load8(p + row * ld + col, row < rows ? cols - col : 0);
+            }
+        }
+    }
+    template <class E>
+    __device__ __forceinline__ void put(E* s, int rows, int cols) const
+    {
+        constexpr int kPitch = W + kPad<E>;
+        if (WHOLE && (rows < kC || cols < W)) {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int i = (int)threadIdx.x + j * THREADS;
+                const int row = i / (W / 8), col = i % (W / 8) * 8;
+                put8(s + row * kPitch + col, row < rows && col < cols ? r[j] : Pack<T, 8>{});
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                const int i = (int)threadIdx.x + j * THREADS;
+                put8(s + i / (W / 8) * kPitch + i % (W / 8) * 8, r[j]);
+            }
         }
     }
     // Whether any of the values is inf or NaN: its exponent is all ones, and
@@ -97,16 +143,6 @@ struct RowTile {
             for (int i = 0; i < 2 * (int)sizeof(T); ++i) any |= (w[i] & kExp) + kOne;
         }
         return any & kSign;
-    }
-    template <class E>
-    __device__ __forceinline__ void put(E* s) const
-    {
-        constexpr int kPitch = W + kPad<E>;
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int i = (int)threadIdx.x + j * THREADS;
-            put8(s + i / (W / 8) * kPitch + i % (W / 8) * 8, r[j]);
-        }
     }
 };
 
