@@ -68,6 +68,14 @@ struct Out {
     template <int C>
     __device__ __forceinline__ void put_tiles(int row0, int col0, int rows, int cols, const f32x4 (&x)[C]) const
     {
+        if (!sums && rows == kC && cols >= 16 * C) {
+            T* p = to + row0 * ld + col0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < C; ++c) p[r * ld + 16 * c] = (T)x[c][r];
+            return;
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             if (row0 + r >= rows) continue;
@@ -134,10 +142,12 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     // This chunk's rows of the results: of the arrays, or of planes of partial
     // sums where several workgroups add to one row.
     const int hq0 = h0 / rq, hk0 = h0 / rk, hv0 = h0 / rv;
-    const Out<T> oq = out_rows<T>(A.dq, A.lddq, A.part_q, h0 % rq / A.loop, A.n, A.hq * A.dk, t.row, hq0 * A.dk + k0);
-    const Out<T> ok = out_rows<T>(A.dkey, A.lddk, A.part_k, h0 % rk / A.loop, A.n, A.hk * A.dk, t.row, hk0 * A.dk + k0);
-    const Out<TG> og = out_rows<TG>(A.dg, A.lddg, A.part_g, kb, A.n, A.heads, t.row, h0);
+    auto out_q = [&] { return out_rows<T>(A.dq, A.lddq, A.part_q, h0 % rq / A.loop, A.n, A.hq * A.dk, t.row, hq0 * A.dk + k0); };
+    auto out_k = [&] { return out_rows<T>(A.dkey, A.lddk, A.part_k, h0 % rk / A.loop, A.n, A.hk * A.dk, t.row, hk0 * A.dk + k0); };
+    auto out_g = [&] { return out_rows<TG>(A.dg, A.lddg, A.part_g, kb, A.n, A.heads, t.row, h0); };
     if (t.group < 0) {
+        const Out<T> oq = out_q(), ok = out_k();
+        const Out<TG> og = out_g();
         for (int i = threadIdx.x; i < rows * DK; i += kGradThreads) {
             if (i % DK >= kcols) continue;
             if (A.dq) oq.put(i / DK, i % DK, 0.f);
@@ -162,22 +172,25 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     const int64_t edge_at = ((t.group * A.heads + h0) * A.dk + k0) * (int64_t)A.dv;
     const int at0 = threadIdx.x / (DV / 4), col0 = threadIdx.x % (DV / 4) * 4;  // of a thread's values of a state
     constexpr int kStep = kGradThreads / (DV / 4);                             // rows to its next ones
+    const bool plain = A.dk == A.dkp && A.dv == A.dvp;  // edges look like slots
     auto state_in = [&](f32x4 (&x)[NS], bool edge, const float* slots, const float* edges, int hl, int v0) {
-        if (!edge) {
-            const float* p = slots + hl * size + v0 + (int64_t)at0 * A.dvp + col0;
+        if (!edge || (plain && edges)) {
+            const float* p = (edge ? edges + edge_at : slots) + hl * size + v0 + (at0 * A.dvp + col0);
 #pragma unroll
             for (int u = 0; u < NS; ++u) x[u] = *reinterpret_cast<const f32x4*>(p + u * kStep * A.dvp);
-        } else {
-            const float* p = edges ? edges + edge_at + hl * ((int64_t)A.dk * A.dv) + v0 + col0 : nullptr;
-            const int cols = A.dv - v0 - col0;
+            return;
+        }
+        const float* p = edges + edge_at + hl * ((int64_t)A.dk * A.dv) + v0;
+        const int cols = A.dv - v0;
 #pragma unroll
-            for (int u = 0; u < NS; ++u) {
-                x[u] = f32x4{};
-                const int row = at0 + u * kStep;
-                if (p && row < kcols)
+        for (int u = 0; u < NS; ++u) {
+            x[u] = f32x4{};
+            if (!edges) continue;
+            const int row = at0 + u * kStep;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (r < cols) x[u][r] = p[(int64_t)row * A.dv + r];
+            for (int r = 0; r < 4; ++r) {  // what is not there is read from the last that is
+                const float y = p[(row < kcols ? row : kcols - 1) * A.dv + (col0 + r < cols ? col0 + r : cols - 1)];
+                x[u][r] = row < kcols && col0 + r < cols ? y : 0.f;
             }
         }
     };
@@ -234,6 +247,12 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     int flip = 0, vb = 0, hl = 0;  // block of columns; head, from h0 on
     int hv = hv0, in_hv = h0 - hv0 * rv;  // the value head, and which of those that share it
     for (;; flip ^= 1) {
+        // Places worked out anew each time: kept for all heads they would take
+        // the registers that the next head's values need.
+        int here = lane, thread = threadIdx.x;
+        asm volatile("" : "+v"(here), "+v"(thread));
+        const int g4 = 4 * (here >> 4), l16 = here & 15, i = w16 + l16;
+        const int at0 = thread / (DV / 4), col0 = thread % (DV / 4) * 4;
         const int v0 = vb * DV, vcols = A.dv - v0;
         const bool ends_head = vb + 1 == nvb;
         const bool more = !(ends_head && hl + 1 == A.loop);
@@ -277,6 +296,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     u[r] += x[r] * (float)s_q[(w16 + g4 + r) * PK + 16 * c + l16];
                     acc[c][r] += x[r];
                 }
+                if (c & 1) __builtin_amdgcn_sched_barrier(0);  // not more fragments at a time than registers
             }
             const float hi_i = s_d.hi[i], lo_i = s_d.lo[i];
             const int last_i = s_d.last[i];
@@ -314,6 +334,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     sums[r] = sum16(w[r]);
                 }
                 if (l16 == 0) *reinterpret_cast<f32x4*>(&s_col[wave][16 * jt + g4]) = sums;
+                __builtin_amdgcn_sched_barrier(0);
             }
             row_sum += __shfl_xor(row_sum, 16);
             row_sum += __shfl_xor(row_sum, 32);
@@ -343,6 +364,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     u[r] += x[r] * (float)s_k[(w16 + g4 + r) * PK + 16 * c + l16];
                     acc[c][r] += x[r];
                 }
+                if (c & 1) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) u[r] = sum16(u[r]);
@@ -360,23 +382,29 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) dv[b][r] = out[r] == 0.f ? 0.f : out[r] * x[r];
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
         __syncthreads();
         if (side == 0) {
 #pragma unroll
-            for (int c = 0; c < DK / 16; ++c)
+            for (int c = 0; c < DK / 16; ++c) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (32 * s <= w16) acc[c] = mma(fe[s], frag_across(s_k + 32 * s * PK + 16 * c, PK), acc[c]);
+                if (c & 1) __builtin_amdgcn_sched_barrier(0);
+            }
         } else {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (32 * s + 16 < w16) continue;
                 const Frag<E> f = frag_across(s_e + 32 * s * PC + w16, PC);
 #pragma unroll
-                for (int c = 0; c < DK / 16; ++c) acc[c] = mma(f, frag_across(s_q + 32 * s * PK + 16 * c, PK), acc[c]);
+                for (int c = 0; c < DK / 16; ++c) {
+                    acc[c] = mma(f, frag_across(s_q + 32 * s * PK + 16 * c, PK), acc[c]);
+                    if ((c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+                }
             }
             if (A.dval) {
 #pragma unroll
@@ -405,7 +433,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
             const float through = whole == 0.f ? 0.f : whole * z;
             // the last cut up to a row is the row itself: its decay has no gradient
             dg = (vb ? dg : 0.f) + (s_d.last[lane] == lane ? 0.f : from + (to - own) + through);
-            if (A.dg && ends_head && lane < rows) og.put(lane, hl, dg);
+            if (A.dg && ends_head && lane < rows) out_g().put(lane, hl, dg);
         }
         if (!more) break;
         if (ends_head) {
@@ -418,7 +446,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         }
     }
     if (side == 0 ? A.dq != nullptr : A.dkey != nullptr)
-        (side == 0 ? oq : ok).template put_tiles<DK / 16>(w16 + g4, l16, rows, kcols, acc);
+        (side == 0 ? out_q() : out_k()).template put_tiles<DK / 16>(w16 + g4, l16, rows, kcols, acc);
 }
 
 template <class T, class TG, int DK, int DV>
