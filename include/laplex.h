@@ -438,13 +438,14 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  *             float32's range.
  *   h0, final float32 [seqs][heads][dk][dv], states before the first and after
  *             the last rows, or NULL (h0: 0).
- *   states    float32[laplex_attend_states(n, heads, dk, dv)] or NULL: what
+ *   states    float32[laplex_attend_states(n, seqs, heads, dk, dv)] or NULL: what
  *             laplex_attend_backward needs of this pass (16-byte aligned).
  *   ws        device scratch of laplex_attend_workspace(..., 0) bytes, 16-byte
  *             aligned.
  * Float32 and float16 rows are multiplied in float32.  With bfloat16 rows,
- * scores and states are rounded to bfloat16 (states: to two of them) where
- * they enter a product; the states themselves stay float32.
+ * what enters a product is bfloat16 too: scores, states for y and gradients
+ * of scores rounded once, rows times decays for the states and states for
+ * gradients in two terms, 16 bits; the states themselves stay float32.
  * A row that holds inf or NaN reaches its own and later rows of its heads and
  * sequence, up to a decay of 0; they may get NaN where inf is due.  In the
  * backward pass it may reach every gradient of its heads and sequence.
@@ -461,8 +462,8 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  *
  * The two size functions return -1 for sizes out of range.
  */
-int64_t laplex_attend_states(int64_t n, int64_t heads, int64_t dk, int64_t dv);
-int64_t laplex_attend_workspace(int64_t n, int64_t heads, int64_t query_heads, int64_t key_heads,
+int64_t laplex_attend_states(int64_t n, int64_t seqs, int64_t heads, int64_t dk, int64_t dv);
+int64_t laplex_attend_workspace(int64_t n, int64_t seqs, int64_t heads, int64_t query_heads, int64_t key_heads,
                                 int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type, int backward);
 laplex_status laplex_attend(int64_t n, int64_t seqs, const int32_t* offsets, int64_t heads, int64_t query_heads,
                             int64_t key_heads, int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type,

@@ -2079,10 +2079,10 @@ constexpr const char* kBadExperts =
 
 // Sizes of a pass of the matrix memory, the same for both directions.
 constexpr int kAttendMaxHeads = 4096, kAttendMaxDim = 1024;
-bool attend_sizes(lx::AttendArgs& A, int64_t n, int64_t heads, int64_t hq, int64_t hk, int64_t hv, int64_t dk,
+bool attend_sizes(lx::AttendArgs& A, int64_t n, int64_t seqs, int64_t heads, int64_t hq, int64_t hk, int64_t hv, int64_t dk,
                   int64_t dv, laplex_dtype type)
 {
-    if (n < 0 || n > 0x7FFFFFFF || heads < 1 || heads > kAttendMaxHeads || dk < 1 || dk > kAttendMaxDim || dv < 1 ||
+    if (n < 0 || n > 0x7FFFFFFF || seqs < 1 || seqs > (int64_t)1 << 24 || heads < 1 || heads > kAttendMaxHeads || dk < 1 || dk > kAttendMaxDim || dv < 1 ||
         dv > kAttendMaxDim || !dtype_ok(type))
         return false;
     for (int64_t h : {hq, hk, hv})
@@ -2101,7 +2101,7 @@ bool attend_sizes(lx::AttendArgs& A, int64_t n, int64_t heads, int64_t hq, int64
     A.dvp = A.nvb * 64;
     A.grad_block_k = type == LAPLEX_BF16 ? A.block_k : 64;
     A.loop = hq == hk ? (int)(heads / hq) : 1;
-    A.segment = lx::attend_segment(n, heads * A.nkb * A.nvb);
+    A.segment = lx::attend_segment(n, seqs, heads * A.nkb * (A.nvb % 2 ? A.nvb : A.nvb / 2));
     // states of all slots between chunks stay below 2^46 bytes
     return (double)(n / lx::kAttendChunk + 1) * (double)heads * A.dkp * A.dvp < 1.7e13;
 }
@@ -2138,15 +2138,14 @@ size_t attend_carve(lx::AttendArgs& A, char* base, bool backward, bool own_state
 }
 
 constexpr const char* kBadAttend =
-    "bad sizes or type: 0 <= n < 2^31, heads in [1, 4096] and a multiple of each array's, dk and dv in [1, 1024]";
+    "bad sizes or type: 0 <= n < 2^31, seqs in [1, 2^24], heads in [1, 4096] and a multiple of each array's, dk and dv in [1, 1024]";
 
 const char* attend_common(lx::AttendArgs& A, int64_t n, int64_t seqs, const int32_t* offsets, int64_t heads,
                           int64_t hq, int64_t hk, int64_t hv, int64_t dk, int64_t dv, laplex_dtype type,
                           laplex_dtype gate_type, float scale, const void* q, int64_t ldq, const void* k, int64_t ldk,
                           const void* v, int64_t ldv, const void* g, int64_t ldg, const float* h0)
 {
-    if (!attend_sizes(A, n, heads, hq, hk, hv, dk, dv, type)) return kBadAttend;
-    if (seqs < 1 || seqs > (int64_t)1 << 24) return "seqs must be in [1, 2^24]";
+    if (!attend_sizes(A, n, seqs, heads, hq, hk, hv, dk, dv, type)) return kBadAttend;
     if (!offsets && n % seqs) return "without offsets n must be a multiple of seqs";
     if (gate_type != type && gate_type != LAPLEX_F32) return "bad gate_type";
     if (n > 0 && (!q || !k || !v || !g)) return "q, k, v or g is NULL";
@@ -2267,19 +2266,19 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
     return LAPLEX_OK;
 }
 
-int64_t laplex_attend_states(int64_t n, int64_t heads, int64_t dk, int64_t dv)
+int64_t laplex_attend_states(int64_t n, int64_t seqs, int64_t heads, int64_t dk, int64_t dv)
 {
     lx::AttendArgs A;
-    if (!attend_sizes(A, n, heads, heads, heads, heads, dk, dv, LAPLEX_F32)) return -1;
+    if (!attend_sizes(A, n, seqs, heads, heads, heads, heads, dk, dv, LAPLEX_F32)) return -1;
     return attend_slots(A) * (int64_t)attend_slot_values(A);
 }
 
-int64_t laplex_attend_workspace(int64_t n, int64_t heads, int64_t query_heads, int64_t key_heads,
+int64_t laplex_attend_workspace(int64_t n, int64_t seqs, int64_t heads, int64_t query_heads, int64_t key_heads,
                                 int64_t value_heads, int64_t dk, int64_t dv, laplex_dtype type, int backward)
 {
     lx::AttendArgs A;
     if ((backward != 0 && backward != 1) ||
-        !attend_sizes(A, n, heads, query_heads, key_heads, value_heads, dk, dv, type))
+        !attend_sizes(A, n, seqs, heads, query_heads, key_heads, value_heads, dk, dv, type))
         return -1;
     return (int64_t)attend_carve(A, nullptr, backward, true);
 }
@@ -2297,11 +2296,11 @@ laplex_status laplex_attend(int64_t n, int64_t seqs, const int32_t* offsets, int
         return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
     if (n > 0 && !y) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "y is NULL");
     const int64_t need =
-        laplex_attend_workspace(n, heads, query_heads, key_heads, value_heads, dk, dv, type, 0);
+        laplex_attend_workspace(n, seqs, heads, query_heads, key_heads, value_heads, dk, dv, type, 0);
     if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < need))
         return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_attend_workspace");
     const size_t e = dtype_size(type), eg = dtype_size(gate_type);
-    const int64_t ns = laplex_attend_states(n, heads, dk, dv), one = heads * dk * dv;
+    const int64_t ns = laplex_attend_states(n, seqs, heads, dk, dv), one = heads * dk * dv;
     if (ns > 0 && (uintptr_t)states % 16) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "states must be 16-byte aligned");
     const Rows outs[4] = {{y, n, ldy, heads * dv, e}, {final, seqs, one, one, 4},
                           {ns > 0 ? states : nullptr, 1, ns, ns, 4}, {need > 0 ? ws : nullptr, 1, need, need, 1}};
@@ -2337,11 +2336,11 @@ laplex_status laplex_attend_backward(int64_t n, int64_t seqs, const int32_t* off
         return fail(LAPLEX_ERR_INVALID_ARGUMENT, m);
     if (!dq && !dk_out && !dv_out && !dg && !dh0) return LAPLEX_OK;
     if (n > 0 && !dy) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "dy is NULL");
-    const int64_t ns = laplex_attend_states(n, heads, dk, dv), one = heads * dk * dv;
+    const int64_t ns = laplex_attend_states(n, seqs, heads, dk, dv), one = heads * dk * dv;
     if (ns > 0 && (!states || (uintptr_t)states % 16))
         return fail(LAPLEX_ERR_INVALID_ARGUMENT, "states is NULL or misaligned");
     const int64_t need =
-        laplex_attend_workspace(n, heads, query_heads, key_heads, value_heads, dk, dv, type, 1);
+        laplex_attend_workspace(n, seqs, heads, query_heads, key_heads, value_heads, dk, dv, type, 1);
     if (need > 0 && (!ws || (uintptr_t)ws % 16 || ws_bytes < need))
         return fail(LAPLEX_ERR_INVALID_ARGUMENT, "ws is NULL, misaligned or smaller than laplex_attend_workspace");
     const size_t e = dtype_size(type), eg = dtype_size(gate_type);
@@ -2385,7 +2384,7 @@ laplex_status laplex_attend_step(int64_t n, int64_t pool, const int32_t* slots, 
                                  void* y, int64_t ldy, void* stream)
 {
     lx::AttendArgs sizes;  // a step's own limits: those of a pass of no rows
-    if (!attend_sizes(sizes, 0, heads, query_heads, key_heads, value_heads, dk, dv, type) || n < 0 ||
+    if (!attend_sizes(sizes, 0, 1, heads, query_heads, key_heads, value_heads, dk, dv, type) || n < 0 ||
         n > 0x7FFFFFFF || pool < 0 || pool > 0x7FFFFFFF)
         return fail(LAPLEX_ERR_INVALID_ARGUMENT, kBadAttend);
     if (gate_type != type && gate_type != LAPLEX_F32) return fail(LAPLEX_ERR_INVALID_ARGUMENT, "bad gate_type");

@@ -322,7 +322,7 @@ template <bool REV>
 __global__ __launch_bounds__(256) void lx_attend_scan(AttendArgs A)
 {
     const int64_t block = (int64_t)A.dkp * A.dvp;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // of [heads][dkp][dvp]
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // of [heads][dkp][dvp]
     if (i >= A.heads * block) return;
     const int h = (int)(i / block), row = (int)(i % block / A.dvp), col = (int)(i % A.dvp);
     const Ragged R{A.offsets, A.seqs, A.n, A.seq_len};
@@ -331,14 +331,30 @@ __global__ __launch_bounds__(256) void lx_attend_scan(AttendArgs A)
         const int64_t first = R.bound(q + 1), end = R.bound(q + 2);
         if (end - first <= A.segment) continue;
         const int64_t count = (end - first + A.segment - 1) / A.segment - 1;
-        float s = 0.f;
-        if (edge && row < A.dk && col < A.dv) s = edge[((q * A.heads + h) * A.dk + row) * (int64_t)A.dv + col];
+        f32x4 s = {};
+        if (edge && row < A.dk)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (col + r < A.dv) s[r] = edge[((q * A.heads + h) * A.dk + row) * (int64_t)A.dv + col + r];
+        // a slot is loaded while the one before it is worked out
+        const int64_t slot0 = first / A.segment + (REV ? count - 1 : 0), step = REV ? -1 : 1;
+        f32x4* p = reinterpret_cast<f32x4*>(A.seg_states + slot0 * A.heads * block + i);
+        const float* d = A.seg_decays + slot0 * A.heads + h;
+        f32x4 own = *p;
+        float decay = *d;
         for (int64_t c = 0; c < count; ++c) {
-            const int64_t slot = first / A.segment + (REV ? count - 1 - c : c);
-            float* p = A.seg_states + slot * A.heads * block + i;
-            const float decay = A.seg_decays[slot * A.heads + h];
-            s = decay == 0.f ? *p : decay * s + *p;
-            *p = s;
+            f32x4* at = p;
+            const f32x4 x = own;
+            const float a = decay;
+            if (c + 1 < count) {
+                p += step * A.heads * block / 4;
+                d += step * A.heads;
+                own = *p;
+                decay = *d;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] = a == 0.f ? x[r] : a * s[r] + x[r];
+            *at = s;
         }
     }
 }
@@ -453,7 +469,7 @@ hipError_t sweep_go(AttendArgs a, const char* label, hipStream_t s)
 template <bool REV>
 hipError_t scan_go(const AttendArgs& a, hipStream_t s)
 {
-    const int64_t groups = ((int64_t)a.heads * a.dkp * a.dvp + 255) / 256;
+    const int64_t groups = ((int64_t)a.heads * a.dkp * a.dvp + 1023) / 1024;
     const unsigned seqs = (unsigned)(a.seqs < 1024 ? a.seqs : 1024);
     LX_LAUNCH("attend_scan", s, (lx_attend_scan<REV><<<dim3((unsigned)groups, seqs), 256, 0, s>>>(a)));
     return hipSuccess;

@@ -522,11 +522,15 @@ struct AttendArgs {
     int64_t lddq = 0, lddk = 0, lddv = 0, lddg = 0;
     float *part_q = nullptr, *part_k = nullptr, *part_v = nullptr, *part_g = nullptr;
 };
-// Rows of a segment: about 1024 workgroups, `parts` of them beside each other.
-inline int attend_segment(int64_t n, int64_t parts)
+// Rows of a segment, of which `parts` workgroups work beside each other: 512
+// workgroups, two on each of the 256 CUs, for one sequence; twice as many for
+// several, whose lengths may differ (one of 65536 rows, 16 heads: 421 us at
+// 512, 461 at 1024; 24 of 32768 in all, 32 heads, both directions: 1484 and
+// 1363); at least two chunks each.
+inline int attend_segment(int64_t n, int64_t seqs, int64_t parts)
 {
-    const double rows = (double)n * (double)parts / 1024.0;
-    const int64_t r = rows < 512.0 ? 512 : rows > 1073741824.0 ? 1073741824 : (int64_t)rows;
+    const double rows = (double)n * (double)parts / (seqs > 1 ? 1024.0 : 512.0);
+    const int64_t r = rows < 128.0 ? 128 : rows > 1073741824.0 ? 1073741824 : (int64_t)rows;
     return (int)((r + kAttendChunk - 1) / kAttendChunk * kAttendChunk);
 }
 // Whether a sequence may have more than one segment.

@@ -60,8 +60,8 @@ SIGNATURES = {
     "laplex_experts": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _I64, _VP, _I64, _VP]),
     "laplex_experts_backward": (_I32, [_I64, _I64, _VP, _I64, _I64, _I32, _I32, _VP, _I64, _VP, _I64, _I64, _VP, _I64,
                                        _VP, _I64, _VP, _I64, _I64, _VP]),
-    "laplex_attend_states": (_I64, [_I64] * 4),
-    "laplex_attend_workspace": (_I64, [_I64] * 7 + [_I32, _I32]),
+    "laplex_attend_states": (_I64, [_I64] * 5),
+    "laplex_attend_workspace": (_I64, [_I64] * 8 + [_I32, _I32]),
     "laplex_attend": (_I32, [_I64, _I64, _VP] + [_I64] * 6 + [_I32, _I32, ctypes.c_float] + [_VP, _I64] * 4
                       + [_VP, _VP, _I64, _VP, _VP, _VP, _I64, _VP]),
     "laplex_attend_backward": (_I32, [_I64, _I64, _VP] + [_I64] * 6 + [_I32, _I32, ctypes.c_float] + [_VP, _I64] * 4
@@ -750,12 +750,12 @@ def laplex_attend(q, k, v, g, offsets=None, h0=None, scale: float = 1.0, final: 
     n, seqs, sizes, (ldq, ldk, ldv, ldg) = _attend_parts(q, k, v, g, offsets, h0)
     heads, dk, dv = sizes[0], sizes[4], sizes[5]
     lib, dev, kind = load(), q.device, _DTYPES[q.dtype]
-    need = _size(lib.laplex_attend_workspace(n, *sizes, kind, 0), "laplex_attend")
+    need = _size(lib.laplex_attend_workspace(n, seqs, *sizes, kind, 0), "laplex_attend")
     s, ctx = _launch(stream, dev, q, k, v, g, offsets, h0)
     with ctx:
         y = q.new_empty((*g.shape, dv))
         hf = torch.empty((seqs, heads, dk, dv), dtype=torch.float32, device=dev) if final else None
-        states = torch.empty(lib.laplex_attend_states(n, heads, dk, dv), dtype=torch.float32, device=dev) if keep else None
+        states = torch.empty(lib.laplex_attend_states(n, seqs, heads, dk, dv), dtype=torch.float32, device=dev) if keep else None
         ws = _scratch(need, dev)
         _check(lib.laplex_attend(n, seqs, _at(offsets), *sizes, kind, _DTYPES[g.dtype], scale, _at(q), ldq, _at(k),
                                  ldk, _at(v), ldv, _at(g), ldg, _at(h0), _at(y), heads * dv, _at(hf), _at(states),
@@ -776,10 +776,10 @@ def laplex_attend_backward(q, k, v, g, dy, states, offsets=None, h0=None, scale:
     if (hy, wy) != (heads, dv):
         raise ValueError(f"dy must have shape {(*g.shape, dv)}")
     lib = load()
-    need = _size(lib.laplex_attend_workspace(n, *sizes, kind, 1), "laplex_attend_backward")
+    need = _size(lib.laplex_attend_workspace(n, seqs, *sizes, kind, 1), "laplex_attend_backward")
     if not isinstance(states, torch.Tensor):
         raise TypeError("states must be those of laplex_attend(keep=True)")
-    _flat(states, "states", torch.float32, (lib.laplex_attend_states(n, heads, dk, dv),), dev)
+    _flat(states, "states", torch.float32, (lib.laplex_attend_states(n, seqs, heads, dk, dv),), dev)
     _flat(dfinal, "dfinal", torch.float32, (seqs, heads, dk, dv), dev)
     s, ctx = _launch(stream, dev, q, k, v, g, dy, states, offsets, h0, dfinal)
     out = {}

@@ -95,19 +95,19 @@ def test_nothing_to_do_is_ok():
 
 def test_attend_sizes():
     lib = lx.load()
-    assert lib.laplex_attend_states(1, 4, 64, 64) == lib.laplex_attend_states(0, 4, 64, 64) == 0
-    assert lib.laplex_attend_states(100000, 4, 64, 64) >= 4 * 64 * 64
-    need = lib.laplex_attend_workspace
-    assert need(10, 4, 4, 4, 4, 64, 64, 1, 0) == 0
+    states, need = lib.laplex_attend_states, lib.laplex_attend_workspace
+    assert states(1, 1, 4, 64, 64) == states(0, 1, 4, 64, 64) == 0
+    assert states(100000, 1, 4, 64, 64) >= 4 * 64 * 64
+    assert need(10, 1, 4, 4, 4, 4, 64, 64, 1, 0) == 0
     # states between chunks in both directions
-    assert need(128, 4, 4, 4, 4, 64, 64, 1, 1) >= 2 * 4 * 2 * 4 * 64 * 64
+    assert need(128, 1, 4, 4, 4, 4, 64, 64, 1, 1) >= 2 * 4 * 2 * 4 * 64 * 64
     # heads that share values take partial sums
-    assert need(128, 4, 4, 4, 1, 64, 64, 1, 1) >= need(128, 4, 4, 4, 4, 64, 64, 1, 1) + 4 * 4 * 128 * 64
-    for args in ((-1, 4, 4, 4, 4, 64, 64, 1, 0), (10, 0, 1, 1, 1, 64, 64, 1, 0), (10, 4, 3, 4, 4, 64, 64, 1, 0),
-                 (10, 4, 4, 4, 4, 0, 64, 1, 0), (10, 4, 4, 4, 4, 64, 1025, 1, 0), (10, 4, 4, 4, 4, 64, 64, 3, 0),
-                 (10, 4, 4, 4, 4, 64, 64, 1, 2)):
+    assert need(128, 1, 4, 4, 4, 1, 64, 64, 1, 1) >= need(128, 1, 4, 4, 4, 4, 64, 64, 1, 1) + 4 * 4 * 128 * 64
+    for args in ((-1, 1, 4, 4, 4, 4, 64, 64, 1, 0), (10, 0, 4, 4, 4, 4, 64, 64, 1, 0), (10, 1, 0, 1, 1, 1, 64, 64, 1, 0),
+                 (10, 1, 4, 3, 4, 4, 64, 64, 1, 0), (10, 1, 4, 4, 4, 4, 0, 64, 1, 0), (10, 1, 4, 4, 4, 4, 64, 1025, 1, 0),
+                 (10, 1, 4, 4, 4, 4, 64, 64, 3, 0), (10, 1, 4, 4, 4, 4, 64, 64, 1, 2)):
         assert need(*args) == -1
-    assert lib.laplex_attend_states(-1, 4, 64, 64) == lib.laplex_attend_states(5, 0, 64, 64) == -1
+    assert states(-1, 1, 4, 64, 64) == states(5, 1, 0, 64, 64) == states(5, 1 << 25, 4, 64, 64) == -1
 
 
 def test_binding_refuses_host_tensors_and_types():
