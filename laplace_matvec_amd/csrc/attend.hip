@@ -75,26 +75,26 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
     // slot i of a sequence: the state between its segments i and i + 1 (the
     // gradient there); before and past the sequence they are the edges
     const int64_t slot = t.first / A.segment + t.index + (MODE == kEnd ? 0 : -1) + (REV ? (MODE == kEnd ? -1 : 1) : 0);
-    float* seg_state = A.seg_states + ((slot * A.heads + h) * A.dkp + k0) * A.dvp + v0;
+    float* seg_state = A.seg_states + (slot * A.heads + h) * ((int64_t)A.dkp * A.dvp) + tile_at(kb * (DK / 16), vb * TB, A.dvp) + 4 * lane;
     const float* edge = REV ? A.dfinal : A.h0;  // [seqs][heads][dk][dv]
     const bool at_edge = REV ? is_last : is_first;
     const int64_t edge_at = ((t.group * A.heads + h) * A.dk + k0) * (int64_t)A.dv + v0;
 #pragma unroll
     for (int a = 0; a < TA; ++a)
 #pragma unroll
-        for (int b = 0; b < TB; ++b)
+        for (int b = 0; b < TB; ++b) {
+            acc[a][b] = f32x4{};
+            if (MODE == kEnd) continue;
+            if (!at_edge) {
+                acc[a][b] = *reinterpret_cast<const f32x4*>(seg_state + tile_at(wave * TA + a, b, A.dvp));
+            } else if (edge) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * (wave * TA + a) + g4 + r, col = 16 * b + l16;
-                float x = 0.f;
-                if (MODE != kEnd) {
-                    if (!at_edge)
-                        x = seg_state[(int64_t)row * A.dvp + col];
-                    else if (edge && row < kcols && col < vcols)
-                        x = edge[edge_at + (int64_t)row * A.dv + col];
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * (wave * TA + a) + g4 + r, col = 16 * b + l16;
+                    if (row < kcols && col < vcols) acc[a][b][r] = edge[edge_at + (int64_t)row * A.dv + col];
                 }
-                acc[a][b][r] = x;
             }
+        }
 
     const int64_t ldk = REV ? A.ldq : A.ldk, ldv = REV ? A.lddy : A.ldv;
     const T* kp = (const T*)(REV ? A.q : A.k) + h / (A.heads / (REV ? A.hq : A.hk)) * A.dk + k0;
@@ -180,15 +180,14 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
         if (MODE == kStore) {
             // slots between chunks, likewise
             const int64_t between = t.first / kC + (row - t.first) / kC - (REV ? 0 : 1);
-            float* to = (REV ? A.chunk_grads : A.chunk_states) + ((between * A.heads + h) * A.dkp + k0) * A.dvp + v0;
+            float* to = (REV ? A.chunk_grads : A.chunk_states) + (between * A.heads + h) * ((int64_t)A.dkp * A.dvp) +
+                        tile_at(kb * (DK / 16) + wave * TA, vb * TB, A.dvp) + 4 * lane;
             if (REV ? row + kC < t.end : row > t.first) {
 #pragma unroll
                 for (int a = 0; a < TA; ++a)
 #pragma unroll
                     for (int b = 0; b < TB; ++b)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            to[(int64_t)(16 * (wave * TA + a) + g4 + r) * A.dvp + 16 * b + l16] = acc[a][b][r];
+                        *reinterpret_cast<f32x4*>(to + tile_at(a, b, A.dvp)) = acc[a][b];
             }
         }
         if (MODE == kOut) {
@@ -300,7 +299,13 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
     if (MODE == kEnd && threadIdx.x == 0 && kb == 0 && vb == 0) A.seg_decays[slot * A.heads + h] = decay;
     float* end = MODE == kOut ? A.final : A.dh0;
     const bool write_edge = MODE != kEnd && end && (REV ? is_first : MODE == kOut && is_last);
-    if (MODE == kEnd || write_edge) {
+    if (MODE == kEnd) {
+#pragma unroll
+        for (int a = 0; a < TA; ++a)
+#pragma unroll
+            for (int b = 0; b < TB; ++b)
+                *reinterpret_cast<f32x4*>(seg_state + tile_at(wave * TA + a, b, A.dvp)) = acc[a][b];
+    } else if (write_edge) {
 #pragma unroll
         for (int a = 0; a < TA; ++a)
 #pragma unroll
@@ -308,10 +313,7 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int rr = 16 * (wave * TA + a) + g4 + r, col = 16 * b + l16;
-                    if (MODE == kEnd)
-                        seg_state[(int64_t)rr * A.dvp + col] = acc[a][b][r];
-                    else if (rr < kcols && col < vcols)
-                        end[edge_at + (int64_t)rr * A.dv + col] = acc[a][b][r];
+                    if (rr < kcols && col < vcols) end[edge_at + (int64_t)rr * A.dv + col] = acc[a][b][r];
                 }
     }
 }
@@ -324,7 +326,8 @@ __global__ __launch_bounds__(256) void lx_attend_scan(AttendArgs A)
     const int64_t block = (int64_t)A.dkp * A.dvp;
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // of [heads][dkp][dvp]
     if (i >= A.heads * block) return;
-    const int h = (int)(i / block), row = (int)(i % block / A.dvp), col = (int)(i % A.dvp);
+    const int h = (int)(i / block), tile = (int)(i % block >> 8), lane = (int)(i & 255) >> 2;
+    const int row = 16 * (tile / (A.dvp >> 4)) + 4 * (lane >> 4), col = 16 * (tile % (A.dvp >> 4)) + (lane & 15);
     const Ragged R{A.offsets, A.seqs, A.n, A.seq_len};
     const float* edge = REV ? A.dfinal : A.h0;
     for (int64_t q = blockIdx.y; q < A.seqs; q += gridDim.y) {
@@ -332,10 +335,10 @@ __global__ __launch_bounds__(256) void lx_attend_scan(AttendArgs A)
         if (end - first <= A.segment) continue;
         const int64_t count = (end - first + A.segment - 1) / A.segment - 1;
         f32x4 s = {};
-        if (edge && row < A.dk)
+        if (edge && col < A.dv)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (col + r < A.dv) s[r] = edge[((q * A.heads + h) * A.dk + row) * (int64_t)A.dv + col + r];
+                if (row + r < A.dk) s[r] = edge[((q * A.heads + h) * A.dk + row + r) * (int64_t)A.dv + col];
         // a slot is loaded while the one before it is worked out
         const int64_t slot0 = first / A.segment + (REV ? count - 1 : 0), step = REV ? -1 : 1;
         f32x4* p = reinterpret_cast<f32x4*>(A.seg_states + slot0 * A.heads * block + i);

@@ -116,8 +116,8 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     __shared__ alignas(16) E s_k[kC * PK];
     __shared__ alignas(16) E s_v[kC * PV];
     __shared__ alignas(16) E s_do[kC * PV];
-    __shared__ alignas(16) E s_s[N * DK * PV];  // S
-    __shared__ alignas(16) E s_t[N * DK * PV];  // S+
+    __shared__ alignas(16) E s_s[N * DV * PK];  // S, transposed
+    __shared__ alignas(16) E s_t[N * DV * PK];  // S+, transposed
     __shared__ alignas(16) E s_p[kC * PC];
     __shared__ alignas(16) E s_e[kC * PC];
     __shared__ alignas(16) Decays s_d;
@@ -167,32 +167,29 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     const bool is_first = t.index == 0, is_last = t.row + t.rows == t.end;
     const int64_t slot = t.first / kC + t.index;
     const int64_t size = (int64_t)A.dkp * A.dvp;
-    const float* slot_s = A.chunk_states + ((slot - 1) * A.heads + h0) * size + (int64_t)k0 * A.dvp;
-    const float* slot_t = A.chunk_grads + (slot * A.heads + h0) * size + (int64_t)k0 * A.dvp;
+    const float* slot_s = A.chunk_states + ((slot - 1) * A.heads + h0) * size + tile_at(k0 / 16, 0, A.dvp);
+    const float* slot_t = A.chunk_grads + (slot * A.heads + h0) * size + tile_at(k0 / 16, 0, A.dvp);
     const int64_t edge_at = ((t.group * A.heads + h0) * A.dk + k0) * (int64_t)A.dv;
-    const int at0 = threadIdx.x / (DV / 4), col0 = threadIdx.x % (DV / 4) * 4;  // of a thread's values of a state
-    constexpr int kStep = kGradThreads / (DV / 4);                             // rows to its next ones
-    const bool plain = A.dk == A.dkp && A.dv == A.dvp;  // edges look like slots
-    auto state_in = [&](f32x4 (&x)[NS], bool edge, const float* slots, const float* edges, int hl, int v0) {
-        if (!edge || (plain && edges)) {
-            const float* p = (edge ? edges + edge_at : slots) + hl * size + v0 + (at0 * A.dvp + col0);
-#pragma unroll
-            for (int u = 0; u < NS; ++u) x[u] = *reinterpret_cast<const f32x4*>(p + u * kStep * A.dvp);
-            return;
-        }
-        const float* p = edges + edge_at + hl * ((int64_t)A.dk * A.dv) + v0;
-        const int cols = A.dv - v0;
+    // a thread's values: four of tile wave + 8 u of the block, row by row of tiles
+    constexpr int kAcross = DV / 16;
+    auto state_in = [&](f32x4 (&x)[NS], const float* slots, int hl, int v0) {
+        const float* p = slots + hl * size + v0 * 16 + 4 * lane;
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
-            x[u] = f32x4{};
-            if (!edges) continue;
-            const int row = at0 + u * kStep;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {  // what is not there is read from the last that is
-                const float y = p[(row < kcols ? row : kcols - 1) * A.dv + (col0 + r < cols ? col0 + r : cols - 1)];
-                x[u][r] = row < kcols && col0 + r < cols ? y : 0.f;
-            }
+            const int tile = wave + u * (kGradThreads / 64);
+            x[u] = *reinterpret_cast<const f32x4*>(p + tile_at(tile / kAcross, tile % kAcross, A.dvp));
         }
+    };
+    // The same from an edge, where it is used: once or twice in a sequence.
+    auto at_edge = [&](const float* edges, int hl, int v0, int row, int col) {
+        f32x4 x = {};
+        if (edges && v0 + col < A.dv) {
+            const float* p = edges + edge_at + hl * ((int64_t)A.dk * A.dv) + v0 + col;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (row + r < kcols) x[r] = p[(int64_t)(row + r) * A.dv];
+        }
+        return x;
     };
     RowTile<T, DV, WHOLE, kGradThreads> tv, td;
     f32x4 ts[NS], tt[NS];
@@ -204,8 +201,8 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         const int v0 = vb * DV, vcols = A.dv - v0;
         tv.load(vp + hv * A.dv + v0, A.ldv, rows, vcols);
         td.load(dp + hl * A.dv + v0, A.lddy, rows, vcols);
-        state_in(ts, is_first, slot_s, A.h0, hl, v0);
-        state_in(tt, is_last, slot_t, A.dfinal, hl, v0);
+        if (!is_first) state_in(ts, slot_s, hl, v0);
+        if (!is_last) state_in(tt, slot_t, hl, v0);
         if (wave == 0) tg = gp[hl];
     };
     auto put_state = [&](const f32x4& x, E* s, int row, int col) {
@@ -218,7 +215,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
             for (int m = 0; m < N; ++m) w[m][r] = e[m];
         }
 #pragma unroll
-        for (int m = 0; m < N; ++m) *reinterpret_cast<V4*>(&s[(m * DK + row) * PV + col]) = w[m];
+        for (int m = 0; m < N; ++m) *reinterpret_cast<V4*>(&s[(m * DV + col) * PK + row]) = w[m];
     };
     {
         RowTile<T, DK, WHOLE, kGradThreads> a, b;
@@ -229,18 +226,6 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         b.put(s_k, rows, kcols);
     }
     __syncthreads();
-    const int i = w16 + l16;
-    // scores, transposed: column i, rows j = 16 jt + g4 + r
-    f32x4 score[4] = {};
-    if (side == 0) {
-#pragma unroll
-        for (int jt = 0; jt < 4; ++jt)
-            if (16 * jt <= w16)
-#pragma unroll
-                for (int kk = 0; kk < DK / 32; ++kk)
-                    score[jt] = mma(frag_along(s_k + (16 * jt + l16) * PK + 32 * kk + 2 * g4),
-                                    frag_along(s_q + i * PK + 32 * kk + 2 * g4), score[jt]);
-    }
     // dq, or dk: rows w16 + g4 + r, columns 16 c + l16
     f32x4 acc[DK / 16] = {};
     float dg = 0.f;  // wave 0: row `lane`
@@ -249,10 +234,9 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
     for (;; flip ^= 1) {
         // Places worked out anew each time: kept for all heads they would take
         // the registers that the next head's values need.
-        int here = lane, thread = threadIdx.x;
-        asm volatile("" : "+v"(here), "+v"(thread));
+        int here = lane;
+        asm volatile("" : "+v"(here));
         const int g4 = 4 * (here >> 4), l16 = here & 15, i = w16 + l16;
-        const int at0 = thread / (DV / 4), col0 = thread % (DV / 4) * 4;
         const int v0 = vb * DV, vcols = A.dv - v0;
         const bool ends_head = vb + 1 == nvb;
         const bool more = !(ends_head && hl + 1 == A.loop);
@@ -262,10 +246,14 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         float z = 0.f;
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
-            put_state(ts[u], s_s, at0 + u * kStep, col0);
-            put_state(tt[u], s_t, at0 + u * kStep, col0);
+            const int tile = wave + u * (kGradThreads / 64);
+            const int row = 16 * (tile / kAcross) + g4, col = 16 * (tile % kAcross) + l16;
+            const f32x4 x = is_first ? at_edge(A.h0, hl, v0, row, col) : ts[u];
+            const f32x4 y = is_last ? at_edge(A.dfinal, hl, v0, row, col) : tt[u];
+            put_state(x, s_s, row, col);
+            put_state(y, s_t, row, col);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) z += ts[u][r] * tt[u][r];
+            for (int r = 0; r < 4; ++r) z += x[r] * y[r];
         }
         z = sum16(z);
         z += __shfl_xor(z, 16);
@@ -285,10 +273,10 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                 f32x4 x = {};
 #pragma unroll
                 for (int kk = 0; kk < DV / 32; ++kk) {
-                    const Frag<E> f = frag_along(s_do + i * PV + 32 * kk + 2 * g4);
+                    const Frag<E> f = frag_along_split(s_do + i * PV + 32 * kk);
 #pragma unroll
                     for (int m = 0; m < N; ++m)
-                        x = mma(f, frag_along(s_s + (m * DK + 16 * c + l16) * PV + 32 * kk + 2 * g4), x);
+                        x = mma(f, frag_across(s_s + (m * DV + 32 * kk) * PK + 16 * c, PK), x);
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -306,7 +294,14 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                 V4 p4 = {}, e4 = {};
                 f32x4 w = {};
                 if (16 * jt <= w16) {
-                    f32x4 x = {};
+                    // scores and dy . v, transposed: column i, rows j = 16 jt + g4 + r.
+                    // Scores are made again for every head that shares them:
+                    // registers are short.
+                    f32x4 x = {}, score = {};
+#pragma unroll
+                    for (int kk = 0; kk < DK / 32; ++kk)
+                        score = mma(frag_along(s_k + (16 * jt + l16) * PK + 32 * kk + 2 * g4),
+                                    frag_along(s_q + i * PK + 32 * kk + 2 * g4), score);
 #pragma unroll
                     for (int kk = 0; kk < DV / 32; ++kk)
                         x = mma(frag_along(s_v + (16 * jt + l16) * PV + 32 * kk + 2 * g4),
@@ -318,7 +313,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                         const int j = 16 * jt + g4 + r;
                         const bool on = j <= i && j >= last_i;
                         const float d = A.scale * s_d.between(hi_i, lo_i, hi[r], lo[r]);
-                        const float p = on ? score[jt][r] * d : 0.f;
+                        const float p = on ? score[r] * d : 0.f;
                         p4[r] = (E)p;
                         e4[r] = (E)(on ? x[r] * d : 0.f);
                         w[r] = on && j < i ? p * x[r] : 0.f;
@@ -353,10 +348,10 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                 f32x4 x = {};
 #pragma unroll
                 for (int kk = 0; kk < DV / 32; ++kk) {
-                    const Frag<E> f = frag_along(s_v + i * PV + 32 * kk + 2 * g4);
+                    const Frag<E> f = frag_along_split(s_v + i * PV + 32 * kk);
 #pragma unroll
                     for (int m = 0; m < N; ++m)
-                        x = mma(f, frag_along(s_t + (m * DK + 16 * c + l16) * PV + 32 * kk + 2 * g4), x);
+                        x = mma(f, frag_across(s_t + (m * DV + 32 * kk) * PK + 16 * c, PK), x);
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -375,10 +370,10 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     f32x4 x = {};
 #pragma unroll
                     for (int kk = 0; kk < DK / 32; ++kk) {
-                        const Frag<E> f = frag_along_split(s_k + i * PK + 32 * kk);
+                        const Frag<E> f = frag_along(s_k + i * PK + 32 * kk + 2 * g4);
 #pragma unroll
                         for (int m = 0; m < N; ++m)
-                            x = mma(f, frag_across(s_t + (m * DK + 32 * kk) * PV + 16 * b, PV), x);
+                            x = mma(f, frag_along(s_t + (m * DV + 16 * b + l16) * PK + 32 * kk + 2 * g4), x);
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) dv[b][r] = out[r] == 0.f ? 0.f : out[r] * x[r];

@@ -24,6 +24,12 @@ struct Compute<bf16_t> { typedef bf16_t E; static constexpr int kTerms = 2; };
 template <class E>
 constexpr int kPad = 16 / (int)sizeof(E);
 
+// States between chunks and segments are kept as their results lie in
+// registers, so that a wave moves a tile of 16 x 16 in one piece: tile (kt, vt)
+// of a head's [dkp][dvp] is 64 lanes of four values, rows 16 kt + 4 (lane /
+// 16) + r, column 16 vt + lane % 16.
+__device__ __forceinline__ int64_t tile_at(int kt, int vt, int dvp) { return ((int64_t)kt * (dvp >> 4) + vt) * 256; }
+
 // 8 neighbours from p on, of which `count` are there (0 past them).
 template <class T>
 __device__ __forceinline__ Pack<T, 8> load8(const T* p, int64_t count)
