@@ -284,7 +284,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     u[r] += x[r] * (float)s_q[(w16 + g4 + r) * PK + 16 * c + l16];
                     acc[c][r] += x[r];
                 }
-                if (c & 1) __builtin_amdgcn_sched_barrier(0);  // not more fragments at a time than registers
+                if ((c & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // not more fragments at a time than registers
             }
             const float hi_i = s_d.hi[i], lo_i = s_d.lo[i];
             const int last_i = s_d.last[i];
@@ -359,7 +359,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     u[r] += x[r] * (float)s_k[(w16 + g4 + r) * PK + 16 * c + l16];
                     acc[c][r] += x[r];
                 }
-                if (c & 1) __builtin_amdgcn_sched_barrier(0);
+                if ((c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) u[r] = sum16(u[r]);
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (32 * s <= w16) acc[c] = mma(fe[s], frag_across(s_k + 32 * s * PK + 16 * c, PK), acc[c]);
-                if (c & 1) __builtin_amdgcn_sched_barrier(0);
+                if ((c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
             }
         } else {
 #pragma unroll

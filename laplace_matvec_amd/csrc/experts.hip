@@ -228,14 +228,13 @@ __device__ __forceinline__ void to_lds(const void* base, uint32_t off, void* s)
 template <class T, int ROWS, bool ALONG, int THREADS, bool DMA>
 struct Mover {
     typedef Lines<ROWS, ALONG> L;
-    static constexpr int kAll = ROWS * kK / 8, kVecs = (kAll + THREADS - 1) / THREADS;
-    static_assert(kAll % 64 == 0, "whole waves");
+    static constexpr int kVecs = ROWS * kK / 8 / THREADS;
+    static_assert(kVecs * THREADS * 8 == ROWS * kK, "whole vectors for every thread");
     // vectors of wave w, j-th: 64 from here on
     static __device__ __forceinline__ int first(int j)
     {
         return (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kVecs + j) * 64;
     }
-    static __device__ __forceinline__ bool has(int j) { return kAll % THREADS == 0 || first(j) < kAll; }
     const T* base;    // first row, first step
     int64_t ld;
     int rows;         // rows that are there
@@ -264,7 +263,6 @@ struct Mover {
     // Vector j of the step whose contraction starts at k0, of k in all.
     __device__ __forceinline__ void load(int j, int64_t k0, int64_t k, T* s)
     {
-        if (!has(j)) return;
         const T* p = base + (ALONG ? k0 : k0 * ld);
         if constexpr (DMA) {
             const int64_t left = k - k0;
@@ -294,7 +292,7 @@ struct Mover {
         if constexpr (!DMA) {
 #pragma unroll
             for (int j = 0; j < kVecs; ++j)
-                if (has(j)) *reinterpret_cast<Pack<T, 8>*>(s + (first(j) + (threadIdx.x & 63)) * 8) = r[j];
+                *reinterpret_cast<Pack<T, 8>*>(s + (first(j) + (threadIdx.x & 63)) * 8) = r[j];
         }
     }
 };
@@ -394,25 +392,19 @@ __device__ __forceinline__ void tile_products(int64_t lda, int64_t ldb, int64_t 
 #pragma unroll
                 for (int j = 0; j < TN; ++j) fb[0][j] = LB::read(sb, n0 + 16 * j, 0);
                 fa[0][0] = LA::read(sa, m0, 0);
-                if (TM > 1) fa[0][1] = LA::read(sa, m0 + 16, 0);
+                fa[0][1] = LA::read(sa, m0 + 16, 0);
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int i = 0; i < TM; ++i) {
                         __builtin_amdgcn_sched_barrier(0);
-                        if (TM == 1) {
-                            if (s == 0) {
-                                fa[1][0] = LA::read(sa, m0, 1);
-#pragma unroll
-                                for (int j = 0; j < TN; ++j) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
-                            }
-                        } else if (i + 2 < TM) {
+                        if (i + 2 < TM) {
                             fa[s][i + 2] = LA::read(sa, m0 + 16 * (i + 2), s);
                         } else if (s == 0) {
                             fa[1][i + 2 - TM] = LA::read(sa, m0 + 16 * (i + 2 - TM), 1);
 #pragma unroll
                             for (int j = 0; j < TN; ++j)
-                                if ((j < (TN + 1) / 2) == (i == TM - 2)) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
+                                if ((j < TN / 2) == (i == TM - 2)) fb[1][j] = LB::read(sb, n0 + 16 * j, 1);
                         }
                         constexpr int kEach = TM >= 8 ? 2 : VA + VB;
                         if (s == 0 && i * kEach < VA + VB && more) {
@@ -692,7 +684,6 @@ hipError_t tile_grad_go(const ExpertsArgs& a, bool dma, hipStream_t s)
 typedef Shape<256, 256, 2, 4> Large;
 typedef Shape<128, 128, 2, 2> Middle;
 typedef Shape<64, 64, 2, 2> Little;
-typedef Shape<16, 128, 1, 4> Small;
 
 // Tiles that a launch of shape S has work for, at most.
 template <class S>
@@ -707,14 +698,23 @@ hipError_t tiles_go(const ExpertsArgs& a, hipStream_t s)
 {
     const bool dma = a.in % 8 == 0 && (!a.transpose || a.out % 8 == 0) && lines16(a.x, a.ldx) && lines16(a.w, a.ldw) &&
                      a.pitch_w % 8 == 0;
-    const int64_t each = a.n / a.experts;  // rows of an expert
-    if (each > 16) {
-        if (each > 160 && tiles_of<Large>(a) >= 224) return tile_go<T, Large>(a, dma, s);
-        if (tiles_of<Middle>(a) >= 384) return tile_go<T, Middle>(a, dma, s);
-        return tile_go<T, Little>(a, dma, s);
-    }
-    if (!a.transpose && tiles_of<Small>(a) < 512) return few_go<T>(a, s);
-    return tile_go<T, Small>(a, dma, s);
+    // Rows of an expert.  us for 64 experts of 2048 x 2048, with each shape:
+    //   rows     few  Little  Middle  Large
+    //      1      92     126     130    130
+    //      8     127     127     130    130
+    //     16     161     128     130    132
+    //    100     779     167     146    151
+    //    192    1389     248     188    169
+    //   1024            966     669    526
+    // Fewer experts need smaller tiles to fill the card: 8 of them, rows 192:
+    // Little 27.7, Middle 29.6, Large 51.7; 400: 55, 37, 57; 1024: 115, 75, 66;
+    // rows 8: few 18.7, Little 21.6.  An expert with more than 16 rows is read
+    // twice by `few`: 512 rows unevenly on 128 experts 151, Little 143.
+    const int64_t each = a.n / a.experts;
+    if (!a.transpose && (each <= 2 || (each <= 8 && tiles_of<Little>(a) < 512))) return few_go<T>(a, s);
+    if (each > 160 && tiles_of<Large>(a) >= 224) return tile_go<T, Large>(a, dma, s);
+    if (each > 40 && tiles_of<Middle>(a) >= 256) return tile_go<T, Middle>(a, dma, s);
+    return tile_go<T, Little>(a, dma, s);
 }
 
 template <class T>

@@ -204,3 +204,66 @@ def test_another_stream(gpu):
         y = lx.laplex_experts(x, w, at, transpose=True, stream=s)
         side.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts,inner,outer", [
+    ([1000, 0, 517, 300], 200, 5400),      # whole and broken tiles of 256, a tail of the contraction; workgroups that stay
+    ([1000, 0, 517, 300], 72, 5400),       # the same where each has one tile
+    ([257, 1, 700], 203, 6301),            # odd widths, by registers
+    ([90, 0, 260, 41, 7, 130, 128, 150], 136, 3080),  # tiles of 128
+    ([90, 0, 260, 41, 7, 130, 128, 150], 131, 3001),
+])
+def test_larger_tiles(gpu, dtype, transpose, counts, inner, outer):
+    x, w, dy, offsets = make(gpu, dtype, counts, inner, outer, transpose, past=3)
+    y, dx, _ = ref.experts(x, w, offsets, transpose, dy)
+    at = on(gpu, offsets)
+    assert_within(lx.laplex_experts(x, w, at, transpose=transpose), *y)
+    assert_within(lx.laplex_experts_backward(x, w, dy, at, transpose=transpose, want=("dx",))["dx"], *dx)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts,inner,outer", [([300, 0, 517, 256], 2056, 2104), ([60, 0, 5, 33], 2056, 2104),
+                                                ([300, 0, 517, 256], 2051, 2103)])
+def test_larger_tiles_of_the_matrices_gradient(gpu, dtype, transpose, counts, inner, outer):
+    x, w, dy, offsets = make(gpu, dtype, counts, inner, outer, transpose)
+    _, _, dw = ref.experts(x, w, offsets, transpose, dy)
+    assert_within(lx.laplex_experts_backward(x, w, dy, on(gpu, offsets), transpose=transpose, want=("dw",))["dw"], *dw)
+
+
+def test_many_experts(gpu):
+    """More experts than lanes: the largest number that routing gives, rows for some of them."""
+    gen = torch.Generator().manual_seed(3)
+    counts = (torch.rand(4096, generator=gen) < 0.05).int() * torch.randint(1, 40, (4096,), generator=gen)
+    x, w, dy, offsets = make(gpu, torch.bfloat16, counts.tolist(), 40, 24, False)
+    check(x, w, dy, offsets, False, gpu)
+
+
+def test_many_experts_in_larger_tiles(gpu):
+    counts = [0] * 130 + [45, 300, 0, 129] * 50
+    x, w, dy, offsets = make(gpu, torch.bfloat16, counts, 40, 264, False)
+    check(x, w, dy, offsets, False, gpu)
+
+
+def test_offsets_past_2_31_bytes(gpu):
+    """Rows, results and matrices further than 32 bits from the start of their arrays; whole numbers throughout."""
+    n, width, experts = 1 << 19, 2048, 700
+    x = torch.arange(n, device=gpu, dtype=torch.int32).remainder_(7).to(torch.bfloat16)[:, None].expand(n, width).contiguous()
+    w = torch.zeros(experts, 8, width, dtype=torch.bfloat16, device=gpu)
+    w[:, :, 0] = torch.arange(experts, device=gpu).remainder(5)[:, None].to(torch.bfloat16)
+    w[:, :, width - 1] = 1
+    at = torch.full((experts + 1,), n, dtype=torch.int32, device=gpu)
+    at[0], at[1:experts - 1] = 0, 100  # the first expert has 100 rows, the last but one all others
+    at[experts - 1] = n
+    y = lx.laplex_experts(x, w, at)
+    by = torch.full((n, 1), float((experts - 2) % 5 + 1), device=gpu)
+    by[:100] = 1.0
+    assert torch.equal(y.float(), (x[:, :1].float() * by).expand(n, 8))
+    dw = lx.laplex_experts_backward(x, w, y, at, want=("dw",))["dw"]
+    assert not dw[1:experts - 2].any() and not dw[experts - 1].any()
+    total = (x[100:, 0].double() * y[100:, 0].double()).sum()
+    assert torch.allclose(dw[experts - 2].double(), total, rtol=2.0 ** -8, atol=0)
+    dx = lx.laplex_experts_backward(x, w, y, at, want=("dx",))["dx"]
+    assert torch.equal(dx[:, width - 1].float(), 8 * y[:, 0].float())
