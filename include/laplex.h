@@ -444,8 +444,9 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  *             aligned.
  * Float32 and float16 rows are multiplied in float32.  With bfloat16 rows,
  * what enters a product is bfloat16 too: scores, states for y and gradients
- * of scores rounded once, rows times decays for the states and states for
- * gradients in two terms, 16 bits; the states themselves stay float32.
+ * of scores rounded once, states for gradients in two terms (16 bits), rows
+ * times decays for the states in three (24); the states themselves stay
+ * float32.
  * A row that holds inf or NaN reaches its own and later rows of its heads and
  * sequence, up to a decay of 0; they may get NaN where inf is due.  In the
  * backward pass it may reach every gradient of its heads and sequence.

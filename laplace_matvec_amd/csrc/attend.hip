@@ -29,7 +29,7 @@ template <class T, class TG, int DK, int DV, int MODE, bool REV, bool WHOLE>
 __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof(typename Compute<T>::E) == 4 ? 1 : 2) void lx_attend_sweep(AttendArgs A)
 {
     typedef typename Compute<T>::E E;
-    constexpr int NU = Compute<T>::kTerms;  // terms of a row times its decay
+    constexpr int NU = sizeof(E) == 2 ? 3 : 1;  // terms of a row times its decay: all of its bits
     constexpr int TB = DV / 16;
     constexpr int PK = DK + kPad<E>, PV = DV + kPad<E>;
     constexpr int TA = DK / 64;  // 16-row tiles of the state per wave

@@ -12,9 +12,14 @@ constexpr int kC = kAttendChunk;  // rows of a chunk: one per lane
 
 // What products are made in for storage type T: bfloat16 rows as they are,
 // other types as float32 (float16's range is too small for states and
-// scores).  Values that are made here (states, rows times decays) go into
-// bfloat16 products in two terms, the value's rounding and the rounding of
-// what is left: 17 bits, so that float32 results keep 5 digits.
+// scores).  What is made here goes into bfloat16 products rounded, in as many
+// terms as its results need:
+//     scores, states for y         1   they reach bfloat16 results only, and
+//                                      add less to them than their own rounding
+//     states for gradients         2   dg is float32: off by 2e-6 of itself
+//                                      (three planes do not fit in LDS)
+//     rows times decays (states)   3   final states and dh0 are float32: off by
+//                                      2e-7 of themselves, 1.6e-6 with two terms
 template <class T>
 struct Compute { typedef float E; static constexpr int kTerms = 1; };
 template <>
@@ -195,12 +200,15 @@ struct Decays {
     }
 };
 
-// x in terms: term 0 the rounding of x, term 1 of what is left.
+// x in terms: each the rounding of what the ones before it leave.
 template <class E, int N>
 __device__ __forceinline__ void split(float x, E (&t)[N])
 {
-    t[0] = (E)x;
-    if constexpr (N == 2) t[1] = (E)(x - (float)t[0]);
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+        t[m] = (E)x;
+        if (m + 1 < N) x -= (float)t[m];
+    }
 }
 
 }  // namespace lx

@@ -115,10 +115,10 @@ def _attend(q, k, v, g, offsets, h0, scale, dy, dfinal, weigh):
 def attend(q, k, v, g, offsets, h0=None, scale=1.0, dy=None, dfinal=None):
     """{name: (value, bound)}.
 
-    With bfloat16 rows scores are rounded once (2^-8), which reaches y, dq, dk
-    and dv; states and rows times decays keep two terms, what is left of the
-    second is 2^-16 of the value, and at most two such values meet in a
-    result.  Float32 sums: over dk or dv, over 64 rows, over a row's chunks
+    With bfloat16 rows scores (and states for y) are rounded once (2^-8), which
+    reaches y, dq, dk and dv; states for gradients keep two terms, what is
+    left of the second is 2^-16 of the value, rows times decays at least as
+    many, and at most two such values meet in a result.  Float32 sums: over dk or dv, over 64 rows, over a row's chunks
     (three roundings each), and sums of at most 16 lanes and 8 partial
     results (planes of blocks, shared heads)."""
     kind = q.dtype
