@@ -5,10 +5,25 @@
 //     y_r   = W_e x_r                  rows: n x out, contraction in
 //     dx_r  = W_e^T dy_r               rows: n x in, contraction out
 //     dW_e  = sum over r of dy_r x_r^T  out x in for each expert, contraction its rows
-// Row tiles of one expert are numbered in closed form, first tile
-// offsets[e] / BM + e, so a workgroup finds its expert by a search in the
-// offsets and no list of tiles is made; what the numbering leaves over (less
-// than one tile per expert) ends at once.
+// A workgroup finds its expert by a search in the offsets (lx_ragged.h), so
+// no list of tiles is made and nothing is launched before.
+//
+// Three families of kernels:
+//   lx_experts_tile   16-bit values, tiles of 256 x 256, 128 x 128 or 64 x 64
+//     through LDS.  Bound by the matrix units' rate under the power limit:
+//     8 x 4096 rows, 4096 x 4096 bf16: 905 us, 1.21 PFLOP/s; a library product
+//     of all rows with one matrix 700 (steps of 1.6 us a tile against 1.3: it
+//     reads a third less LDS with four waves of 128 x 128, which lost here, 890
+//     against 850 in one matrix, and waits less).  Also tried for one matrix
+//     of 32768 x 4096 x 4096: matrix instructions of 32 x 32 x 16 980, four
+//     steps of 32 in LDS 1000, two workgroups of 128 x 256 a CU 1030, one half
+//     of the waves multiplying while the other reads LDS 845 to 860, the same
+//     as all of them together.
+//   lx_experts_few    a few rows: bound by memory, 64 x 2048 x 2048 read for
+//     one row each in 92 us, 5.8 TB/s; 4 rows of 16 experts 5.7 us of kernel.
+//   lx_experts_any    float32, any layout: 4096 x 512 x 769 in 8 experts 49 us,
+//     66 TFLOP/s of the 154 of a large library product: short of workgroups
+//     and of LDS reads ahead of their products.
 #include "lx_device.h"
 #include "lx_internal.h"
 #include "lx_mma.h"
