@@ -448,8 +448,9 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  * times decays for the states in three (24); the states themselves stay
  * float32.
  * A row that holds inf or NaN reaches its own and later rows of its heads and
- * sequence, up to a decay of 0; they may get NaN where inf is due.  In the
- * backward pass it may reach every gradient of its heads and sequence.
+ * sequence, until the decays since it, or those of a chunk of 64 rows, are 0
+ * in float32; they may get NaN where inf is due.  In the backward pass it may
+ * reach every gradient of its heads and sequence.
  *
  * laplex_attend_backward -- gradients: dy (y's layout) and dfinal (or NULL)
  *   in; dq, dk_out, dv_out (q's, k's and v's layout, summed over the heads
