@@ -21,9 +21,10 @@
 // lx_attend_sum adds the planes in their order.
 //
 // 32768 rows, 32 heads of 128 x 64 on 8 query and key heads, bf16: 640 us for
-// 1.5 GB (S and S+ 1.1 of them).  Bound by latency: 66 % of the waves' time is
+// 1.5 GB (S and S+ 1.1 of them).  Bound by latency: half of the waves' time is
 // waiting, at one workgroup of eight waves a CU (144 KB of LDS) and three
-// barriers a head.  One workgroup of four waves doing both sides in turn,
+// barriers a head; rows padded so that no two lines of a transposing read
+// share banks changed nothing.  One workgroup of four waves doing both sides in turn,
 // loads where they are used: 1630; addresses worked out per value instead of
 // per head 1211 (of eight waves); kept across heads, which spills, 760.
 #include "lx_attend.h"
