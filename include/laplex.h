@@ -447,10 +447,11 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  * of scores rounded once, states for gradients in two terms (16 bits), rows
  * times decays for the states in three (24); the states themselves stay
  * float32.
- * A row that holds inf or NaN reaches its own and later rows of its heads and
- * sequence, until the decays since it, or those of a chunk of 64 rows, are 0
- * in float32; they may get NaN where inf is due.  In the backward pass it may
- * reach every gradient of its heads and sequence.
+ * A row that holds inf or NaN (a decay of that kind in float32 too) reaches
+ * its own and later rows of its heads and sequence, until one decay after it,
+ * or the product of all decays of a later chunk of 64 rows (counted from the
+ * sequence's first), is 0 in float32; they may get NaN where inf is due.  In
+ * the backward pass it may reach every gradient of its heads and sequence.
  *
  * laplex_attend_backward -- gradients: dy (y's layout) and dfinal (or NULL)
  *   in; dq, dk_out, dv_out (q's, k's and v's layout, summed over the heads

@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
         }
         if (ci + 1 < chunks) fetch(ci + 1);
         const float whole = s_d.into[kC - 1];
-        if (MODE == kEnd) decay *= whole;
+        if (MODE == kEnd) decay = whole == 0.f ? 0.f : decay * whole;  // also after NaN
         if (MODE == kStore) {
             // slots between chunks, likewise
             const int64_t between = t.first / kC + (row - t.first) / kC - (REV ? 0 : 1);

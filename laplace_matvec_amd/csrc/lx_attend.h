@@ -160,7 +160,9 @@ struct RowTile {
 // Decays of a chunk, worked out by one wave with a row per lane.  Sums of the
 // logarithms are float64, handed on in two floats, so that a difference of two
 // is as good after thousands of strong decays as at the start.  A decay that
-// is 0 in float32 cuts: rows before it are gone for the rows from it on.
+// is 0 in float32 cuts: rows before it are gone for the rows from it on.  One
+// that is NaN, or infinite in float32, is left out of the sums too, which would
+// carry it past the next cut: the sums from it up to there are set to NaN.
 struct Decays {
     float hi[kC], lo[kC];  // sums of log2 of the decays up to each row, cuts left out
     float into[kC];        // what a row sees of the state before the chunk
@@ -171,16 +173,18 @@ struct Decays {
     {
         const int lane = threadIdx.x & 63;
         const bool cut = g < -103.972f;  // e^g < 2^-150
-        const uint64_t cuts = __ballot(cut);
-        double sum = cut ? 0.0 : (double)g * 1.4426950408889634074;
+        const bool bad = !(g < 88.72284f);  // e^g >= 2^128, or NaN
+        const uint64_t cuts = __ballot(cut), bads = __ballot(bad);
+        double sum = cut || bad ? 0.0 : (double)g * 1.4426950408889634074;
         sum += dpp_move<0x111>(sum, 0.0);
         sum += dpp_move<0x112>(sum, 0.0);
         sum += dpp_move<0x114>(sum, 0.0);
         sum += dpp_move<0x118>(sum, 0.0);
         sum += dpp_move<0x142, 0xA>(sum, 0.0);
         sum += dpp_move<0x143, 0xC>(sum, 0.0);
+        const uint64_t upto = (2ull << lane) - 1, mine = cuts & upto;
+        if (bads & upto && (bads & upto) > mine) sum = __builtin_nan("");  // the last bad one lies past the last cut
         const double total = __shfl(sum, 63);
-        const uint64_t mine = cuts & ((2ull << lane) - 1);
         hi[lane] = (float)sum;
         lo[lane] = (float)(sum - (double)(float)sum);
         last[lane] = mine ? 63 - __builtin_clzll(mine) : -1;
