@@ -435,7 +435,9 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  *             the decays.  Where exp(g) is 0 in float32 the state is
  *             forgotten, whatever it held.  Decays may be above 1 as long as
  *             their products along any stretch of a sequence stay in
- *             float32's range.
+ *             float32's range.  Products down to its smallest number (2^-149)
+ *             count; a row or state times one may be lost where the result
+ *             is below 2^-126.
  *   h0, final float32 [seqs][heads][dk][dv], states before the first and after
  *             the last rows, or NULL (h0: 0).
  *   states    float32[laplex_attend_states(n, seqs, heads, dk, dv)] or NULL: what

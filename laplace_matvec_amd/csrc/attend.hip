@@ -416,7 +416,7 @@ __global__ __launch_bounds__(256) void lx_attend_step(AttendStepArgs A)
     const T* q = (const T*)A.q + b * A.ldq + h / (A.heads / A.hq) * A.dk;
     const T* k = (const T*)A.k + b * A.ldk + h / (A.heads / A.hk) * A.dk;
     const float g = has ? (float)((const TG*)A.g)[b * A.ldg + h] : 0.f;
-    const float a = g < -103.972f ? 0.f : expf(g);
+    const float a = is_cut(g) ? 0.f : exp2_whole((double)g * kLog2e);
     float* state = A.state + (has ? slot * A.heads + h : 0) * (int64_t)A.dk * A.dv;
     // column groups of the row, at most 64 at a time
     const int groups = (A.dv + V - 1) / V;

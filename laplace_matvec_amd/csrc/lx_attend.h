@@ -157,14 +157,31 @@ struct RowTile {
     }
 };
 
+constexpr double kLog2e = 1.4426950408889634074;
+
+// 2^x: from x in two floats, as one is off by 2^-24 of x, and also where it is
+// below the smallest normal number, which v_exp_f32 makes 0.
+__device__ __forceinline__ float exp2_whole(double x)
+{
+    const float hi = (float)x, lo = (float)(x - (double)hi);
+    const bool deep = hi < -126.f;
+    const float e = __builtin_amdgcn_exp2f(deep ? hi + 64.f : hi) * __builtin_fmaf(lo, 0.69314718f, 1.f);
+    return e * (deep ? 0x1p-64f : 1.f);
+}
+
+// The logarithm of a decay that is 0 in float32: e^g <= 2^-150.
+__device__ __forceinline__ bool is_cut(float g) { return g < -103.97208f; }
+
 // Decays of a chunk, worked out by one wave with a row per lane.  Sums of the
 // logarithms are float64, handed on in two floats, so that a difference of two
 // is as good after thousands of strong decays as at the start.  A decay that
 // is 0 in float32 cuts: rows before it are gone for the rows from it on.  One
 // that is NaN, or infinite in float32, is left out of the sums too, which would
 // carry it past the next cut: the sums from it up to there are set to NaN.
+// Products of decays are float32 numbers, subnormal ones included, as those of
+// the single-token form are.
 struct Decays {
-    float hi[kC], lo[kC];  // sums of log2 of the decays up to each row, cuts left out
+    float hi[kC], lo[kC];  // half the sums of log2 of the decays up to each row, cuts left out
     float into[kC];        // what a row sees of the state before the chunk
     float out[kC];         // what the state after the chunk holds of a row
     int last[kC];          // the last cut up to each row, -1 for none
@@ -172,10 +189,10 @@ struct Decays {
     __device__ __forceinline__ void make(float g)
     {
         const int lane = threadIdx.x & 63;
-        const bool cut = g < -103.972f;  // e^g < 2^-150
+        const bool cut = is_cut(g);
         const bool bad = !(g < 88.72284f);  // e^g >= 2^128, or NaN
         const uint64_t cuts = __ballot(cut), bads = __ballot(bad);
-        double sum = cut || bad ? 0.0 : (double)g * 1.4426950408889634074;
+        double sum = cut || bad ? 0.0 : (double)g * kLog2e;
         sum += dpp_move<0x111>(sum, 0.0);
         sum += dpp_move<0x112>(sum, 0.0);
         sum += dpp_move<0x114>(sum, 0.0);
@@ -185,22 +202,23 @@ struct Decays {
         const uint64_t upto = (2ull << lane) - 1, mine = cuts & upto;
         if (bads & upto && (bads & upto) > mine) sum = __builtin_nan("");  // the last bad one lies past the last cut
         const double total = __shfl(sum, 63);
-        hi[lane] = (float)sum;
-        lo[lane] = (float)(sum - (double)(float)sum);
+        hi[lane] = (float)(0.5 * sum);
+        lo[lane] = (float)(0.5 * sum - (double)(float)(0.5 * sum));
         last[lane] = mine ? 63 - __builtin_clzll(mine) : -1;
-        into[lane] = mine ? 0.f : __builtin_amdgcn_exp2f((float)sum);
+        into[lane] = mine ? 0.f : exp2_whole(sum);
         // a cut after this row takes it away; its own does not
-        out[lane] = (cuts >> lane) > 1 ? 0.f : __builtin_amdgcn_exp2f((float)(total - sum));
+        out[lane] = (cuts >> lane) > 1 ? 0.f : exp2_whole(total - sum);
     }
     // rows that see the state before the chunk, a bit each
     __device__ __forceinline__ unsigned long long sees_before() const
     {
         return __ballot(last[threadIdx.x & 63] < 0);
     }
-    // exp of the decays after row j up to row i >= j
+    // exp of the decays after row j up to row i >= j: the square of the root
     __device__ __forceinline__ float between(float hi_i, float lo_i, float hi_j, float lo_j) const
     {
-        return __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j));
+        const float root = __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j));
+        return root * root;
     }
 };
 
