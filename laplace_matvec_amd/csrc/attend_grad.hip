@@ -346,7 +346,11 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
             if (g4 == 0) s_row[i] = row_sum;
 #pragma unroll
             for (int r = 0; r < 4; ++r) u[r] = sum16(u[r]);
-            // the wave's own rows: no other wave touches them
+            // The wave's own rows, no other wave's; but other lanes stored them,
+            // which only a fence keeps before these reads.
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
             if (l16 == 0)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) s_row[w16 + g4 + r] += u[r];
