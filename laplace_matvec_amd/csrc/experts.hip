@@ -226,16 +226,14 @@ struct Lines {
 // 16 bytes a lane from base + off to LDS, lane after lane from s on.  By hand
 // because the compiler, which cannot tell the two tiles apart, would wait for
 // every such load before the next read of LDS; tile_product waits for them
-// itself before it hands a tile over.  No register is written.  A scalar
-// register that a vector instruction wrote may not be read here for five
-// cycles, and m0 not for one: the wait covers both.
+// itself before it hands a tile over.  No register is written; m0, which holds
+// the place in LDS, is an operand, so the compiler sets it and knows of it.  A
+// scalar register that a vector instruction wrote may not be read here for
+// five cycles, and m0 not for one: the wait covers both.
 __device__ __forceinline__ void to_lds(const void* base, uint32_t off, void* s)
 {
     const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)s;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(at), "v"(off), "s"(base)
-                 : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(at) : "memory");
 }
 
 // What a thread moves of a tile: kVecs vectors of 16 bytes a step, straight to
