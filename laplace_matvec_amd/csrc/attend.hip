@@ -66,9 +66,9 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
     const int kcols = A.dk - k0, vcols = A.dv - v0;  // how many are there
     if (t.group < 0) {
         if (MODE != kOut) return;
-        for (int i = threadIdx.x; i < t.rows * DV; i += kAttendThreads) {
+        for (int64_t i = threadIdx.x; i < (int64_t)t.rows * DV; i += kAttendThreads) {
             const int64_t row = t.row + i / DV;
-            const int c = i % DV;
+            const int c = (int)(i % DV);
             if (c >= vcols) continue;
             if (A.part)
                 A.part[(kb * A.n + row) * ((int64_t)A.heads * A.dv) + h * A.dv + v0 + c] = 0.f;
