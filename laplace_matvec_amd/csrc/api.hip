@@ -2128,7 +2128,7 @@ size_t attend_carve(lx::AttendArgs& A, char* base, bool backward, bool own_state
     A.seg_grads = take(slots * one);
     A.chunk_states = take(n / lx::kAttendChunk * one);
     A.chunk_grads = take(n / lx::kAttendChunk * one);
-    const size_t nkb = (size_t)(A.dkp / A.grad_block_k);
+    const size_t nkb = (size_t)lx::attend_grad_blocks(A);
     const size_t rq = A.heads / A.hq / A.loop, rk = A.heads / A.hk / A.loop, rv = A.heads / A.hv * nkb;
     A.part_q = take(rq > 1 ? rq * n * A.hq * A.dk : 0);
     A.part_k = take(rk > 1 ? rk * n * A.hk * A.dk : 0);

@@ -487,7 +487,7 @@ hipError_t attend_grad_launch(const AttendArgs& a, int dtype, int gtype, hipStre
     if (e != hipSuccess || a.n == 0 || (!a.dq && !a.dkey && !a.dval && !a.dg)) return e;
     AttendArgs b = a;
     b.block_k = a.grad_block_k;
-    b.nkb = a.dkp / b.block_k;
+    b.nkb = attend_grad_blocks(a);
     switch (dtype) {
         case 0: e = grad_type<float, float>(b, s); break;
         case 1: e = gtype ? grad_type<bf16_t, bf16_t>(b, s) : grad_type<bf16_t, float>(b, s); break;

@@ -533,6 +533,9 @@ inline int attend_segment(int64_t n, int64_t seqs, int64_t parts)
     const int64_t r = rows < 128.0 ? 128 : rows > 1073741824.0 ? 1073741824 : (int64_t)rows;
     return (int)((r + kAttendChunk - 1) / kAttendChunk * kAttendChunk);
 }
+// Key blocks of the gradients.  The states' rows are padded to blocks of
+// block_k, so with smaller ones the last may be past dk: those have no work.
+inline int attend_grad_blocks(const AttendArgs& a) { return (a.dk + a.grad_block_k - 1) / a.grad_block_k; }
 // Whether a sequence may have more than one segment.
 inline bool attend_may_split(const AttendArgs& a) { return (a.offsets ? a.n : a.seq_len) > a.segment; }
 hipError_t attend_launch(const AttendArgs& a, int dtype, int gtype, hipStream_t s);

@@ -365,3 +365,10 @@ def test_another_stream(gpu):
         d = lx.laplex_attend_backward(*args, t["dy"], r.states, h0=t["h0"], dfinal=t["dfinal"], stream=s)
         side.synchronize()
         assert torch.equal(r.y, want["y"]) and all(torch.equal(d[name], want[name]) for name in ALL)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dk,dv", [(129, 24), (136, 64), (160, 64), (176, 40), (192, 128), (264, 8), (320, 72)])
+def test_key_widths_that_end_inside_the_states_blocks(gpu, dtype, dk, dv):
+    """States are padded to blocks of 128 keys; gradients of float32 and float16 rows go by blocks of 64."""
+    check(make(gpu, dtype, 150, 2, dk, dv, (2, 1, 2), seed=dk), None, gpu)

@@ -206,3 +206,15 @@ def test_experts_reference_gradient():
         got = ref.experts(x, w, offsets, transpose, dy)
         for (value, _), want in zip(got, (y.detach(), x.grad, w.grad)):
             assert torch.allclose(value, want, atol=1e-12)
+
+
+def test_gradients_take_no_planes_for_blocks_past_the_keys():
+    """float32 and float16 gradients go by key blocks of 64.  Between widths of the same padded states the scratch
+    grows by what a block takes: a plane of dv and one of dg."""
+    n, heads, dv = 4096, 2, 40
+    size = lambda dk, kind: lx.load().laplex_attend_workspace(n, 1, heads, heads, heads, heads, dk, dv, kind, 1)  # noqa: E731
+    plane = n * heads * dv * 4 + n * heads * 4
+    for kind in (0, 2):
+        assert size(256, kind) - size(192, kind) == size(512, kind) - size(448, kind) == plane
+        assert size(129, kind) == size(136, kind) == size(192, kind)
+    assert size(256, 1) == size(192, 1) == size(136, 1)  # bfloat16: blocks of 128
