@@ -372,3 +372,21 @@ def test_another_stream(gpu):
 def test_key_widths_that_end_inside_the_states_blocks(gpu, dtype, dk, dv):
     """States are padded to blocks of 128 keys; gradients of float32 and float16 rows go by blocks of 64."""
     check(make(gpu, dtype, 150, 2, dk, dv, (2, 1, 2), seed=dk), None, gpu)
+
+
+def test_digits_of_float32_results_of_bfloat16_rows(gpu):
+    """The relative L2 norm of the errors, which is that of independent errors and far below their worst case.
+
+    final, dh0: a row's decay is off by at most 2^-23 + 2^-24 (rms below 1e-7); the product with it and its three terms
+    by 2.5e-8 rms each (half a step of 2^-24, uniform, mean significand).  Over 300 rows the sums take 6 products for
+    each of 5 chunks, of at most 4 additions each, and 5 products with decays: 125 roundings of 2.5e-8 of partial
+    results whose squares grow in proportion, sqrt(125 / 2) * 2.5e-8 = 2e-7.  Together 2.3e-7; the bound is twice that.
+    Two terms leave 2^-17 of the binade at most, 1.6e-6 to 2.3e-6 rms, and do not pass.
+    dg: both states in two terms, 2.3e-6 each, meet in one product: 3.3e-6, and the bound is 1.5 times that.  One term
+    (2^-9 and more) does not pass."""
+    t = make(gpu, torch.bfloat16, 300, 4, 64, 64)
+    got = passes(t, None, gpu, 0.125)
+    want = ref.attend(t["q"], t["k"], t["v"], t["g"], [0, 300], t["h0"], 0.125, t["dy"], t["dfinal"])
+    off = {name: float((got[name].cpu().double() - want[name][0]).norm() / want[name][0].norm()) for name in got}
+    print(off)
+    assert off["final"] < 5e-7 and off["dh0"] < 5e-7 and off["dg"] < 5e-6, off

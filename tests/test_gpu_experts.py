@@ -267,3 +267,37 @@ def test_offsets_past_2_31_bytes(gpu):
     assert torch.allclose(dw[experts - 2].double(), total, rtol=2.0 ** -8, atol=0)
     dx = lx.laplex_experts_backward(x, w, y, at, want=("dx",))["dx"]
     assert torch.equal(dx[:, width - 1].float(), 8 * y[:, 0].float())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts,inner", [([1000, 0, 517, 300], 200), ([0, 600, 2, 0, 1200], 248), ([1500, 37], 1032)])
+def test_workgroups_that_take_several_tiles(gpu, dtype, transpose, counts, inner):
+    """y of 9000 columns and dx of as many: 36 tiles of 256 columns by 9 row tiles of experts (with one of no expert)
+    make 360, by 9 (two) 396 and by 7 (one) 288, for 256 workgroups that stay, as the contraction is at least 192.  Its
+    tail is 8 of 64 (200, 1032) or 56 (248); the tile after it is loaded during the step that has it."""
+    wide = 9000
+    before, past = (0, 3) if counts[0] else (70, 40)
+    x, w, dy, offsets = make(gpu, dtype, counts, inner, wide, transpose, before=before, past=past, seed=inner)
+    at = on(gpu, offsets)
+    assert_within(lx.laplex_experts(x, w, at, transpose=transpose), *ref.experts(x, w, offsets, transpose))
+    # the gradient of rows of `wide` values from dy of `inner`: the same tiles by the other orientation's kernel
+    w = w.transpose(1, 2).contiguous()
+    _, dx, dw = ref.experts(dy, w, offsets, transpose, x)
+    got = lx.laplex_experts_backward(dy, w, x, at, transpose=transpose)
+    assert_within(got["dx"], *dx)
+    assert_within(got["dw"], *dw)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_bad_rows_beside_tiles_that_are_cleared(gpu, transpose):
+    """The tail of a contraction is cleared in LDS while the next tile's first values arrive: rows of no expert between
+    two tiles of one workgroup, and rows that hold inf and NaN, reach nothing."""
+    x, w, _, offsets = make(gpu, torch.bfloat16, [1000, 0, 517, 300], 200, 9000, transpose, before=300, past=300)
+    at = on(gpu, offsets)
+    y0 = lx.laplex_experts(x, w, at, transpose=transpose)
+    assert not y0[:300].any() and not y0[offsets[-1]:].any()
+    x[:300], x[offsets[-1]:], x[700, 199] = float("nan"), float("inf"), float("inf")
+    y = lx.laplex_experts(x, w, at, transpose=transpose)
+    others = torch.arange(x.shape[0], device=gpu) != 700
+    assert torch.equal(y[others], y0[others]) and not torch.isfinite(y[700]).any()
