@@ -448,7 +448,11 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  * what enters a product is bfloat16 too: scores, states for y and gradients
  * of scores rounded once, states for gradients in two terms (16 bits), rows
  * times decays for the states in three (24); the states themselves stay
- * float32.
+ * float32.  y is then off by up to sqrt(2) times what rounding it costs
+ * (relative norms), final and dh0 by 2e-7, dg by 2e-6 where decays are weak:
+ * dg is a difference of sums over its chunk of 64 rows, and off by that part
+ * of the sum of their absolute terms, also where a strong decay leaves little
+ * of dg itself.
  * A row that holds inf or NaN (a decay of that kind in float32 too) reaches
  * its own and later rows of its heads and sequence, until one decay after it,
  * or the product of all decays of a later chunk of 64 rows (counted from the
@@ -459,7 +463,12 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  *   in; dq, dk_out, dv_out (q's, k's and v's layout, summed over the heads
  *   that share one), dg (g's, 0 where the decay is 0) and dh0 out, each or
  *   NULL.  q, k, v, g, h0 as in the forward pass, states from it (NULL if it
- *   has no values).  Scratch: laplex_attend_workspace(..., 1).
+ *   has no values).  Scratch: laplex_attend_workspace(..., 1), mainly two
+ *   float32 states for every 64 rows and head, 8 dk dv n heads / 64 bytes with
+ *   dk and dv rounded up to 64 (dk above 64 to 128): 2.1 GB for 65536 rows of
+ *   16 heads of 128 x 128.  With less, take the sequences in several calls,
+ *   or a long one in parts: a part's final is the next one's h0, and a part's
+ *   dh0 is the dfinal of the one before it.
  *
  * laplex_attend_step -- one token for each of n requests, states updated in
  *   place: state float32 [pool][heads][dk][dv]; slots as for

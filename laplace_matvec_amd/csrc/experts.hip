@@ -10,9 +10,14 @@
 //
 // Three families of kernels:
 //   lx_experts_tile   16-bit values, tiles of 256 x 256, 128 x 128 or 64 x 64
-//     through LDS.  Bound by the matrix units' rate under the power limit:
-//     8 x 4096 rows, 4096 x 4096 bf16: 905 us, 1.21 PFLOP/s; a library product
-//     of all rows with one matrix 700 (steps of 1.6 us a tile against 1.3: it
+//     through LDS.  Bound by issue and waits within a step: the matrix units
+//     are busy for 56 % of the cycles (at 1.7 GHz, below the full clock), a
+//     third of the waves' time is waiting, and about one scalar instruction is
+//     issued for each matrix instruction.  8 x 4096 rows, 4096 x 4096 bf16:
+//     905 to 945 us, 1.16 to 1.21 PFLOP/s; a library product
+//     of all rows with one matrix 700 (steps of 1.6 us a tile against 1.3: 85 %
+//     busy at 1.5 GHz, a third of the scalar and two thirds of the vector
+//     instructions; it
 //     reads a third less LDS with four waves of 128 x 128, which lost here, 890
 //     against 850 in one matrix, and waits less).  Also tried for one matrix
 //     of 32768 x 4096 x 4096: matrix instructions of 32 x 32 x 16 980, four
@@ -725,6 +730,12 @@ hipError_t tiles_go(const ExpertsArgs& a, hipStream_t s)
     // Little 27.7, Middle 29.6, Large 51.7; 400: 55, 37, 57; 1024: 115, 75, 66;
     // rows 8: few 18.7, Little 21.6.  An expert with more than 16 rows is read
     // twice by `few`: 512 rows unevenly on 128 experts 151, Little 143.
+    // The host knows the average only.  Where a router sends all rows to one
+    // expert, the shape is that of the even case, and the call takes longer than
+    // the shape for one expert would, but no longer than the even case: 128
+    // experts of 2048 x 2048, 256 rows 72 (one expert 16, even 193), 4096 rows
+    // 64 (39, 214), 16384 rows 152 (127, 255); the farthest, two rows an expert
+    // on average in 4096 experts of 512 x 1024, 479 (18, 1090).
     const int64_t each = a.n / a.experts;
     if (!a.transpose && (each <= 2 || (each <= 8 && tiles_of<Little>(a) < 512))) return few_go<T>(a, s);
     if (each > 160 && tiles_of<Large>(a) >= 224) return tile_go<T, Large>(a, dma, s);

@@ -15,9 +15,18 @@ constexpr int kC = kAttendChunk;  // rows of a chunk: one per lane
 // scores).  What is made here goes into bfloat16 products rounded, in as many
 // terms as its results need:
 //     scores, states for y         1   they reach bfloat16 results only, and
-//                                      add less to them than their own rounding
-//     states for gradients         2   dg is float32: off by 2e-6 of itself
-//                                      (three planes do not fit in LDS)
+//                                      add no more to them than their own
+//                                      rounding: y is off by 0.0024 where that
+//                                      is 0.0017.  States in two terms give
+//                                      0.0019, scores too 0.0017; their planes
+//                                      take the LDS of a second workgroup on a
+//                                      CU: 65536 rows of 16 heads of 128 x 128
+//                                      477 us against 714 (624 in blocks of 64
+//                                      columns), packed training 1431 against
+//                                      1460
+//     states for gradients         2   dg is float32: off by 2e-6 of the terms
+//                                      of its chunk, 1e-3 with one (three
+//                                      planes do not fit in LDS)
 //     rows times decays (states)   3   final states and dh0 are float32: off by
 //                                      2e-7 of themselves, 1.6e-6 with two terms
 template <class T>

@@ -802,7 +802,8 @@ def laplex_attend_step(q, k, v, g, state, slots=None, scale: float = 1.0, stream
     """One token for each request, in place on state float32 [pool, heads, dk,
     dv]: S = exp(g_i) S + k_i v_i^T for S = state[slots[i]]; returns y [n,
     heads, dv] = scale S^T q_i.  slots int32 [n] (None: request i has state i);
-    a slot outside the pool has no state and gives 0."""
+    a slot outside the pool has no state and gives 0.  No two requests may
+    share a slot."""
     if not isinstance(g, torch.Tensor) or g.dim() != 2:
         raise TypeError("g must be a CUDA tensor [n, heads]")
     n, _, sizes, (ldq, ldk, ldv, ldg) = _attend_parts(q, k, v, g, None, None)

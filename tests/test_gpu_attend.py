@@ -390,3 +390,27 @@ def test_digits_of_float32_results_of_bfloat16_rows(gpu):
     off = {name: float((got[name].cpu().double() - want[name][0]).norm() / want[name][0].norm()) for name in got}
     print(off)
     assert off["final"] < 5e-7 and off["dh0"] < 5e-7 and off["dg"] < 5e-6, off
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_sequence_in_parts(gpu, dtype):
+    """A long sequence part by part, as where scratch is short: last states are the next part's first ones, and the
+    gradient of a part's first states is that of the part before's last ones.  Three parts have 7 chunks instead of 5,
+    three roundings each: 6 of the 270 and more that the bounds count, 3 in 100."""
+    t = make(gpu, dtype, 300, 2, 24, 24)
+    want = ref.attend(t["q"], t["k"], t["v"], t["g"], [0, 300], t["h0"], 0.2, t["dy"], t["dfinal"])
+    parts, first, passed = [slice(0, 130), slice(130, 131), slice(131, 300)], t["h0"], []
+    for at in parts:
+        r = lx.laplex_attend(*(t[x][at] for x in "qkvg"), h0=first, scale=0.2, final=True, keep=True)
+        passed.append((at, first, r))
+        first = r.final
+    assert_within(first, want["final"][0], 1.03 * want["final"][1])
+    got, last = {"y": torch.cat([r.y for _, _, r in passed])}, t["dfinal"]
+    grads = []
+    for at, h0, r in reversed(passed):
+        d = lx.laplex_attend_backward(*(t[x][at] for x in "qkvg"), t["dy"][at], r.states, h0=h0, scale=0.2, dfinal=last)
+        last = d["dh0"]
+        grads.insert(0, d)
+    got.update({name: torch.cat([d[name] for d in grads]) for name in ("dq", "dk", "dv", "dg")}, dh0=last)
+    for name, x in got.items():
+        assert_within(x, want[name][0], 1.03 * want[name][1])
