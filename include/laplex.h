@@ -445,10 +445,10 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  *   ws        device scratch of laplex_attend_workspace(..., 0) bytes, 16-byte
  *             aligned.
  * Float32 and float16 rows are multiplied in float32.  With bfloat16 rows,
- * what enters a product is bfloat16 too: scores, states for y and gradients
- * of scores rounded once, states for gradients in two terms (16 bits), rows
- * times decays for the states in three (24); the states themselves stay
- * float32.  y is then off by up to sqrt(2) times what rounding it costs
+ * what enters a product is bfloat16 too: scores and states for y and states
+ * for gradients in two terms (16 bits), scores and their gradients in the
+ * backward pass rounded once, rows times decays for the states in three terms
+ * (24); the states themselves stay float32.  y is off by its own rounding
  * (relative norms), final and dh0 by 2e-7, dg by 2e-6 where decays are weak:
  * dg is a difference of sums over its chunk of 64 rows, and off by that part
  * of the sum of their absolute terms, also where a strong decay leaves little

@@ -43,9 +43,16 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
     constexpr int TB = DV / 16;
     constexpr int PK = DK + kPad<E>, PV = DV + kPad<E>;
     constexpr int TA = DK / 64;  // 16-row tiles of the state per wave
-    __shared__ alignas(16) E s_k[kC * PK];
-    __shared__ alignas(16) E s_v[kC * PV];
-    __shared__ alignas(16) E s_s[MODE == kOut ? DV * PK : 1];
+    // Terms of scores and of the state in y.  Two planes of a state of 128 x
+    // 128 leave no room for a second workgroup on the CU: the second plane then
+    // shares its place with keys and values, which come after it.
+    constexpr int NY = sizeof(E) == 2 ? 2 : 1;
+    constexpr bool kShare = MODE == kOut && NY == 2 && DK == 128 && DV == 128;
+    __shared__ alignas(16) E s_kv[kC * PK + kC * PV];
+    __shared__ alignas(16) E s_s[MODE == kOut ? (kShare ? 1 : NY) * DV * PK : 1];  // the state, transposed
+    static_assert(!kShare || DV * PK <= kC * PK + kC * PV, "room for a plane");
+    E *const s_k = s_kv, *const s_v = s_kv + kC * PK;
+    auto plane = [&](int m) { return kShare && m ? s_kv : s_s + m * (DV * PK); };
     __shared__ alignas(16) Decays s_d;
     __shared__ alignas(16) float s_f[kC];
     __shared__ int s_odd[4];
@@ -117,23 +124,27 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
     RowTile<T, DV, WHOLE> tv;
     Pack<T, 8> tq[DK / 32];
     TG tg = (TG)0.f;
+    auto fetch_q = [&](int ci) {
+        const int c = REV ? chunks - 1 - ci : ci;
+        const int64_t row = t.row + (int64_t)c * kC;
+        const int rows = t.rows - c * kC < kC ? t.rows - c * kC : kC;
+        const int i = 16 * wave + l16;
+#pragma unroll
+        for (int kk = 0; kk < DK / 32; ++kk)
+            if (WHOLE) {
+                const int at = i < rows ? i : rows - 1, col = 32 * kk + 2 * g4;
+                tq[kk] = load8_whole(qp + (row + at) * A.ldq + (col < kcols ? col : kcols - 8));
+            } else {
+                tq[kk] = load8(qp + (row + i) * A.ldq + 32 * kk + 2 * g4, i < rows ? kcols - 32 * kk - 2 * g4 : 0);
+            }
+    };
     auto fetch = [&](int ci) {
         const int c = REV ? chunks - 1 - ci : ci;
         const int64_t row = t.row + (int64_t)c * kC;
         const int rows = t.rows - c * kC < kC ? t.rows - c * kC : kC;
         tk.load(kp + row * ldk, ldk, rows, kcols);
         tv.load(vp + row * ldv, ldv, rows, vcols);
-        if (MODE == kOut) {
-            const int i = 16 * wave + l16;
-#pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk)
-                if (WHOLE) {
-                    const int at = i < rows ? i : rows - 1, col = 32 * kk + 2 * g4;
-                    tq[kk] = load8_whole(qp + (row + at) * A.ldq + (col < kcols ? col : kcols - 8));
-                } else {
-                    tq[kk] = load8(qp + (row + i) * A.ldq + 32 * kk + 2 * g4, i < rows ? kcols - 32 * kk - 2 * g4 : 0);
-                }
-        }
+        if (MODE == kOut && (!kShare || ci == 0)) fetch_q(ci);
         if (wave == 0) tg = gp[(row + (lane < rows ? lane : rows - 1)) * A.ldg];
     };
     fetch(0);
@@ -142,17 +153,33 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
         const int c = REV ? chunks - 1 - ci : ci;
         const int64_t row = t.row + (int64_t)c * kC;
         const int rows = t.rows - c * kC < kC ? t.rows - c * kC : kC;
+        // Places worked out anew for each chunk where registers are short.
+        int here = lane;
+        if (kShare) asm volatile("" : "+v"(here));
+        const int g4 = 4 * (here >> 4), l16 = here & 15;
         if (wave == 0) {
             s_d.make(lane < rows ? (float)tg : 0.f);
             s_f[lane] = REV ? s_d.into[lane] * A.scale : s_d.out[lane];
         }
-        tk.put(s_k, rows, kcols);
-        tv.put(s_v, rows, vcols);
-        {
+        auto put_rows = [&] {
+            tk.put(s_k, rows, kcols);
+            tv.put(s_v, rows, vcols);
             const bool odd = __any(tv.odd());
             if (lane == 0) s_odd[wave] = odd;
-        }
+        };
+        if (!kShare) put_rows();
         Frag<E> fq[DK / 32];
+        // what the wave's rows see of columns 16 b .. of the state
+        auto see = [&](int b) {
+            f32x4 o = {};
+#pragma unroll
+            for (int m = 0; m < NY; ++m)
+#pragma unroll
+                for (int kk = 0; kk < DK / 32; ++kk)
+                    o = mma(fq[kk], frag_along(plane(m) + (16 * b + l16) * PK + 32 * kk + 2 * g4), o);
+            return o;
+        };
+        f32x4 seen[kShare ? TB : 1];
         if (MODE == kOut) {
 #pragma unroll
             for (int kk = 0; kk < DK / 32; ++kk) fq[kk] = to_frag<E>(tq[kk]);
@@ -161,11 +188,28 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
             for (int a = 0; a < TA; ++a)
 #pragma unroll
                 for (int b = 0; b < TB; ++b) {
-                    V4 w;
+                    V4 w[NY];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) w[r] = (E)acc[a][b][r];
-                    *reinterpret_cast<V4*>(&s_s[(16 * b + l16) * PK + 16 * (wave * TA + a) + g4]) = w;
+                    for (int r = 0; r < 4; ++r) {
+                        E e[NY];
+                        split<E, NY>(acc[a][b][r], e);
+#pragma unroll
+                        for (int m = 0; m < NY; ++m) w[m][r] = e[m];
+                    }
+#pragma unroll
+                    for (int m = 0; m < NY; ++m)
+                        *reinterpret_cast<V4*>(&plane(m)[(16 * b + l16) * PK + 16 * (wave * TA + a) + g4]) = w[m];
                 }
+        }
+        if constexpr (kShare) {
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                seen[b] = see(b);
+                if (b & 1) __builtin_amdgcn_sched_barrier(0);
+            }
+            __syncthreads();
+            put_rows();
         }
         __syncthreads();
         // 0 times inf or NaN is not 0: rows that do not see such a value of v
@@ -204,7 +248,7 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
             const int i = 16 * wave + l16;
             const float hi_i = s_d.hi[i], lo_i = s_d.lo[i];
             const int last_i = s_d.last[i];
-            Frag<E> fp[2];
+            Frag<E> fp[NY][2];
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
                 f32x4 p = {};
@@ -222,21 +266,31 @@ __global__ __launch_bounds__(kAttendThreads, MODE == kOut && DK == 128 && sizeof
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) fp[jt >> 1].v[4 * (jt & 1) + r] = (E)p[r];
+                for (int r = 0; r < 4; ++r) {
+                    E e[NY];
+                    split<E, NY>(p[r], e);
+#pragma unroll
+                    for (int m = 0; m < NY; ++m) fp[m][jt >> 1].v[4 * (jt & 1) + r] = e[m];
+                }
+                if (kShare) __builtin_amdgcn_sched_barrier(0);  // not more fragments at a time than registers
             }
+            if (kShare && ci + 1 < chunks) fetch_q(ci + 1);  // in place of these, which are done with
             const f32x4 into = *reinterpret_cast<const f32x4*>(&s_d.into[16 * wave + g4]);
             T* yp = (T*)A.y + (row + 16 * wave + g4) * A.ldy + h * A.dv + v0 + l16;
 #pragma unroll
             for (int b = 0; b < TB; ++b) {
-                f32x4 o = {};
-#pragma unroll
-                for (int kk = 0; kk < DK / 32; ++kk)
-                    o = mma(fq[kk], frag_along(s_s + (16 * b + l16) * PK + 32 * kk + 2 * g4), o);
+                f32x4 o;
+                if constexpr (kShare) o = seen[b];
+                else o = see(b);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[r] = into[r] == 0.f ? 0.f : o[r] * (into[r] * A.scale);
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    if (2 * s <= wave) o = mma(fp[s], frag_across(s_v + 32 * s * PV + 16 * b, PV), o);
+                    if (2 * s <= wave) {
+                        const Frag<E> f = frag_across(s_v + 32 * s * PV + 16 * b, PV);
+#pragma unroll
+                        for (int m = 0; m < NY; ++m) o = mma(fp[m][s], f, o);
+                    }
                 const int col = 16 * b + l16;
                 if (odd) {
 #pragma unroll

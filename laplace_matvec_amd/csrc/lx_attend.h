@@ -14,16 +14,11 @@ constexpr int kC = kAttendChunk;  // rows of a chunk: one per lane
 // other types as float32 (float16's range is too small for states and
 // scores).  What is made here goes into bfloat16 products rounded, in as many
 // terms as its results need:
-//     scores, states for y         1   they reach bfloat16 results only, and
-//                                      add no more to them than their own
-//                                      rounding: y is off by 0.0024 where that
-//                                      is 0.0017.  States in two terms give
-//                                      0.0019, scores too 0.0017; their planes
-//                                      take the LDS of a second workgroup on a
-//                                      CU: 65536 rows of 16 heads of 128 x 128
-//                                      477 us against 714 (624 in blocks of 64
-//                                      columns), packed training 1431 against
-//                                      1460
+//     scores, states for y         2   y is off by its own rounding, 0.0017; by
+//                                      0.0024 with one term.  65536 rows of 16
+//                                      heads of 128 x 128 518 us against 471,
+//                                      packed training 1459 against 1425
+//     scores for gradients         1   they reach bfloat16 results only
 //     states for gradients         2   dg is float32: off by 2e-6 of the terms
 //                                      of its chunk, 1e-3 with one (three
 //                                      planes do not fit in LDS)
