@@ -445,14 +445,13 @@ laplex_status laplex_experts_backward(int64_t n, int64_t n_experts, const int32_
  *   ws        device scratch of laplex_attend_workspace(..., 0) bytes, 16-byte
  *             aligned.
  * Float32 and float16 rows are multiplied in float32.  With bfloat16 rows,
- * what enters a product is bfloat16 too: scores and states for y and states
- * for gradients in two terms (16 bits), scores and their gradients in the
- * backward pass rounded once, rows times decays for the states in three terms
- * (24); the states themselves stay float32.  y is off by its own rounding
- * (relative norms), final and dh0 by 2e-7, dg by 2e-6 where decays are weak:
- * dg is a difference of sums over its chunk of 64 rows, and off by that part
- * of the sum of their absolute terms, also where a strong decay leaves little
- * of dg itself.
+ * what enters a product is bfloat16 too, in as many terms as the result has
+ * digits: scores, their gradients and states for y two (16 bits), states for
+ * gradients and rows times decays three (24); the states themselves stay
+ * float32.  So 16-bit results are off by their own rounding, float32 ones
+ * (final, dh0, dg) by a few 1e-7 of the terms that they sum.  dg is a
+ * difference of sums over its chunk of 64 rows, and off by that part of the
+ * sum of their absolute terms, also where a strong decay leaves little of dg.
  * A row that holds inf or NaN (a decay of that kind in float32 too) reaches
  * its own and later rows of its heads and sequence, until one decay after it,
  * or the product of all decays of a later chunk of 64 rows (counted from the

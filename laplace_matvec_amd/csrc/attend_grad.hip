@@ -22,15 +22,17 @@
 // share unequally, states of several blocks) each writes a plane and
 // lx_attend_sum adds the planes in their order.
 //
-// 32768 rows, 32 heads of 128 x 64 on 8 query and key heads, bf16: 640 us for
+// 32768 rows, 32 heads of 128 x 64 on 8 query and key heads, bf16: 760 us for
 // 1.5 GB (S and S+ 1.1 of them).  Bound by latency: half of the waves' time is
-// waiting, at one workgroup of eight waves a CU (144 KB of LDS) and three
+// waiting, at one workgroup of eight waves a CU (157 KB of LDS) and four
 // barriers a head; rows padded so that no two lines of a transposing read
 // share banks changed nothing.  One workgroup of four waves doing both sides in turn,
 // loads where they are used: 1630; addresses worked out per value instead of
-// per head 1211 (of eight waves); kept across heads, which spills, 760.  With
-// 16-bit gates two registers spill, at no cost (the whole pass 1428 us, 1460
-// with float32 gates).
+// per head 1211 (of eight waves); kept across heads, which spills, 760 (these
+// with states in two terms, scores in one and three barriers: 640).  Scores
+// go where S was, so they wait in registers until all waves are done with it;
+// written at once behind a barrier of their own the whole pass took 1603 us,
+// so 1567.
 #include "lx_attend.h"
 
 namespace lx {
@@ -123,19 +125,22 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
 {
     typedef typename Compute<T>::E E;
     typedef E V4 __attribute__((ext_vector_type(4)));
-    constexpr int N = Compute<T>::kTerms;
+    constexpr int N = Compute<T>::kTerms, NP = Compute<T>::kScoreTerms;
+    constexpr int NS2 = N < 2 ? N : 2;  // of S+ for dv, which is rounded to T
     constexpr int PK = DK + kPad<E>, PV = DV + kPad<E>, PC = kC + kPad<E>;
     constexpr int NS = DK * DV / 4 / kGradThreads;  // groups of four state values a thread
     __shared__ alignas(16) E s_q[kC * PK];
     __shared__ alignas(16) E s_k[kC * PK];
     __shared__ alignas(16) E s_v[kC * PV];
     __shared__ alignas(16) E s_do[kC * PV];
-    __shared__ alignas(16) E s_s[N * DV * PK];  // S, transposed
+    // S, transposed; once all waves have used it, P and E in its place
+    constexpr int kStates = N * DV * PK, kScores = 2 * NP * kC * PC;
+    __shared__ alignas(16) E s_s[kStates > kScores ? kStates : kScores];
     __shared__ alignas(16) E s_t[N * DV * PK];  // S+, transposed
-    __shared__ alignas(16) E s_p[kC * PC];
-    __shared__ alignas(16) E s_e[kC * PC];
+    E *const s_p = s_s, *const s_e = s_s + NP * kC * PC;
     __shared__ alignas(16) Decays s_d;
-    __shared__ float s_row[kC], s_col[4][kC], s_b[kC], s_z[2][8];
+    __shared__ alignas(16) float s_row[kC], s_col[4][kC], s_a[kC], s_b[kC];
+    __shared__ float s_z[2][8];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int side = wave >> 2, w16 = 16 * (wave & 3);
@@ -219,6 +224,9 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         if (!is_last) state_in(tt, slot_t, hl, v0);
         if (wave == 0) tg = gp[hl];
     };
+    auto half_of = [](const Frag<E>& f, int h) {
+        return h ? __builtin_shufflevector(f.v, f.v, 4, 5, 6, 7) : __builtin_shufflevector(f.v, f.v, 0, 1, 2, 3);
+    };
     auto put_state = [&](const f32x4& x, E* s, int row, int col) {
         V4 w[N];
 #pragma unroll
@@ -277,10 +285,10 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         __syncthreads();
         if (more) fetch(ends_head ? hl + 1 : hl, next_hv, ends_head ? 0 : vb + 1);
 
-        Frag<E> fe[2];
+        Frag<E> fp[NP][2], fe[NP][2];
         f32x4 dv[DV / 16];
+        f32x4 u = {};
         if (side == 0) {
-            f32x4 u = {};
             const f32x4 into = *reinterpret_cast<const f32x4*>(&s_d.into[w16 + g4]);
 #pragma unroll
             for (int c = 0; c < DK / 16; ++c) {
@@ -300,13 +308,15 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                 }
                 if ((c & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // not more fragments at a time than registers
             }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[r] = sum16(u[r]);
+            if (l16 == 0) *reinterpret_cast<f32x4*>(&s_a[w16 + g4]) = u;
             const float hi_i = s_d.hi[i], lo_i = s_d.lo[i];
             const int last_i = s_d.last[i];
             float row_sum = 0.f;
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
-                V4 p4 = {}, e4 = {};
-                f32x4 w = {};
+                f32x4 w = {}, p = {}, e = {};
                 if (16 * jt <= w16) {
                     // scores and dy . v, transposed: column i, rows j = 16 jt + g4 + r.
                     // Scores are made again for every head that shares them:
@@ -327,19 +337,23 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                         const int j = 16 * jt + g4 + r;
                         const bool on = j <= i && j >= last_i;
                         const float d = A.scale * s_d.between(hi_i, lo_i, hi[r], lo[r]);
-                        const float p = on ? score[r] * d : 0.f;
-                        p4[r] = (E)p;
-                        e4[r] = (E)(on ? x[r] * d : 0.f);
-                        w[r] = on && j < i ? p * x[r] : 0.f;
+                        p[r] = on ? score[r] * d : 0.f;
+                        e[r] = on ? x[r] * d : 0.f;
+                        w[r] = on && j < i ? p[r] * x[r] : 0.f;
                         row_sum += w[r];
                     }
                 }
-                *reinterpret_cast<V4*>(&s_p[i * PC + 16 * jt + g4]) = p4;
-                *reinterpret_cast<V4*>(&s_e[i * PC + 16 * jt + g4]) = e4;
                 f32x4 sums;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    fe[jt >> 1].v[4 * (jt & 1) + r] = e4[r];
+                    E pt[NP], et[NP];
+                    split<E, NP>(p[r], pt);
+                    split<E, NP>(e[r], et);
+#pragma unroll
+                    for (int m = 0; m < NP; ++m) {
+                        fp[m][jt >> 1].v[4 * (jt & 1) + r] = pt[m];
+                        fe[m][jt >> 1].v[4 * (jt & 1) + r] = et[m];
+                    }
                     sums[r] = sum16(w[r]);
                 }
                 if (l16 == 0) *reinterpret_cast<f32x4*>(&s_col[wave][16 * jt + g4]) = sums;
@@ -348,19 +362,8 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
             row_sum += __shfl_xor(row_sum, 16);
             row_sum += __shfl_xor(row_sum, 32);
             if (g4 == 0) s_row[i] = row_sum;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) u[r] = sum16(u[r]);
-            // The wave's own rows, no other wave's; but other lanes stored them,
-            // which only a fence keeps before these reads.
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            if (l16 == 0)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) s_row[w16 + g4 + r] += u[r];
         } else {
             const f32x4 out = *reinterpret_cast<const f32x4*>(&s_d.out[w16 + g4]);
-            f32x4 u = {};
 #pragma unroll
             for (int c = 0; c < DK / 16; ++c) {
                 f32x4 x = {};
@@ -390,7 +393,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                     for (int kk = 0; kk < DK / 32; ++kk) {
                         const Frag<E> f = frag_along(s_k + i * PK + 32 * kk + 2 * g4);
 #pragma unroll
-                        for (int m = 0; m < N; ++m)
+                        for (int m = 0; m < NS2; ++m)
                             x = mma(f, frag_along(s_t + (m * DV + 16 * b + l16) * PK + 32 * kk + 2 * g4), x);
                     }
 #pragma unroll
@@ -399,23 +402,42 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
                 }
             }
         }
+        __syncthreads();  // S has been used
+        if (side == 0) {
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) {
+                    const int at = (m * kC + i) * PC + 16 * jt + g4;
+                    *reinterpret_cast<V4*>(&s_p[at]) = half_of(fp[m][jt >> 1], jt & 1);
+                    *reinterpret_cast<V4*>(&s_e[at]) = half_of(fe[m][jt >> 1], jt & 1);
+                }
+        }
         __syncthreads();
         if (side == 0) {
 #pragma unroll
             for (int c = 0; c < DK / 16; ++c) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    if (32 * s <= w16) acc[c] = mma(fe[s], frag_across(s_k + 32 * s * PK + 16 * c, PK), acc[c]);
+                    if (32 * s <= w16) {
+                        const Frag<E> f = frag_across(s_k + 32 * s * PK + 16 * c, PK);
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) acc[c] = mma(fe[m][s], f, acc[c]);
+                    }
                 if ((c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
             }
         } else {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (32 * s + 16 < w16) continue;
-                const Frag<E> f = frag_across(s_e + 32 * s * PC + w16, PC);
+                Frag<E> f[NP];
+#pragma unroll
+                for (int m = 0; m < NP; ++m) f[m] = frag_across(s_e + (m * kC + 32 * s) * PC + w16, PC);
 #pragma unroll
                 for (int c = 0; c < DK / 16; ++c) {
-                    acc[c] = mma(f, frag_across(s_q + 32 * s * PK + 16 * c, PK), acc[c]);
+                    const Frag<E> fq = frag_across(s_q + 32 * s * PK + 16 * c, PK);
+#pragma unroll
+                    for (int m = 0; m < NP; ++m) acc[c] = mma(f[m], fq, acc[c]);
                     if ((c & 3) == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -423,9 +445,15 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (32 * s + 16 < w16) continue;
-                    const Frag<E> f = frag_across(s_p + 32 * s * PC + w16, PC);
+                    Frag<E> f[NP];
 #pragma unroll
-                    for (int b = 0; b < DV / 16; ++b) dv[b] = mma(f, frag_across(s_do + 32 * s * PV + 16 * b, PV), dv[b]);
+                    for (int m = 0; m < NP; ++m) f[m] = frag_across(s_p + (m * kC + 32 * s) * PC + w16, PC);
+#pragma unroll
+                    for (int b = 0; b < DV / 16; ++b) {
+                        const Frag<E> fd = frag_across(s_do + 32 * s * PV + 16 * b, PV);
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) dv[b] = mma(f[m], fd, dv[b]);
+                    }
                 }
                 const Out<T> ov = out_rows<T>(A.dval, A.lddv, A.part_v, in_hv * A.nkb + kb, A.n, A.hv * A.dv, t.row,
                                               hv * A.dv + v0);
@@ -434,7 +462,7 @@ __global__ __launch_bounds__(kGradThreads) void lx_attend_grad(AttendArgs A)
         }
         __syncthreads();
         if (wave == 0) {
-            float from = s_row[lane] - ((s_col[0][lane] + s_col[1][lane]) + (s_col[2][lane] + s_col[3][lane]));
+            float from = (s_row[lane] + s_a[lane]) - ((s_col[0][lane] + s_col[1][lane]) + (s_col[2][lane] + s_col[3][lane]));
             float to = s_b[lane];
             const float own = to;
             to = scan_up(to);

@@ -18,16 +18,19 @@ constexpr int kC = kAttendChunk;  // rows of a chunk: one per lane
 //                                      0.0024 with one term.  65536 rows of 16
 //                                      heads of 128 x 128 518 us against 471,
 //                                      packed training 1459 against 1425
-//     scores for gradients         1   they reach bfloat16 results only
-//     states for gradients         2   dg is float32: off by 2e-6 of the terms
-//                                      of its chunk, 1e-3 with one (three
-//                                      planes do not fit in LDS)
+//     scores and their gradients   2   dq, dk and dv likewise; 0.0019 with one
+//                                      term.  Packed training 1612 us against
+//                                      1561
+//     states for gradients         3   dg is float32: off by 1e-7 to 4e-7,
+//                                      which is what float32 products give;
+//                                      2.6e-6 with two terms.  1612 against
+//                                      1558
 //     rows times decays (states)   3   final states and dh0 are float32: off by
 //                                      2e-7 of themselves, 1.6e-6 with two terms
 template <class T>
-struct Compute { typedef float E; static constexpr int kTerms = 1; };
+struct Compute { typedef float E; static constexpr int kTerms = 1, kScoreTerms = 1; };
 template <>
-struct Compute<bf16_t> { typedef bf16_t E; static constexpr int kTerms = 2; };
+struct Compute<bf16_t> { typedef bf16_t E; static constexpr int kTerms = 3, kScoreTerms = 2; };
 
 // Values of padding at the end of an LDS row of E: 16 bytes.
 template <class E>

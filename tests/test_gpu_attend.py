@@ -429,3 +429,23 @@ def test_results_of_bfloat16_rows_are_rounded_once(gpu, gates, dk, dv, shared):
     exact = ref.attend(t["q"], t["k"], t["v"], t["g"], [0, 300], t["h0"], scale)["y"][0]
     own = (exact.bfloat16().double() - exact).norm()
     assert (y.double() - exact).norm() < 1.001 * own
+
+
+@pytest.mark.parametrize("gates", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv,shared", [(128, 128, (3, 3, 3)), (128, 64, (1, 1, 3)), (64, 128, (3, 3, 3)), (64, 64, (3, 3, 1)),
+                                          (40, 72, (3, 3, 3)), (101, 100, (3, 1, 3)), (200, 256, (1, 3, 3))])
+def test_gradients_of_bfloat16_rows_are_rounded_once(gpu, gates, dk, dv, shared):
+    """dq, dk and dv like y: scores and their gradients in two terms.  dg (float32 gates): states in three terms, to the
+    last digits of float32, sums of 64 pairs and of dk + dv products: below the 2.3e-6 / 2 that even one state in two
+    terms leaves."""
+    t = make(gpu, torch.bfloat16, 300, 3, dk, dv, shared, gates=gates, seed=dk)
+    scale = dk ** -0.5
+    got = passes(t, None, gpu, scale)
+    want = ref.attend(t["q"], t["k"], t["v"], t["g"], [0, 300], t["h0"], scale, t["dy"], t["dfinal"])
+    off = {name: float((got[name].cpu().double() - want[name][0]).norm()) for name in ALL}
+    print({name: x / float(want[name][0].norm()) for name, x in off.items()})
+    for name in ("dq", "dk", "dv") + (("dg",) if gates is torch.bfloat16 else ()):
+        exact = want[name][0]
+        assert off[name] < 1.001 * float((exact.bfloat16().double() - exact).norm()), name
+    if gates is torch.float32:
+        assert off["dg"] < 1.0e-6 * float(want["dg"][0].norm())
