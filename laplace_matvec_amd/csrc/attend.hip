@@ -16,15 +16,17 @@
 // A segment is as short as it takes to fill the card (attend_segment); with
 // one segment per sequence the first two are left out.
 //
-// 65536 rows of 16 heads of 128 x 128 bf16 in 470 us: kEnd 135 (keys and values
-// once, 4 TB/s), scan 16, kOut 318 (1.07 GB, 3.4 TB/s); a copy would take 212.
-// Bound by the latency of a chunk, 6 us with two workgroups a CU: vector
-// instructions (decays, rounding) about half of it, two barriers, matrix
-// products a quarter.  Loads of the next chunk are on their way meanwhile,
-// which only pays without branches (444 us against 624).  One block of 128
-// columns per workgroup shares keys and scores: 624 us against 827 with 64.
-// In the backward pass kStore leaves 16 KB to 64 KB a chunk and head, as many
-// bytes as the rows themselves or more: 165 us for 564 MB.
+// 65536 rows of 16 heads of 128 x 128 bf16 in 518 us; under the profiler, at
+// the least, kEnd 156 (keys and values once, 3.4 TB/s), scan 15, kOut 371 (1.07
+// GB, 2.9 TB/s); a copy would take 212.  Bound by the latency of a chunk, 11.6
+// us in kOut with two workgroups a CU: a third of the waves' time is waiting
+// (four barriers), vector instructions (decays, terms) take 47 % of the SIMDs'
+// cycles, matrix products 25 %.  Loads of the next chunk are on their way
+// meanwhile, which only pays without branches (444 us against 624, with states
+// and scores for y in one term).  One block of 128 columns per workgroup shares
+// keys and scores: 518 us against 624 with 64.  In the backward pass kStore
+// leaves 16 KB to 64 KB a chunk and head, as many bytes as the rows themselves
+// or more: 165 to 185 us for 564 MB.
 #include "lx_attend.h"
 
 namespace lx {
@@ -454,7 +456,7 @@ __global__ __launch_bounds__(256) void lx_attend_sum(const float* part, int plan
 // One token for each request.  A thread has V neighbouring columns of every
 // 256 / (columns / V) -th row of a head's state, which is read and written
 // once: 256 requests of 16 heads of 128 x 128, 537 MB, in 106 us, 5.1 TB/s.  A
-// few requests take the launch (3 of 8 heads of 64 x 64: 5.6 us of kernel).
+// few requests take the launch (3 of 8 heads of 64 x 64: 5.4 us of kernel).
 template <class T, class TG, int V>
 __global__ __launch_bounds__(256) void lx_attend_step(AttendStepArgs A)
 {

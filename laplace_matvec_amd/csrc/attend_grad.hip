@@ -22,7 +22,7 @@
 // share unequally, states of several blocks) each writes a plane and
 // lx_attend_sum adds the planes in their order.
 //
-// 32768 rows, 32 heads of 128 x 64 on 8 query and key heads, bf16: 760 us for
+// 32768 rows, 32 heads of 128 x 64 on 8 query and key heads, bf16: 750 us for
 // 1.5 GB (S and S+ 1.1 of them).  Bound by latency: half of the waves' time is
 // waiting, at one workgroup of eight waves a CU (157 KB of LDS) and four
 // barriers a head; rows padded so that no two lines of a transposing read
